@@ -282,6 +282,64 @@ int igc_sparse_conv_backward(const igc_grid* grid, const int32_t* d_map, const v
                              int32_t cin, const void* d_w, int32_t cout, const void* d_dout, void* d_dfeats,
                              float* d_dw, int32_t path, igc_stream stream);
 
+/* Channels of a row that share one scale of an 8-bit activation checkpoint. */
+#define IGC_Q8_GROUP 64
+
+/* 8-bit activation checkpoint of n rows of c channels (features kept between the forward and the
+ * backward pass at about half the bytes of bf16). Groups of IGC_Q8_GROUP consecutive channels of a
+ * row (the last may be shorter) share a scale; with a = the group's largest magnitude, every step
+ * rounded to fp32,
+ *     d_codes[r, ch] = rint(x * (127 * (1 / a))), d_scales[r, ch / 64] = a * (1 / 127).
+ * Groups with a < 2^-100 store scale 0 and zeros; a group that holds an infinity or a NaN stores a
+ * NaN scale, so all of it reads back as NaN. d_x [n, c] of type `dtype`, d_codes int8 [n, c],
+ * d_scales float [n, ceil(c / 64)]. c is 1 to 4096 (IGC_ERR_UNSUPPORTED beyond). */
+int igc_checkpoint_pack(const void* d_x, int64_t n, int32_t c, int32_t dtype, int8_t* d_codes, float* d_scales,
+                        igc_stream stream);
+
+/* d_x[r, ch] = d_codes[r, ch] * d_scales[r, ch / 64], rounded to `dtype`. */
+int igc_checkpoint_unpack(const int8_t* d_codes, const float* d_scales, int64_t n, int32_t c, int32_t dtype,
+                          void* d_x, igc_stream stream);
+
+/* igc_sparse_conv_backward with the forward input held as an 8-bit checkpoint (d_codes, d_scales of
+ * igc_checkpoint_pack, or codes in its format): d_dw is the weight gradient for the values
+ * igc_checkpoint_unpack gives in `dtype`. The bf16 matrix-core kernel reads the checkpoint itself;
+ * other shapes restore the values into a temporary first. d_dfeats does not depend on them. */
+int igc_sparse_conv_backward_q8(const igc_grid* grid, const int32_t* d_map, const int8_t* d_codes,
+                                const float* d_scales, int32_t dtype, int32_t cin, const void* d_w, int32_t cout,
+                                const void* d_dout, void* d_dfeats, float* d_dw, int32_t path, igc_stream stream);
+
+/* Layer norm over the c channels (1 to 4096) of each of n rows:
+ *     mean = sum(x) / c, rstd = 1 / sqrt(sum((x - mean)^2) / c + eps),
+ *     d_y = (x - mean) * rstd * d_w + d_b
+ * d_x and d_y [n, c] of type `dtype`; d_w and d_b [c] of type `wdtype` (IGC_F32 or `dtype`; NULL: ones,
+ * zeros); d_mean and d_rstd float [n]. Sums and statistics are fp32. d_y must not alias d_x. */
+int igc_layer_norm(const void* d_x, int64_t n, int32_t c, int32_t dtype, const void* d_w, const void* d_b,
+                   int32_t wdtype, float eps, void* d_y, float* d_mean, float* d_rstd, igc_stream stream);
+
+/* igc_layer_norm that also writes an 8-bit checkpoint of the normalised rows (x - mean) * rstd, which
+ * with d_rstd is all its backward pass reads: x itself need not be kept. */
+int igc_layer_norm_q8(const void* d_x, int64_t n, int32_t c, int32_t dtype, const void* d_w, const void* d_b,
+                      int32_t wdtype, float eps, void* d_y, int8_t* d_codes, float* d_scales, float* d_rstd,
+                      igc_stream stream);
+
+/* Bytes of d_ws that the backward passes below need where d_dw is given (host only). */
+int igc_layer_norm_workspace(int64_t n, int32_t c, size_t* bytes);
+
+/* Gradients of igc_layer_norm for d_dy = dL/dY: with g = dy * w and xhat = (x - mean) * rstd,
+ *     d_dx = rstd * (g - mean(g) - xhat * mean(g * xhat))    (type `dtype`)
+ *     d_dw = sum over rows of dy * xhat, d_db = sum over rows of dy   (float [c]; NULL skips both)
+ * The sums over rows are fp32 within a workgroup and fp64 across workgroups in a fixed order, so
+ * reruns are bit-identical. d_ws: device memory of at least igc_layer_norm_workspace bytes
+ * (IGC_ERR_CAPACITY otherwise; not read where d_dw is NULL). d_dx must not alias d_dy or d_x. */
+int igc_layer_norm_backward(const void* d_dy, const void* d_x, const float* d_mean, const float* d_rstd, int64_t n,
+                            int32_t c, int32_t dtype, const void* d_w, int32_t wdtype, void* d_dx, float* d_dw,
+                            float* d_db, void* d_ws, size_t ws_bytes, igc_stream stream);
+
+/* The same from igc_layer_norm_q8's checkpoint: xhat = code * scale in fp32. */
+int igc_layer_norm_q8_backward(const void* d_dy, const int8_t* d_codes, const float* d_scales, const float* d_rstd,
+                               int64_t n, int32_t c, int32_t dtype, const void* d_w, int32_t wdtype, void* d_dx,
+                               float* d_dw, float* d_db, void* d_ws, size_t ws_bytes, igc_stream stream);
+
 /* Output grid of a 3x3x3 convolution with per-axis stride h_stride[0..2] (host, each 1, 2 or 3)
  * over `in` (the grid-to-grid ops ConvGrid and ConvTransposeGrid in the op table of the "ONNX
  * Runtime support for fVDB operations" proposal; the pages name the ops without a formula, so

@@ -12,37 +12,21 @@ import numpy as np
 import torch
 
 from . import _lib
+from ._args import BF16, F32, _device_tensor, _dtype_code, _ptr, _stream
+from ._block import (Checkpoint8, checkpoint_pack, checkpoint_unpack, layer_norm, layer_norm_backward,
+                     layer_norm_checkpoint, layer_norm_checkpoint_backward)
 from ._lib import IgcError
 
 __all__ = [
     "Grid", "grid_build", "kernel_map", "sparse_conv", "sparse_conv_backward", "conv_grid", "conv_grid_chain", "conv_map",
     "sparse_conv_between", "standard_offsets", "release_memory", "tuning_load", "IgcError",
+    "Checkpoint8", "checkpoint_pack", "checkpoint_unpack", "layer_norm", "layer_norm_backward", "layer_norm_checkpoint",
+    "layer_norm_checkpoint_backward",
     "PATH_AUTO", "PATH_LEAF", "PATH_GGS", "PATH_GATHER",
 ]
 
-F32, BF16 = 0, 1
 PATH_AUTO, PATH_LEAF, PATH_GGS, PATH_MIXED, PATH_GATHER = 0, 1, 2, 3, 4
 _PATHS = {"auto": PATH_AUTO, "leaf": PATH_LEAF, "ggs": PATH_GGS, "mixed": PATH_MIXED, "gather": PATH_GATHER}
-
-
-def _stream(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p | None:
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
-
-
-def _device_tensor(t: torch.Tensor, name: str, dtype: torch.dtype, cols: int | None = None) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if cols is not None and (t.dim() != 2 or t.shape[1] != cols):
-        raise ValueError(f"{name} must have shape [n, {cols}], got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
 
 
 def standard_offsets() -> np.ndarray:
@@ -154,14 +138,6 @@ class Grid:
         return {PATH_LEAF: "leaf", PATH_GGS: "ggs", PATH_GATHER: "gather"}[p.value]
 
 
-def _dtype_code(dtype: torch.dtype) -> int:
-    if dtype == torch.float32:
-        return F32
-    if dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"unsupported dtype {dtype}")
-
-
 def grid_build(ijk: torch.Tensor, memory: str = "torch") -> Grid:
     """IndexGrid from int32[n, 3] device coordinates (any order, duplicates allowed). Its device
     memory, and that of every later call on it, comes from PyTorch's caching allocator
@@ -217,14 +193,17 @@ def sparse_conv(grid: Grid, feats: torch.Tensor, weights: torch.Tensor, kmap: to
     return out
 
 
-def sparse_conv_backward(grid: Grid, feats: torch.Tensor, weights: torch.Tensor, dout: torch.Tensor,
+def sparse_conv_backward(grid: Grid, feats: torch.Tensor | Checkpoint8, weights: torch.Tensor, dout: torch.Tensor,
                          kmap: torch.Tensor, path: str = "auto", need_dfeats: bool = True,
                          need_dweights: bool = True):
     """Gradients of sparse_conv: (dfeats [N, cin] of feats' dtype or None, dweights [27, cin, cout]
-    float32 or None) for the output gradient dout [N, cout]."""
+    float32 or None) for the output gradient dout [N, cout]. feats may be an 8-bit checkpoint of the
+    features (checkpoint_pack): the weight gradient is then that of the values it stands for."""
     dt = feats.dtype
-    cin = feats.shape[1] if feats.dim() == 2 else -1
-    feats = _device_tensor(feats, "feats", dt, cin)
+    q8 = isinstance(feats, Checkpoint8)
+    cin = feats.shape[1] if len(feats.shape) == 2 else -1
+    if not q8:
+        feats = _device_tensor(feats, "feats", dt, cin)
     if weights.dim() != 3 or weights.shape[0] != 27 or weights.shape[1] != cin:
         raise ValueError(f"weights must have shape [27, {cin}, cout], got {tuple(weights.shape)}")
     weights = _device_tensor(weights, "weights", dt)
@@ -235,9 +214,14 @@ def sparse_conv_backward(grid: Grid, feats: torch.Tensor, weights: torch.Tensor,
         raise ValueError("feats, dout and kmap must cover the grid's voxels")
     dx = torch.empty((grid.n_voxels, cin), dtype=dt, device=grid.device) if need_dfeats else None
     dw = torch.empty((27, cin, cout), dtype=torch.float32, device=grid.device) if need_dweights else None
-    _lib.check(_lib.load().igc_sparse_conv_backward(grid.handle, _ptr(kmap), _ptr(feats), _dtype_code(dt), cin,
-                                                    _ptr(weights), cout, _ptr(dout), _ptr(dx), _ptr(dw),
-                                                    _PATHS[path], _stream(grid.device)))
+    if q8:
+        _lib.check(_lib.load().igc_sparse_conv_backward_q8(grid.handle, _ptr(kmap), _ptr(feats.codes), _ptr(feats.scales),
+                                                           _dtype_code(dt), cin, _ptr(weights), cout, _ptr(dout), _ptr(dx),
+                                                           _ptr(dw), _PATHS[path], _stream(grid.device)))
+    else:
+        _lib.check(_lib.load().igc_sparse_conv_backward(grid.handle, _ptr(kmap), _ptr(feats), _dtype_code(dt), cin,
+                                                        _ptr(weights), cout, _ptr(dout), _ptr(dx), _ptr(dw),
+                                                        _PATHS[path], _stream(grid.device)))
     return dx, dw
 
 

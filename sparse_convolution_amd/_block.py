@@ -1,0 +1,166 @@
+"""Operators between convolutions: layer norm and 8-bit activation checkpoints over voxel
+features [n, channels]."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._args import _device_tensor, _dtype_code, _ptr, _stream
+
+Q8_GROUP = 64  # channels of a row that share a checkpoint scale (IGC_Q8_GROUP)
+
+
+class Checkpoint8:
+    """Features held in 8 bits (igc_checkpoint_pack): codes int8 [n, c], scales float32
+    [n, ceil(c / 64)] and the type the values are restored in; value = code * scale of its group
+    of 64 channels."""
+
+    __slots__ = ("codes", "scales", "dtype")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.float32):
+        _dtype_code(dtype)
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+            raise ValueError("codes must have shape [n, c]")
+        _device_tensor(codes, "codes", torch.int8)
+        _device_tensor(scales, "scales", torch.float32, -(-codes.shape[1] // Q8_GROUP))
+        if scales.shape[0] != codes.shape[0] or scales.device != codes.device:
+            raise ValueError("codes and scales must have the same rows and device")
+        self.codes, self.scales, self.dtype = codes, scales, dtype
+
+    @property
+    def shape(self) -> torch.Size:
+        return self.codes.shape
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """lib.name(*args, stream) with `device` current."""
+    lib = _lib.load()
+    if device.index is None or device.index == torch.cuda.current_device():
+        _lib.check(getattr(lib, name)(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _lib.check(getattr(lib, name)(*args, _stream(device)))
+
+
+def _rows(x: torch.Tensor, name: str) -> torch.Tensor:
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name} must have shape [n, channels]")
+    _dtype_code(x.dtype)
+    return _device_tensor(x, name, x.dtype)
+
+
+def _same(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device) -> torch.Tensor:
+    _device_tensor(t, name, dtype)
+    if tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _params(weight, bias, c: int, x_dtype: torch.dtype, device: torch.device) -> int:
+    """Checks weight and bias and returns the type code they share."""
+    dt = x_dtype
+    for p in (weight, bias):
+        if p is not None:
+            dt = p.dtype
+            break
+    if dt not in (torch.float32, x_dtype):
+        raise TypeError(f"weight and bias must be float32 or {x_dtype}, got {dt}")
+    for p, name in ((weight, "weight"), (bias, "bias")):
+        if p is not None:
+            _same(p, name, dt, (c,), device)
+    return _dtype_code(dt)
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               eps: float = 1e-5):
+    """Layer norm of each row of x [n, c] (c up to 4096): (y of x's type, mean [n] float32,
+    rstd [n] float32). weight and bias [c] are float32 or of x's type (igc_layer_norm)."""
+    x = _rows(x, "x")
+    n, c = x.shape
+    wd = _params(weight, bias, c, x.dtype, x.device)
+    y = torch.empty_like(x)
+    stats = torch.empty((2, n), dtype=torch.float32, device=x.device)
+    mean, rstd = stats.unbind(0)
+    _call("igc_layer_norm", x.device, _ptr(x), n, c, _dtype_code(x.dtype), _ptr(weight), _ptr(bias), wd, eps, _ptr(y),
+          _ptr(mean), _ptr(rstd))
+    return y, mean, rstd
+
+
+def _backward(name, dy, source, rstd, weight, need_dweight, c):
+    n = dy.shape[0]
+    dev = dy.device
+    wd = _params(weight, None, c, dy.dtype, dev)
+    _same(rstd, "rstd", torch.float32, (n,), dev)
+    dx = torch.empty_like(dy)
+    dw = db = ws = None
+    nbytes = ctypes.c_size_t(0)
+    if need_dweight:
+        dw, db = torch.empty((2, c), dtype=torch.float32, device=dev).unbind(0)
+        _lib.check(_lib.load().igc_layer_norm_workspace(n, c, ctypes.byref(nbytes)))
+        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+    _call(name, dev, _ptr(dy), *source, _ptr(rstd), n, c, _dtype_code(dy.dtype), _ptr(weight), wd, _ptr(dx), _ptr(dw),
+          _ptr(db), _ptr(ws), nbytes)
+    return dx, dw, db
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: torch.Tensor | None = None, need_dweight: bool = True):
+    """Gradients of layer_norm for the output gradient dy: (dx of x's type, dweight [c] float32,
+    dbias [c] float32; the last two None without need_dweight) (igc_layer_norm_backward)."""
+    x = _rows(x, "x")
+    dy = _same(dy, "dy", x.dtype, x.shape, x.device)
+    mean = _same(mean, "mean", torch.float32, (x.shape[0],), x.device)
+    return _backward("igc_layer_norm_backward", dy, (_ptr(x), _ptr(mean)), rstd, weight, need_dweight, x.shape[1])
+
+
+def layer_norm_checkpoint(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                          eps: float = 1e-5):
+    """layer_norm that keeps what its backward pass needs in 8 bits: (y, Checkpoint8 of the normalised
+    rows before weight and bias, rstd [n] float32) (igc_layer_norm_q8)."""
+    x = _rows(x, "x")
+    n, c = x.shape
+    wd = _params(weight, bias, c, x.dtype, x.device)
+    y = torch.empty_like(x)
+    codes = torch.empty((n, c), dtype=torch.int8, device=x.device)
+    scales = torch.empty((n, -(-c // Q8_GROUP)), dtype=torch.float32, device=x.device)
+    rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+    _call("igc_layer_norm_q8", x.device, _ptr(x), n, c, _dtype_code(x.dtype), _ptr(weight), _ptr(bias), wd, eps, _ptr(y),
+          _ptr(codes), _ptr(scales), _ptr(rstd))
+    return y, Checkpoint8(codes, scales, x.dtype), rstd
+
+
+def layer_norm_checkpoint_backward(dy: torch.Tensor, ckpt: Checkpoint8, rstd: torch.Tensor,
+                                   weight: torch.Tensor | None = None, need_dweight: bool = True):
+    """layer_norm_backward from the checkpoint of layer_norm_checkpoint (igc_layer_norm_q8_backward)."""
+    dy = _same(_rows(dy, "dy"), "dy", dy.dtype, ckpt.shape, ckpt.device)
+    return _backward("igc_layer_norm_q8_backward", dy, (_ptr(ckpt.codes), _ptr(ckpt.scales)), rstd, weight, need_dweight,
+                     dy.shape[1])
+
+
+def checkpoint_pack(x: torch.Tensor) -> Checkpoint8:
+    """x [n, c] in 8 bits, one scale per row and 64 channels (igc_checkpoint_pack)."""
+    x = _rows(x, "x")
+    n, c = x.shape
+    codes = torch.empty((n, c), dtype=torch.int8, device=x.device)
+    scales = torch.empty((n, -(-c // Q8_GROUP)), dtype=torch.float32, device=x.device)
+    _call("igc_checkpoint_pack", x.device, _ptr(x), n, c, _dtype_code(x.dtype), _ptr(codes), _ptr(scales))
+    return Checkpoint8(codes, scales, x.dtype)
+
+
+def checkpoint_unpack(ckpt: Checkpoint8, dtype: torch.dtype | None = None) -> torch.Tensor:
+    """The values a checkpoint stands for, in its own type or `dtype` (igc_checkpoint_unpack)."""
+    dt = ckpt.dtype if dtype is None else dtype
+    n, c = ckpt.shape
+    x = torch.empty((n, c), dtype=dt, device=ckpt.device)
+    _call("igc_checkpoint_unpack", ckpt.device, _ptr(ckpt.codes), _ptr(ckpt.scales), n, c, _dtype_code(dt), _ptr(x))
+    return x

@@ -12,7 +12,8 @@ EXPORTS = (
     "igc_grid_build", "igc_grid_destroy", "igc_grid_info", "igc_release_memory", "igc_grid_active_ijk",
     "igc_grid_ijk_to_index", "igc_grid_export", "igc_kernel_map", "igc_sparse_conv", "igc_sparse_conv_noalloc", "igc_tuning_load",
     "igc_sparse_conv_backward", "igc_conv_grid", "igc_conv_grid_chain", "igc_conv_map", "igc_sparse_conv_between", "igc_select_path",
-    "igc_last_error",
+    "igc_last_error", "igc_sparse_conv_backward_q8", "igc_layer_norm", "igc_layer_norm_q8", "igc_layer_norm_workspace",
+    "igc_layer_norm_backward", "igc_layer_norm_q8_backward", "igc_checkpoint_pack", "igc_checkpoint_unpack",
 )
 
 STATUS = {
@@ -64,6 +65,7 @@ def load() -> ctypes.CDLL:
             "(hipcc, gfx950). There is no non-HIP fallback.")
     lib = ctypes.CDLL(LIB_PATH)
     P, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    f32, size = ctypes.c_float, ctypes.c_size_t
     sig = {
         "igc_grid_build": [P, i64, ctypes.POINTER(Allocator), P, ctypes.POINTER(P)],
         "igc_grid_destroy": [P],
@@ -83,6 +85,14 @@ def load() -> ctypes.CDLL:
         "igc_sparse_conv_between": [P, P, i64, P, i32, i32, P, i32, P, P],
         "igc_select_path": [P, i32, i32, i32, ctypes.POINTER(i32)],
         "igc_last_error": [],
+        "igc_sparse_conv_backward_q8": [P, P, P, P, i32, i32, P, i32, P, P, P, i32, P],
+        "igc_layer_norm": [P, i64, i32, i32, P, P, i32, f32, P, P, P, P],
+        "igc_layer_norm_q8": [P, i64, i32, i32, P, P, i32, f32, P, P, P, P, P],
+        "igc_layer_norm_workspace": [i64, i32, ctypes.POINTER(size)],
+        "igc_layer_norm_backward": [P, P, P, P, i64, i32, i32, P, i32, P, P, P, P, size, P],
+        "igc_layer_norm_q8_backward": [P, P, P, P, i64, i32, i32, P, i32, P, P, P, P, size, P],
+        "igc_checkpoint_pack": [P, i64, i32, i32, P, P, P],
+        "igc_checkpoint_unpack": [P, P, i64, i32, i32, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)

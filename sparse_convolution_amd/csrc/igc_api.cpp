@@ -456,22 +456,26 @@ int igc_sparse_conv(const igc_grid* g, const int32_t* d_map, const void* d_feats
   return launch_conv_ggs(g, d_map, d_feats, dtype, cin, d_w, cout, d_out, (hipStream_t)stream);
 }
 
-int igc_sparse_conv_backward(const igc_grid* g, const int32_t* d_map, const void* d_feats, int32_t dtype,
-                             int32_t cin, const void* d_w, int32_t cout, const void* d_dout, void* d_dfeats,
-                             float* d_dw, int32_t path, igc_stream stream) {
+}  // extern "C"
+
+// igc_sparse_conv_backward and its form over an 8-bit checkpoint of the features (fn names the call).
+static int conv_backward(const std::string& fn, const igc_grid* g, const int32_t* d_map, const FeatsIn& feats,
+                         int32_t dtype, int32_t cin, const void* d_w, int32_t cout, const void* d_dout, void* d_dfeats,
+                         float* d_dw, int32_t path, igc_stream stream) {
   clear_error();
-  if (!g) return set_error(IGC_ERR_INVALID_ARG, "igc_sparse_conv_backward: grid is null");
+  const bool have_feats = feats.x || (feats.codes && feats.scales);
+  if (!g) return set_error(IGC_ERR_INVALID_ARG, fn + ": grid is null");
   if (dtype != IGC_F32 && dtype != IGC_BF16)
-    return set_error(IGC_ERR_INVALID_ARG, "igc_sparse_conv_backward: bad dtype");
+    return set_error(IGC_ERR_INVALID_ARG, fn + ": bad dtype");
   if (cin < 1 || cout < 1)
-    return set_error(IGC_ERR_INVALID_ARG, "igc_sparse_conv_backward: cin and cout must be positive");
+    return set_error(IGC_ERR_INVALID_ARG, fn + ": cin and cout must be positive");
   if (path != IGC_PATH_AUTO && path != IGC_PATH_LEAF && path != IGC_PATH_GGS && path != IGC_PATH_GATHER)
-    return set_error(IGC_ERR_INVALID_ARG, "igc_sparse_conv_backward: bad path");
-  if (!d_w) return set_error(IGC_ERR_INVALID_ARG, "igc_sparse_conv_backward: d_w is null");
-  if (g->n_voxels > 0 && (!d_map || !d_dout || (d_dw && !d_feats)))
-    return set_error(IGC_ERR_INVALID_ARG, "igc_sparse_conv_backward: d_map, d_dout or d_feats is null");
-  if (d_dfeats && (d_dfeats == d_dout || d_dfeats == d_feats))
-    return set_error(IGC_ERR_INVALID_ARG, "igc_sparse_conv_backward: d_dfeats aliases an input");
+    return set_error(IGC_ERR_INVALID_ARG, fn + ": bad path");
+  if (!d_w) return set_error(IGC_ERR_INVALID_ARG, fn + ": d_w is null");
+  if (g->n_voxels > 0 && (!d_map || !d_dout || (d_dw && !have_feats)))
+    return set_error(IGC_ERR_INVALID_ARG, fn + ": d_map, d_dout or d_feats is null");
+  if (d_dfeats && (d_dfeats == d_dout || d_dfeats == feats.x || d_dfeats == feats.codes))
+    return set_error(IGC_ERR_INVALID_ARG, fn + ": d_dfeats aliases an input");
   int32_t p = path;
   if (d_dfeats) {
     if (p == IGC_PATH_AUTO) {
@@ -479,21 +483,37 @@ int igc_sparse_conv_backward(const igc_grid* g, const int32_t* d_map, const void
       if (rc) return rc;
     }
     if (p == IGC_PATH_LEAF && !leaf_conv_supported(dtype, cout, cin))
-      return set_error(IGC_ERR_UNSUPPORTED, "igc_sparse_conv_backward: leaf path does not support the input-gradient shape");
+      return set_error(IGC_ERR_UNSUPPORTED, fn + ": leaf path does not support the input-gradient shape");
     if (p == IGC_PATH_GGS && !ggs_conv_supported(dtype, cout, cin))
       return set_error(IGC_ERR_UNSUPPORTED,
-                       "igc_sparse_conv_backward: gather-GEMM-scatter path does not support the input-gradient shape");
+                       fn + ": gather-GEMM-scatter path does not support the input-gradient shape");
     if (p == IGC_PATH_GATHER && !gather_conv_supported(dtype, cout, cin))
       return set_error(IGC_ERR_UNSUPPORTED,
-                       "igc_sparse_conv_backward: general-shape path does not support the input-gradient shape");
+                       fn + ": general-shape path does not support the input-gradient shape");
   }
   if (d_dw && !wgrad_supported(dtype, cin, cout))
-    return set_error(IGC_ERR_UNSUPPORTED, "igc_sparse_conv_backward: weight gradient does not support this dtype / cin / cout");
+    return set_error(IGC_ERR_UNSUPPORTED, fn + ": weight gradient does not support this dtype / cin / cout");
   if (g->n_voxels == 0) {
     if (d_dw) return fill_u32((uint32_t*)d_dw, (int64_t)27 * cin * cout, 0u, (hipStream_t)stream);
     return IGC_OK;
   }
-  return launch_conv_backward(g, d_map, d_feats, dtype, cin, d_w, cout, d_dout, d_dfeats, d_dw, p, (hipStream_t)stream);
+  return launch_conv_backward(g, d_map, feats, dtype, cin, d_w, cout, d_dout, d_dfeats, d_dw, p, (hipStream_t)stream);
+}
+
+extern "C" {
+
+int igc_sparse_conv_backward(const igc_grid* g, const int32_t* d_map, const void* d_feats, int32_t dtype,
+                             int32_t cin, const void* d_w, int32_t cout, const void* d_dout, void* d_dfeats,
+                             float* d_dw, int32_t path, igc_stream stream) {
+  return conv_backward("igc_sparse_conv_backward", g, d_map, FeatsIn{d_feats, nullptr, nullptr}, dtype, cin, d_w, cout,
+                       d_dout, d_dfeats, d_dw, path, stream);
+}
+
+int igc_sparse_conv_backward_q8(const igc_grid* g, const int32_t* d_map, const int8_t* d_codes, const float* d_scales,
+                                int32_t dtype, int32_t cin, const void* d_w, int32_t cout, const void* d_dout,
+                                void* d_dfeats, float* d_dw, int32_t path, igc_stream stream) {
+  return conv_backward("igc_sparse_conv_backward_q8", g, d_map, FeatsIn{nullptr, d_codes, d_scales}, dtype, cin, d_w,
+                       cout, d_dout, d_dfeats, d_dw, path, stream);
 }
 
 int igc_conv_grid(const igc_grid* in, const int32_t* h_stride, int32_t transposed, const igc_allocator* alloc,

@@ -28,6 +28,7 @@
 
 #include "igc_host.h"
 #include "igc_internal.h"
+#include "igc_row.h"
 #include "igc_wave.h"
 
 namespace igc {
@@ -79,11 +80,15 @@ struct WgradSplit {
 // stage waits on its gathers; more workgroups overlap those waits). Measured: 128 -> 256 on 48M
 // voxels 215 -> 195 ms, 128 -> 128 on 17M 36.2 -> 33.8 ms and on 204k 0.269 -> 0.239 ms; the
 // smaller blocks already run six or eight waves per SIMD. Four waves spill.
-template <int MB, int NB, int NWV>
+// Q8: the input rows come from an 8-bit checkpoint (codes and per-64-channel scales): half the
+// gathered bytes, restored to the bf16 values the checkpoint stands for on the way into LDS.
+template <int MB, int NB, int NWV, bool Q8>
 __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) void k_wgrad_bf16(const int32_t* __restrict__ map, int64_t N,
                                                     const int32_t* __restrict__ perm,
                                                     const uint16_t* __restrict__ blk,
                                                     const uint16_t* __restrict__ feats,
+                                                    const int8_t* __restrict__ codes,
+                                                    const float* __restrict__ scales,
                                                     const uint16_t* __restrict__ dout, int cin, int cout,
                                                     int64_t n_tiles, int64_t tiles_per_chunk, WgradSplit sp,
                                                     float* __restrict__ part) {
@@ -139,13 +144,31 @@ __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) v
   };
   auto load_src = [&](int32_t r, int32_t& src) { src = r >= 0 ? map_o[r] : -1; };
   uint4 xa[XI], xb[XI], da[DI], db[DI];  // stage data: rows 2 pr (a) and 2 pr + 1 (b)
+  const int qgroups = (cin + kQ8Group - 1) / kQ8Group;
+  // Q8: 8 codes and, in .z, their scale; restored when the stage is written to LDS.
+  auto load_q8 = [&](int32_t r, int g) -> uint4 {
+    const uint2 q = *(const uint2*)(codes + (size_t)r * cin + c0 + g * 8);
+    return make_uint4(q.x, q.y, __float_as_uint(scales[(size_t)r * qgroups + (c0 + g * 8) / kQ8Group]), 0);
+  };
+  auto restore = [&](const uint4& q) -> uint4 {
+    const float sc = __uint_as_float(q.z);
+    bf16x8 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (__bf16)((float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3))) * sc);
+    return __builtin_bit_cast(uint4, v);
+  };
   auto load_data = [&](int32_t r0, int32_t r1, int32_t s0, int32_t s1) {
 #pragma unroll
     for (int j = 0; j < XI; ++j) {
       const int g = (tid >> 5) + GS * j;
       const bool ok = 32 * XG >= NT || g < XG;
-      xa[j] = ok && s0 >= 0 ? *(const uint4*)(feats + (size_t)s0 * cin + c0 + g * 8) : make_uint4(0, 0, 0, 0);
-      xb[j] = ok && s1 >= 0 ? *(const uint4*)(feats + (size_t)s1 * cin + c0 + g * 8) : make_uint4(0, 0, 0, 0);
+      if constexpr (Q8) {
+        xa[j] = ok && s0 >= 0 ? load_q8(s0, g) : make_uint4(0, 0, 0, 0);
+        xb[j] = ok && s1 >= 0 ? load_q8(s1, g) : make_uint4(0, 0, 0, 0);
+      } else {
+        xa[j] = ok && s0 >= 0 ? *(const uint4*)(feats + (size_t)s0 * cin + c0 + g * 8) : make_uint4(0, 0, 0, 0);
+        xb[j] = ok && s1 >= 0 ? *(const uint4*)(feats + (size_t)s1 * cin + c0 + g * 8) : make_uint4(0, 0, 0, 0);
+      }
     }
 #pragma unroll
     for (int j = 0; j < DI; ++j) {
@@ -193,7 +216,10 @@ __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) v
 #pragma unroll
     for (int j = 0; j < XI; ++j) {
       const int g = (tid >> 5) + GS * j;
-      if (32 * XG >= NT || g < XG) store_pair(s_xt, g, xa[j], xb[j]);
+      if (32 * XG >= NT || g < XG) {
+        if constexpr (Q8) store_pair(s_xt, g, restore(xa[j]), restore(xb[j]));
+        else store_pair(s_xt, g, xa[j], xb[j]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < DI; ++j) {
@@ -281,8 +307,9 @@ int launch_wgrad_reduce(const float* part, int64_t chunks, int64_t E, float* dw,
 
 namespace {
 
+// feats.codes != nullptr: the input rows come from an 8-bit checkpoint.
 template <int MB, int NB, int NWV>
-int launch_wgrad_bf16(const igc_grid* g, const int32_t* d_map, const void* d_feats, int32_t cin,
+int launch_wgrad_bf16(const igc_grid* g, const int32_t* d_map, const FeatsIn& feats, int32_t cin,
                       const void* d_dout, int32_t cout, float* d_dw, hipStream_t s) {
   const int64_t N = g->n_voxels;
   const int64_t n_tiles = (N + kTileRows - 1) / kTileRows;
@@ -318,8 +345,14 @@ int launch_wgrad_bf16(const igc_grid* g, const int32_t* d_map, const void* d_fea
   rc = launch_ggs_plan(d_map, N, perm, blk, s);
   hipError_t e = hipSuccess;
   if (rc == IGC_OK) {
-    k_wgrad_bf16<MB, NB, NWV><<<(unsigned)(kNOff * chunks * sp.mblocks * sp.nblocks), 64 * NWV, 0, s>>>(
-        d_map, N, perm, blk, (const uint16_t*)d_feats, (const uint16_t*)d_dout, cin, cout, n_tiles, tpc, sp, part);
+    const unsigned wgs = (unsigned)(kNOff * chunks * sp.mblocks * sp.nblocks);
+    if (feats.codes)
+      k_wgrad_bf16<MB, NB, NWV, true><<<wgs, 64 * NWV, 0, s>>>(d_map, N, perm, blk, nullptr, feats.codes, feats.scales,
+                                                             (const uint16_t*)d_dout, cin, cout, n_tiles, tpc, sp, part);
+    else
+      k_wgrad_bf16<MB, NB, NWV, false><<<wgs, 64 * NWV, 0, s>>>(d_map, N, perm, blk, (const uint16_t*)feats.x, nullptr,
+                                                              nullptr, (const uint16_t*)d_dout, cin, cout, n_tiles, tpc,
+                                                              sp, part);
     e = hipGetLastError();
     if (e != hipSuccess) rc = hip_status(e, "igc_sparse_conv_backward: wgrad launch");
     else rc = launch_wgrad_reduce(part, chunks, E, d_dw, s);
@@ -370,7 +403,7 @@ bool wgrad_tuned_supported(int32_t dtype, int32_t cin, int32_t cout) {
   return dtype == IGC_F32 && cin >= 1 && cout >= 1 && cin <= 64 && cout <= 64 && cin * cout <= 1024;
 }
 
-int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const void* d_feats, int32_t dtype, int32_t cin,
+int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const FeatsIn& feats, int32_t dtype, int32_t cin,
                          const void* d_w, int32_t cout, const void* d_dout, void* d_dfeats, float* d_dw,
                          int32_t dgrad_path, hipStream_t s) {
   const size_t esize = dtype == IGC_BF16 ? 2 : 4;
@@ -400,17 +433,31 @@ int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const void* d_
     // Shapes the tuned kernels do not take run on the general-shape kernel (IGC_TEST_WGRAD_FORM =
     // "general" sends every shape there: tests and measurements).
     const char* form = std::getenv("IGC_TEST_WGRAD_FORM");
-    if (!wgrad_tuned_supported(dtype, cin, cout) || (form && !std::strcmp(form, "general")))
-      return launch_wgrad_gather(g, d_map, d_feats, dtype, cin, d_dout, cout, d_dw, s);
+    const bool general = !wgrad_tuned_supported(dtype, cin, cout) || (form && !std::strcmp(form, "general"));
+    if (feats.codes && (general || dtype != IGC_BF16 || (uintptr_t)feats.codes % 8)) {
+      // Only the bf16 matrix-core kernel reads a checkpoint itself (8 codes a load): the others
+      // get its values in a temporary.
+      const size_t bytes = (size_t)g->n_voxels * cin * esize;
+      void* x = nullptr;
+      int rc = dev_alloc(&x, bytes, s, "igc_sparse_conv_backward_q8: restored features", grid_alloc(g));
+      if (rc) return rc;
+      rc = launch_unpack(feats.codes, feats.scales, g->n_voxels, cin, dtype, x, s);
+      if (rc == IGC_OK)
+        rc = launch_conv_backward(g, d_map, FeatsIn{x, nullptr, nullptr}, dtype, cin, d_w, cout, d_dout, nullptr, d_dw,
+                                  dgrad_path, s);
+      dev_free(x, bytes, s, grid_alloc(g));
+      return rc;
+    }
+    if (general) return launch_wgrad_gather(g, d_map, feats.x, dtype, cin, d_dout, cout, d_dw, s);
     if (dtype == IGC_BF16) {
       // 128 x 256 blocks on 8 waves (85 FLOP per staged byte instead of 64) measured slower on
       // the large workload (222 ms against 214): staging is not bound by the L2 feed.
       if (cin % 128 == 0 && cout % 128 == 0)
-        return launch_wgrad_bf16<128, 128, 4>(g, d_map, d_feats, cin, d_dout, cout, d_dw, s);
-      if (cin % 64 == 0) return launch_wgrad_bf16<64, 64, 4>(g, d_map, d_feats, cin, d_dout, cout, d_dw, s);
-      return launch_wgrad_bf16<32, 64, 4>(g, d_map, d_feats, cin, d_dout, cout, d_dw, s);
+        return launch_wgrad_bf16<128, 128, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
+      if (cin % 64 == 0) return launch_wgrad_bf16<64, 64, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
+      return launch_wgrad_bf16<32, 64, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
     }
-    return launch_wgrad_f32(g, d_map, d_feats, cin, d_dout, cout, d_dw, s);
+    return launch_wgrad_f32(g, d_map, feats.x, cin, d_dout, cout, d_dw, s);
   }
   return IGC_OK;
 }

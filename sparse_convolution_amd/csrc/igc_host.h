@@ -181,8 +181,37 @@ int launch_conv_map(const igc_grid* in, const igc_grid* out, const int32_t* stri
 int fill_u32(uint32_t* p, int64_t n, uint32_t v, hipStream_t s);
 bool wgrad_supported(int32_t dtype, int32_t cin, int32_t cout);
 bool wgrad_tuned_supported(int32_t dtype, int32_t cin, int32_t cout);
-int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const void* d_feats, int32_t dtype, int32_t cin,
+// A convolution's saved input: the features themselves, or an 8-bit checkpoint of them.
+struct FeatsIn {
+  const void* x = nullptr;
+  const int8_t* codes = nullptr;
+  const float* scales = nullptr;
+};
+int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const FeatsIn& feats, int32_t dtype, int32_t cin,
                          const void* d_w, int32_t cout, const void* d_dout, void* d_dfeats, float* d_dw,
                          int32_t dgrad_path, hipStream_t s);
+
+// 8-bit activation checkpoints (igc_checkpoint.hip).
+int launch_pack(const void* x, int32_t dtype, int64_t n, int32_t c, int8_t* codes, float* scales, hipStream_t s);
+int launch_unpack(const int8_t* codes, const float* scales, int64_t n, int32_t c, int32_t dtype, void* x, hipStream_t s);
+
+// Layer norm over n rows of c channels. codes != nullptr: the forward pass writes an 8-bit checkpoint
+// of the normalised rows and no mean, the backward pass reads it instead of x and mean.
+constexpr int32_t kNormMaxChannels = 4096;
+struct NormArgs {
+  const char* fn = "";  // the call named in messages
+  int32_t dtype = 0, c = 0;
+  int64_t n = 0;
+  const void *x = nullptr, *dy = nullptr, *w = nullptr, *b = nullptr;
+  int wf32 = 0;  // w and b are fp32 (else the features' type)
+  float eps = 0.f;
+  void* y = nullptr;  // y, or dx
+  float *mean = nullptr, *rstd = nullptr, *scales = nullptr, *dw = nullptr, *db = nullptr;
+  int8_t* codes = nullptr;
+};
+int launch_norm(const NormArgs& a, hipStream_t s);
+// Workgroups of the backward pass; ws holds 2 c floats for each where dw is wanted.
+int norm_bwd_parts(int64_t n, int32_t c);
+int launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t s);
 
 }  // namespace igc

@@ -1,0 +1,376 @@
+// Layer norm over the channels of each voxel, forward and backward, and its forms that keep the
+// normalised input as an 8-bit checkpoint.
+//
+//   forward:  mu = mean(x), var = mean((x - mu)^2), rstd = 1 / sqrt(var + eps),
+//             xhat = (x - mu) rstd, y = xhat w + b
+//   backward: g = dy w, dx = rstd (g - mean(g) - xhat mean(g xhat)),
+//             dw = sum over rows of dy xhat, db = sum over rows of dy
+//
+// A row is held in registers by LPR lanes (a power of two, or the whole workgroup for rows over
+// 1024 channels), V channels a load, so memory is read once and the variance is summed around
+// the mean rather than from squares. The mean is corrected by the mean of the differences from
+// it: its rounding error would otherwise be scaled by rstd, up to 316 in a constant row. All sums are fp32; weight and bias gradients are fp32 per lane
+// over the lane's rows, then added in a fixed order: the workgroup's row slots, then all workgroups in
+// fp64, so reruns are bit-identical.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <string>
+#include <type_traits>
+
+#include "igc_host.h"
+#include "igc_row.h"
+#include "igc_wave.h"
+
+// Fused multiply-adds only where written: the compiler's own choice differs between a kernel's
+// forms, and y must not depend on whether the checkpoint is written too.
+#pragma clang fp contract(off)
+
+namespace igc {
+namespace {
+
+constexpr int kNT = 256;  // threads of a workgroup
+
+// Sums a and b over the LPR lanes of a row (LPR == kNT: over the workgroup, through s).
+template <int LPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* s) {
+  if constexpr (LPR <= 64) {
+    a = lanes_sum<LPR>(a);
+    b = lanes_sum<LPR>(b);
+  } else {
+    a = lanes_sum<64>(a);
+    b = lanes_sum<64>(b);
+    __syncthreads();  // the previous sums have been read
+    if (lane_id() == 0) s[threadIdx.x >> 6] = a, s[4 + (threadIdx.x >> 6)] = b;
+    __syncthreads();
+    a = (s[0] + s[1]) + (s[2] + s[3]);
+    b = (s[4] + s[5]) + (s[6] + s[7]);
+  }
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float a, float* s) {
+  float unused = 0.f;
+  if constexpr (LPR <= 64) return lanes_sum<LPR>(a);
+  row_sum2<LPR>(a, unused, s);
+  return a;
+}
+
+template <typename T, int V, int LPR, int NV, bool Q8>
+__global__ __launch_bounds__(kNT) void k_norm(const T* __restrict__ x, int64_t n, int c, const void* __restrict__ w,
+                                              const void* __restrict__ b, int wf32, float eps, T* __restrict__ y,
+                                              float* __restrict__ mean, float* __restrict__ rstd,
+                                              int8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int SL = kNT / LPR;                                    // rows of a workgroup at a time
+  constexpr int GL = LPR < kQ8Group / V ? LPR : kQ8Group / V;      // lanes of a scale group
+  __shared__ float s_red[8];
+  const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+  const float inv_c = 1.0f / (float)c;
+  const int groups = (c + kQ8Group - 1) / kQ8Group;
+  float pw[NV][V], pb[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int ch = (j * LPR + l) * V + i;
+      pw[j][i] = w && ch < c ? load_param(w, ch, wf32) : 1.f;
+      pb[j][i] = b && ch < c ? load_param(b, ch, wf32) : 0.f;
+    }
+  for (int64_t r0 = (int64_t)blockIdx.x * SL; r0 < n; r0 += (int64_t)gridDim.x * SL) {
+    const int64_t r = r0 + slot;
+    const bool live = r < n;
+    float v[NV][V];
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int ch = (j * LPR + l) * V;
+      if (live && ch < c) {
+        load_vec<T, V>(x + r * c + ch, v[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += v[j][i];
+    }
+    const float mu0 = row_sum<LPR>(sum, s_red) * inv_c;
+    float sq = 0.f, rest = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (j * LPR + l) * V < c;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[j][i] = in ? v[j][i] - mu0 : 0.f;
+        rest += v[j][i];
+        sq = fmaf(v[j][i], v[j][i], sq);
+      }
+    }
+    row_sum2<LPR>(rest, sq, s_red);
+    rest *= inv_c;
+    const float mu = mu0 + rest;
+    const float rs = 1.0f / sqrtf(fmaxf(fmaf(-rest, rest, sq * inv_c), 0.f) + eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int ch = (j * LPR + l) * V;
+      float o[V];
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[j][i] = ch < c ? (v[j][i] - rest) * rs : 0.f;
+        o[i] = fmaf(v[j][i], pw[j][i], pb[j][i]);
+        if (Q8) a = absmax2(a, v[j][i]);
+      }
+      if (live && ch < c) store_vec<T, V>(y + r * c + ch, o);
+      if constexpr (Q8) {
+        a = lanes_absmax<GL>(a);
+        float inv, scale;
+        q8_scale(a, inv, scale);
+        if (live && ch < c) {
+          store_codes<V>(codes + r * c + ch, v[j], inv);
+          if (l % GL == 0) scales[r * groups + ch / kQ8Group] = scale;
+        }
+      }
+    }
+    if (live && l == 0) {
+      if (!Q8) mean[r] = mu;
+      rstd[r] = rs;
+    }
+  }
+}
+
+// Q8: xhat comes from codes and scales, otherwise from x, mean and rstd. part (may be null) gets
+// the workgroup's partial dw and db, [gridDim.x][2][c].
+template <typename T, int V, int LPR, int NV, bool Q8>
+__global__ __launch_bounds__(kNT) void k_norm_bwd(const T* __restrict__ dy, const T* __restrict__ x,
+                                                  const float* __restrict__ mean, const int8_t* __restrict__ codes,
+                                                  const float* __restrict__ scales, const float* __restrict__ rstd,
+                                                  const void* __restrict__ w, int wf32, int64_t n, int c,
+                                                  T* __restrict__ dx, float* __restrict__ part) {
+  constexpr int SL = kNT / LPR;
+  extern __shared__ float s_part[];  // [2][c]
+  __shared__ float s_red[8];
+  const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+  const float inv_c = 1.0f / (float)c;
+  const int groups = (c + kQ8Group - 1) / kQ8Group;
+  float pw[NV][V], aw[NV][V], ab[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int ch = (j * LPR + l) * V + i;
+      pw[j][i] = ch >= c ? 0.f : w ? load_param(w, ch, wf32) : 1.f;
+      aw[j][i] = ab[j][i] = 0.f;
+    }
+  for (int64_t r0 = (int64_t)blockIdx.x * SL; r0 < n; r0 += (int64_t)gridDim.x * SL) {
+    const int64_t r = r0 + slot;
+    const bool live = r < n;
+    const float rs = live ? rstd[r] : 0.f;
+    const float mu = !Q8 && live ? mean[r] : 0.f;
+    float g[NV][V], h[NV][V];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int ch = (j * LPR + l) * V;
+      const bool in = live && ch < c;
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[j][i] = h[j][i] = 0.f;
+      if (in) {
+        load_vec<T, V>(dy + r * c + ch, g[j]);
+        if constexpr (Q8) {
+          load_codes<V>(codes + r * c + ch, h[j]);
+          const float sc = scales[r * groups + ch / kQ8Group];
+#pragma unroll
+          for (int i = 0; i < V; ++i) h[j][i] *= sc;
+        } else {
+          load_vec<T, V>(x + r * c + ch, h[j]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) h[j][i] = (h[j][i] - mu) * rs;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        aw[j][i] = fmaf(g[j][i], h[j][i], aw[j][i]);
+        ab[j][i] += g[j][i];
+        g[j][i] *= pw[j][i];
+        s1 += g[j][i];
+        s2 = fmaf(g[j][i], h[j][i], s2);
+      }
+    row_sum2<LPR>(s1, s2, s_red);
+    s1 *= inv_c;
+    s2 *= inv_c;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int ch = (j * LPR + l) * V;
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = rs * fmaf(-h[j][i], s2, g[j][i] - s1);
+      if (live && ch < c) store_vec<T, V>(dx + r * c + ch, o);
+    }
+  }
+  if (!part) return;
+  // The row slots of a wave by lane exchange, then the waves one after the other.
+  constexpr int WL = LPR < 64 ? LPR : 64;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int m = WL; m < 64; m <<= 1) {
+        aw[j][i] += __shfl_xor(aw[j][i], m, 64);
+        ab[j][i] += __shfl_xor(ab[j][i], m, 64);
+      }
+    }
+  if constexpr (LPR == kNT) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int ch = (j * LPR + l) * V + i;
+        if (ch < c) {
+          part[(size_t)blockIdx.x * 2 * c + ch] = aw[j][i];
+          part[(size_t)blockIdx.x * 2 * c + c + ch] = ab[j][i];
+        }
+      }
+  } else {
+    for (int q = 0; q < kNT / 64; ++q) {
+      if ((int)(threadIdx.x >> 6) == q && lane_id() < WL) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int ch = (j * LPR + l) * V + i;
+            if (ch < c) {
+              s_part[ch] = q ? s_part[ch] + aw[j][i] : aw[j][i];
+              s_part[c + ch] = q ? s_part[c + ch] + ab[j][i] : ab[j][i];
+            }
+          }
+      }
+      __syncthreads();
+    }
+    for (int e = threadIdx.x; e < 2 * c; e += kNT) part[(size_t)blockIdx.x * 2 * c + e] = s_part[e];
+  }
+}
+
+// dw[e] (e < c) and db[e - c] = sum over chunks of part[chunk][e] in fp64, in a fixed order.
+__global__ __launch_bounds__(kNT) void k_norm_reduce(const float* __restrict__ part, int chunks, int c,
+                                                     float* __restrict__ dw, float* __restrict__ db) {
+  constexpr int EL = 16, NG = kNT / EL;
+  __shared__ double s_sum[NG][EL];
+  const int el = threadIdx.x % EL, q = threadIdx.x / EL;
+  const int e = blockIdx.x * EL + el;
+  double acc = 0.0;
+  if (e < 2 * c) {
+#pragma unroll 8
+    for (int k = q; k < chunks; k += NG) acc += (double)part[(size_t)k * 2 * c + e];
+  }
+  s_sum[q][el] = acc;
+  __syncthreads();
+  if (q == 0 && e < 2 * c) {
+    double t = 0.0;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) t += s_sum[k][el];
+    if (e < c) dw[e] = (float)t;
+    else db[e - c] = (float)t;
+  }
+}
+
+template <int V>
+using IntC = std::integral_constant<int, V>;
+
+// Calls f(V, LPR, NV) as compile-time integers for rows of c channels loaded V at a time.
+template <int V, typename F>
+void with_row_shape(int c, F f) {
+  const int lanes = (c + V - 1) / V;  // loads of a row
+  if (lanes <= 1) return f(IntC<V>{}, IntC<1>{}, IntC<1>{});
+  if (lanes <= 2) return f(IntC<V>{}, IntC<2>{}, IntC<1>{});
+  if (lanes <= 4) return f(IntC<V>{}, IntC<4>{}, IntC<1>{});
+  if (lanes <= 8) return f(IntC<V>{}, IntC<8>{}, IntC<1>{});
+  if (lanes <= 16) return f(IntC<V>{}, IntC<16>{}, IntC<1>{});
+  if (lanes <= 32) return f(IntC<V>{}, IntC<32>{}, IntC<1>{});
+  if (lanes <= 64) return f(IntC<V>{}, IntC<64>{}, IntC<1>{});
+  if (lanes <= 128) return f(IntC<V>{}, IntC<64>{}, IntC<2>{});
+  if constexpr (V < 8) {
+    if (lanes <= 256) return f(IntC<V>{}, IntC<64>{}, IntC<4>{});
+    if constexpr (V < 4) {
+      if (lanes <= 512) return f(IntC<V>{}, IntC<64>{}, IntC<8>{});
+      if (lanes <= 1024) return f(IntC<V>{}, IntC<64>{}, IntC<16>{});
+      if (lanes <= 2048) return f(IntC<V>{}, IntC<kNT>{}, IntC<8>{});
+      return f(IntC<V>{}, IntC<kNT>{}, IntC<16>{});
+    } else {
+      if (lanes <= 512) return f(IntC<V>{}, IntC<kNT>{}, IntC<2>{});
+      return f(IntC<V>{}, IntC<kNT>{}, IntC<4>{});
+    }
+  } else {
+    if (lanes <= 256) return f(IntC<V>{}, IntC<kNT>{}, IntC<1>{});
+    return f(IntC<V>{}, IntC<kNT>{}, IntC<2>{});
+  }
+}
+
+// Values per load: the widest that divides the row and that every pointer is aligned for.
+template <typename T>
+int row_vec(int c, const void* a, const void* b, const void* q) {
+  const uintptr_t p = (uintptr_t)a | (uintptr_t)b;
+  for (int v = 16 / (int)sizeof(T); v >= 4; v /= 2)
+    if (c % v == 0 && p % (v * sizeof(T)) == 0 && (uintptr_t)q % v == 0) return v;
+  return 1;
+}
+
+template <typename T, typename F>
+void with_shape(int c, int vec, F f) {
+  if constexpr (sizeof(T) == 2) {
+    if (vec == 8) return with_row_shape<8>(c, f);
+  }
+  if (vec == 4) return with_row_shape<4>(c, f);
+  with_row_shape<1>(c, f);
+}
+
+template <typename T, bool Q8>
+int norm_t(const NormArgs& a, hipStream_t s) {
+  const int vec = row_vec<T>(a.c, a.x, a.y, a.codes);
+  with_shape<T>(a.c, vec, [&](auto V, auto L, auto NV) {
+    const int64_t blocks = (a.n + kNT / L - 1) / (kNT / L);
+    k_norm<T, V, L, NV, Q8><<<(unsigned)std::min<int64_t>(blocks, 4096), kNT, 0, s>>>(
+        (const T*)a.x, a.n, a.c, a.w, a.b, a.wf32, a.eps, (T*)a.y, a.mean, a.rstd, a.codes, a.scales);
+  });
+  IGC_HIP(hipGetLastError(), a.fn);
+  return IGC_OK;
+}
+
+template <typename T, bool Q8>
+int norm_bwd_t(const NormArgs& a, void* ws, hipStream_t s) {
+  const int vec = row_vec<T>(a.c, Q8 ? a.y : a.x, (void*)((uintptr_t)a.dy | (uintptr_t)a.y), a.codes);
+  const int parts = norm_bwd_parts(a.n, a.c);
+  float* part = a.dw ? (float*)ws : nullptr;
+  with_shape<T>(a.c, vec, [&](auto V, auto L, auto NV) {
+    k_norm_bwd<T, V, L, NV, Q8><<<(unsigned)parts, kNT, 8 * (size_t)a.c, s>>>(
+        (const T*)a.dy, (const T*)a.x, a.mean, a.codes, a.scales, a.rstd, a.w, a.wf32, a.n, a.c, (T*)a.y, part);
+  });
+  IGC_HIP(hipGetLastError(), a.fn);
+  if (part) {
+    k_norm_reduce<<<(unsigned)((2 * a.c + 15) / 16), kNT, 0, s>>>(part, parts, a.c, a.dw, a.db);
+    IGC_HIP(hipGetLastError(), a.fn);
+  }
+  return IGC_OK;
+}
+
+}  // namespace
+
+int norm_bwd_parts(int64_t n, int32_t c) {
+  // One partial of 2 c floats per workgroup.
+  const int64_t rows = 64;
+  return (int)std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 1024));
+}
+
+int launch_norm(const NormArgs& a, hipStream_t s) {
+  if (a.dtype == IGC_BF16) return a.codes ? norm_t<bf16_t, true>(a, s) : norm_t<bf16_t, false>(a, s);
+  return a.codes ? norm_t<float, true>(a, s) : norm_t<float, false>(a, s);
+}
+
+int launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t s) {
+  if (a.dtype == IGC_BF16) return a.codes ? norm_bwd_t<bf16_t, true>(a, ws, s) : norm_bwd_t<bf16_t, false>(a, ws, s);
+  return a.codes ? norm_bwd_t<float, true>(a, ws, s) : norm_bwd_t<float, false>(a, ws, s);
+}
+
+}  // namespace igc
