@@ -340,6 +340,52 @@ int igc_layer_norm_q8_backward(const void* d_dy, const int8_t* d_codes, const fl
                                int64_t n, int32_t c, int32_t dtype, const void* d_w, int32_t wdtype, void* d_dx,
                                float* d_dw, float* d_db, void* d_ws, size_t ws_bytes, igc_stream stream);
 
+/* A cross-attention problem: queries (voxels or object queries) of `batch` sequences attending to
+ * another set of rows (an encoder's states, or voxels) of the same sequences.
+ *  - q is [n_q, heads, dim], k and v [n_k, kv_heads, dim] of type `dtype`, dim contiguous, with any row
+ *    and head strides (elements): slices of one projection need no copy. Query head h reads key head
+ *    h / (heads / kv_heads). dim is 1 to 128.
+ *  - Sequence b holds query rows d_q_offsets[b] .. d_q_offsets[b+1] and key rows d_kv_offsets[b] ..
+ *    d_kv_offsets[b+1] (int32 device arrays [batch + 1], ascending from 0 to n_q and n_k; they may both be NULL
+ *    with batch 1). Sequences may be empty on either side. Offsets are clamped to the arrays, so wrong ones
+ *    cannot reach outside; rows that no sequence covers are left unwritten.
+ *  - d_key_mask (uint8 [n_k], may be NULL): rows with 0 are left out. Their k and v may hold anything.
+ *  - scale multiplies q . k; positive and finite. */
+typedef struct {
+  int32_t dtype, batch, heads, kv_heads, dim;
+  float scale;
+  int64_t n_q, n_k;
+  int64_t q_stride[2], k_stride[2], v_stride[2]; /* between rows, between heads */
+  const int32_t* d_q_offsets;
+  const int32_t* d_kv_offsets;
+  const uint8_t* d_key_mask;
+} igc_attention_t;
+
+/* Bytes of d_ws that the forward (backward = 0) or backward call needs; may be 0 (host only). */
+int igc_cross_attention_workspace(const igc_attention_t* problem, int32_t backward, size_t* bytes);
+
+/* For query row i and head h, over the keys j of i's sequence that the mask keeps:
+ *     s_j = scale * q[i, h] . k[j, hk], d_lse[i, h] = log(sum_j exp(s_j)),
+ *     d_out[i, h] = sum_j exp(s_j - d_lse[i, h]) * v[j, hk]
+ * d_out [n_q, heads, dim] of type `dtype`, d_lse float [n_q, heads], both dense. A row with no key left
+ * gives d_out = 0 and d_lse = -infinity. Statistics and sums are fp32; with bf16 data the probabilities are
+ * rounded to bf16 for the product with v. d_ws: at least igc_cross_attention_workspace bytes
+ * (IGC_ERR_CAPACITY otherwise). d_out must not alias an input. Reruns are bit-identical. */
+int igc_cross_attention(const igc_attention_t* problem, const void* d_q, const void* d_k, const void* d_v, void* d_out,
+                        float* d_lse, void* d_ws, size_t ws_bytes, igc_stream stream);
+
+/* Gradients of igc_cross_attention from its inputs, d_out, d_lse and d_dout = dL/dout (dense, type
+ * `dtype`): with p_j = exp(s_j - lse) and ds_j = p_j * (dout . v_j - dout . out),
+ *     d_dq[i, h] = scale * sum_j ds_j k_j,
+ *     d_dk[j, hk] = scale * sum of ds_j q[i, h], d_dv[j, hk] = sum of p_j dout[i, h], over the queries i of
+ *     j's sequence and the heads h that share hk.
+ * d_dq [n_q, heads, dim], d_dk and d_dv [n_k, kv_heads, dim], dense, of type `dtype`; NULL d_dq, or NULL d_dk
+ * and d_dv together, skip them. Masked keys get zeros. With bf16 data p and ds are rounded to bf16 for their
+ * products; sums are fp32 in a fixed order (reruns are bit-identical). */
+int igc_cross_attention_backward(const igc_attention_t* problem, const void* d_q, const void* d_k, const void* d_v,
+                                 const void* d_out, const float* d_lse, const void* d_dout, void* d_dq, void* d_dk,
+                                 void* d_dv, void* d_ws, size_t ws_bytes, igc_stream stream);
+
 /* Output grid of a 3x3x3 convolution with per-axis stride h_stride[0..2] (host, each 1, 2 or 3)
  * over `in` (the grid-to-grid ops ConvGrid and ConvTransposeGrid in the op table of the "ONNX
  * Runtime support for fVDB operations" proposal; the pages name the ops without a formula, so

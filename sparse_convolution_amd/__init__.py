@@ -13,15 +13,15 @@ import torch
 
 from . import _lib
 from ._args import BF16, F32, _device_tensor, _dtype_code, _ptr, _stream
-from ._block import (Checkpoint8, checkpoint_pack, checkpoint_unpack, layer_norm, layer_norm_backward,
-                     layer_norm_checkpoint, layer_norm_checkpoint_backward)
+from ._block import (Checkpoint8, checkpoint_pack, checkpoint_unpack, cross_attention, cross_attention_backward,
+                     layer_norm, layer_norm_backward, layer_norm_checkpoint, layer_norm_checkpoint_backward)
 from ._lib import IgcError
 
 __all__ = [
     "Grid", "grid_build", "kernel_map", "sparse_conv", "sparse_conv_backward", "conv_grid", "conv_grid_chain", "conv_map",
     "sparse_conv_between", "standard_offsets", "release_memory", "tuning_load", "IgcError",
     "Checkpoint8", "checkpoint_pack", "checkpoint_unpack", "layer_norm", "layer_norm_backward", "layer_norm_checkpoint",
-    "layer_norm_checkpoint_backward",
+    "layer_norm_checkpoint_backward", "cross_attention", "cross_attention_backward",
     "PATH_AUTO", "PATH_LEAF", "PATH_GGS", "PATH_GATHER",
 ]
 

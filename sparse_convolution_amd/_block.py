@@ -1,5 +1,5 @@
 """Operators between convolutions: layer norm and 8-bit activation checkpoints over voxel
-features [n, channels]."""
+features [n, channels], and cross attention of voxel or object queries to another set of rows."""
 from __future__ import annotations
 
 import ctypes
@@ -164,3 +164,89 @@ def checkpoint_unpack(ckpt: Checkpoint8, dtype: torch.dtype | None = None) -> to
     x = torch.empty((n, c), dtype=dt, device=ckpt.device)
     _call("igc_checkpoint_unpack", ckpt.device, _ptr(ckpt.codes), _ptr(ckpt.scales), n, c, _dtype_code(dt), _ptr(x))
     return x
+
+
+def _heads(t: torch.Tensor, name: str, dtype: torch.dtype) -> torch.Tensor:
+    """Checks a [rows, heads, dim] operand; row and head strides are free."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [rows, heads, dim], got {tuple(t.shape)}")
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return t
+
+
+def _problem(q, k, v, q_offsets, kv_offsets, key_mask, scale) -> _lib.Attention:
+    dt, dev = q.dtype, q.device
+    _dtype_code(dt)
+    _heads(q, "q", dt), _heads(k, "k", dt), _heads(v, "v", dt)
+    (nq, heads, dim), (nk, kv_heads, _) = q.shape, k.shape
+    if k.shape != v.shape or k.shape[2] != dim:
+        raise ValueError(f"k and v must have shape [n, kv_heads, {dim}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    if kv_heads < 1 or heads % kv_heads:
+        raise ValueError(f"heads ({heads}) must be a multiple of kv_heads ({kv_heads})")
+    if (q_offsets is None) != (kv_offsets is None):
+        raise ValueError("q_offsets and kv_offsets come together")
+    batch = 1
+    if q_offsets is not None:
+        batch = q_offsets.shape[0] - 1 if q_offsets.dim() == 1 else -1
+        for t, name in ((q_offsets, "q_offsets"), (kv_offsets, "kv_offsets")):
+            _device_tensor(t, name, torch.int32)
+            if batch < 1 or tuple(t.shape) != (batch + 1,):
+                raise ValueError("q_offsets and kv_offsets must have shape [batch + 1]")
+    if key_mask is not None:
+        if isinstance(key_mask, torch.Tensor) and key_mask.dtype == torch.bool:
+            key_mask = key_mask.view(torch.uint8)
+        _same(key_mask, "key_mask", torch.uint8, (nk,), dev)
+    for t in (k, v, q_offsets, kv_offsets):
+        if t is not None and t.device != dev:
+            raise ValueError("all operands must be on one device")
+    pair = ctypes.c_int64 * 2
+    return _lib.Attention(_dtype_code(dt), batch, heads, kv_heads, dim, dim ** -0.5 if scale is None else scale, nq, nk,
+                          pair(*q.stride()[:2]), pair(*k.stride()[:2]), pair(*v.stride()[:2]), _ptr(q_offsets),
+                          _ptr(kv_offsets), _ptr(key_mask))
+
+
+def _workspace(p: _lib.Attention, backward: int, device: torch.device):
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().igc_cross_attention_workspace(ctypes.byref(p), backward, ctypes.byref(n)))
+    return (torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None), n
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor | None = None,
+                    kv_offsets: torch.Tensor | None = None, key_mask: torch.Tensor | None = None,
+                    scale: float | None = None):
+    """Attention of q [nq, heads, dim] to k and v [nk, kv_heads, dim] (kv_heads divides heads, dim up to 128,
+    any row and head strides), sequence by sequence: rows q_offsets[b] .. q_offsets[b+1] of q attend to rows
+    kv_offsets[b] .. kv_offsets[b+1] of k and v (int32 [batch + 1] on the device; None: one sequence).
+    key_mask (bool or uint8 [nk]): false rows are left out. scale defaults to dim ** -0.5. Returns (out
+    [nq, heads, dim], lse [nq, heads] float32); a row without keys gets zeros and -inf (igc_cross_attention)."""
+    p = _problem(q, k, v, q_offsets, kv_offsets, key_mask, scale)
+    dev = q.device
+    out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    ws, n = _workspace(p, 0, dev)
+    _call("igc_cross_attention", dev, ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(ws), n)
+    return out, lse
+
+
+def cross_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                             lse: torch.Tensor, q_offsets: torch.Tensor | None = None,
+                             kv_offsets: torch.Tensor | None = None, key_mask: torch.Tensor | None = None,
+                             scale: float | None = None, need_dq: bool = True, need_dkv: bool = True):
+    """Gradients (dq, dk, dv) of cross_attention for the output gradient dout, from its inputs and results;
+    None for those not needed (igc_cross_attention_backward)."""
+    p = _problem(q, k, v, q_offsets, kv_offsets, key_mask, scale)
+    dev = q.device
+    _same(dout, "dout", q.dtype, q.shape, dev), _same(out, "out", q.dtype, q.shape, dev)
+    _same(lse, "lse", torch.float32, q.shape[:2], dev)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if need_dq else None
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev) if need_dkv else None
+    dv = torch.empty(k.shape, dtype=q.dtype, device=dev) if need_dkv else None
+    ws, n = _workspace(p, 1, dev)
+    _call("igc_cross_attention_backward", dev, ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+          _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n)
+    return dq, dk, dv

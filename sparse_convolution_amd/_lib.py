@@ -14,6 +14,7 @@ EXPORTS = (
     "igc_sparse_conv_backward", "igc_conv_grid", "igc_conv_grid_chain", "igc_conv_map", "igc_sparse_conv_between", "igc_select_path",
     "igc_last_error", "igc_sparse_conv_backward_q8", "igc_layer_norm", "igc_layer_norm_q8", "igc_layer_norm_workspace",
     "igc_layer_norm_backward", "igc_layer_norm_q8_backward", "igc_checkpoint_pack", "igc_checkpoint_unpack",
+    "igc_cross_attention", "igc_cross_attention_backward", "igc_cross_attention_workspace",
 )
 
 STATUS = {
@@ -44,6 +45,15 @@ class TopologyHost(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in (
         "root_key", "upper_origin", "upper_mask", "upper_first", "lower_origin", "lower_mask",
         "lower_first", "leaf_origin", "leaf_mask", "leaf_offset", "leaf_prefix")]
+
+
+class Attention(ctypes.Structure):  # igc_attention_t
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("dim", ctypes.c_int32), ("scale", ctypes.c_float), ("n_q", ctypes.c_int64), ("n_k", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2),
+        ("d_q_offsets", ctypes.c_void_p), ("d_kv_offsets", ctypes.c_void_p), ("d_key_mask", ctypes.c_void_p),
+    ]
 
 
 class IgcError(RuntimeError):
@@ -93,6 +103,9 @@ def load() -> ctypes.CDLL:
         "igc_layer_norm_q8_backward": [P, P, P, P, i64, i32, i32, P, i32, P, P, P, P, size, P],
         "igc_checkpoint_pack": [P, i64, i32, i32, P, P, P],
         "igc_checkpoint_unpack": [P, P, i64, i32, i32, P, P],
+        "igc_cross_attention_workspace": [ctypes.POINTER(Attention), i32, ctypes.POINTER(size)],
+        "igc_cross_attention": [ctypes.POINTER(Attention), P, P, P, P, P, P, size, P],
+        "igc_cross_attention_backward": [ctypes.POINTER(Attention), P, P, P, P, P, P, P, P, P, P, size, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)

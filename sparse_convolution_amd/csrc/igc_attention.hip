@@ -1,0 +1,277 @@
+// Cross attention of voxel (or object) queries to an encoder's states, forward pass.
+//
+//   s_ij = scale q_i . k_j over the keys j of the query's sequence that the mask keeps
+//   lse_i = log sum_j exp s_ij, out_i = sum_j exp(s_ij - lse_i) v_j
+//
+// One pass over the keys with a running maximum and sum (online softmax); scores never leave
+// registers. A row without keys gives out = 0, lse = -infinity.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "igc_attn.h"
+#include "igc_host.h"
+
+namespace igc {
+namespace {
+
+constexpr int kNT = 256;
+
+// Four waves of 32 NQ query rows each over tiles of BN keys. A row is a (query, head of the group
+// that shares the key head) pair, so few queries with shared key heads still fill a tile.
+// splits > 1: each workgroup takes one part of the sequence's keys and leaves an unnormalised result.
+template <typename T, int DP, int NQ, int BN>
+__global__ __launch_bounds__(kNT) void k_attn_fwd(AttnArgs a) {
+  typedef typename Frag<T>::type frag;
+  constexpr int LD = lds_ld<T, DP>();
+  constexpr int BM = 128 * NQ;
+  constexpr int KT = BN / 32, DT = DP / 32;
+  __shared__ __attribute__((aligned(16))) T s_k[2][BN * LD];
+  __shared__ __attribute__((aligned(16))) T s_v[2][BN * LD];
+
+  const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
+  const int kh = blockIdx.x % a.kv_heads;
+  const int split = (blockIdx.x / a.kv_heads) % a.splits;
+  int b;
+  const int64_t tile = find_tile(a.qo, a.batch, a.nq, a.group, BM, blockIdx.x / (a.kv_heads * a.splits), b);
+  int64_t q0, q1, k0, k1;
+  seq_rows(a.qo, b, a.nq, q0, q1);
+  seq_rows(a.ko, b, a.nk, k0, k1);
+  const int64_t rows = (q1 - q0) * a.group;
+  if (tile * BM >= rows) return;
+  if (a.splits > 1) {
+    const int64_t part = ((k1 - k0 + a.splits - 1) / a.splits + BN - 1) / BN * BN;
+    k0 = k0 + split * part < k1 ? k0 + split * part : k1;
+    k1 = k0 + part < k1 ? k0 + part : k1;
+  }
+
+  // This lane's query rows (one per 32-column tile), and their values as second operands.
+  int64_t qi[NQ];
+  int head[NQ];
+  bool live[NQ];
+  frag fq[NQ][DP / 16];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
+    live[n] = r < rows;
+    split_row(live[n] ? r : 0, a.group, qi[n], head[n]);
+    qi[n] += q0;
+    head[n] += kh * a.group;
+    const T* p = (const T*)a.q + qi[n] * a.qs[0] + head[n] * a.qs[1];
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+      const int d = kk * 16 + h * 8;
+      fq[n][kk] = load8<T>(p + d, live[n] ? a.dim - d : 0, a.qvec);
+    }
+  }
+
+  const float c = a.scale * kLog2e;
+  f32x16 o[NQ][DT];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    m[n] = -INFINITY;
+    l[n] = 0.f;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) o[n][t] = zero16();
+  }
+
+  Stage<T, BN, DP, kNT> sk, sv;
+  const T* kp = (const T*)a.k + kh * a.ks[1];
+  const T* vp = (const T*)a.v + kh * a.vs[1];
+  auto fetch = [&](int64_t j0) {
+    auto row_ok = [&](int row) { return j0 + row < k1 && (!a.mask || a.mask[j0 + row]); };
+    sk.load([&](int row) { return row_ok(row) ? kp + (j0 + row) * a.ks[0] : nullptr; }, a.dim, a.kvec);
+    sv.load([&](int row) { return row_ok(row) ? vp + (j0 + row) * a.vs[0] : nullptr; }, a.dim, a.kvec);
+  };
+  auto key_bits = [&](int64_t j0) -> uint64_t {
+    const bool ok = lane < BN && j0 + lane < k1 && (!a.mask || a.mask[j0 + lane]);
+    return __ballot(ok);
+  };
+
+  uint64_t next_bits = 0;
+  if (k0 < k1) {
+    fetch(k0);
+    next_bits = key_bits(k0);
+  }
+  int buf = 0;
+  for (int64_t j0 = k0; j0 < k1; j0 += BN, buf ^= 1) {
+    sk.template store<LD>(s_k[buf]);
+    sv.template store<LD>(s_v[buf]);
+    const uint64_t bits = next_bits;
+    if (j0 + BN < k1) {
+      fetch(j0 + BN);
+      next_bits = key_bits(j0 + BN);
+    }
+    // Two buffers: the barrier of the last tile already had every wave past reading this one.
+    __syncthreads();
+    f32x16 s[NQ][KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) s[n][t] = zero16();
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        const frag fk = load_row<T>(&s_k[buf][(t * 32 + (lane & 31)) * LD + kk * 16 + h * 8]);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) s[n][t] = mma(fk, fq[n][kk], s[n][t]);
+      }
+    }
+    if (bits != (BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1)) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (!(w >> (8 * (r >> 2) + (r & 3)) & 1)) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) s[n][t][r] = -INFINITY;
+          }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float top = s[n][0][0];
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[n][t][r]);
+      top = fmaxf(top, __shfl_xor(top, 32, 64)) * c;
+      const float m_new = fmaxf(m[n], top);
+      if (__any(m_new > m[n])) {
+        const float f = m[n] == -INFINITY ? 0.f : exp2f(m[n] - m_new);
+        l[n] *= f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[n][t][r] *= f;
+        m[n] = m_new;
+      }
+      const float base = m[n] == -INFINITY ? 0.f : m[n];
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[n][t][r] = __builtin_amdgcn_exp2f(fmaf(s[n][t][r], c, -base));
+          l[n] += s[n][t][r];
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int mm = 0; mm < 2; ++mm) {
+        frag p[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) to_frag(s[n][t], mm, p[n]);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const frag fv = load_tr<LD>(s_v[buf], t * 32 + mm * 16, d * 32);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) o[n][d] = mma(fv, p[n], o[n][d]);
+        }
+      }
+  }
+
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const float total = l[n] + __shfl_xor(l[n], 32, 64);
+    if (!live[n]) continue;
+    const int64_t row = qi[n] * a.heads + head[n];
+    if (a.splits > 1) {
+      float* po = a.part_a + ((int64_t)split * a.nq * a.heads + row) * a.dim;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) store_col<float>(po, d * 32, a.dim, o[n][d], 1.f, a.dim % 4 == 0);
+      if (h == 0) {
+        float* ml = a.part_b + ((int64_t)split * a.nq * a.heads + row) * 2;
+        ml[0] = m[n];
+        ml[1] = total;
+      }
+    } else {
+      const float f = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        store_col<T>((T*)a.out + row * a.dim, d * 32, a.dim, o[n][d], f, a.ovec);
+      if (h == 0) a.lse[row] = total == 0.f ? -INFINITY : kLn2 * (m[n] + log2f(total));
+    }
+  }
+}
+
+// Joins the parts of a split key axis: one wave per row.
+template <typename T>
+__global__ __launch_bounds__(kNT) void k_attn_join(AttnArgs a) {
+  const int lane = lane_id();
+  const int64_t rows = a.nq * a.heads;
+  const int64_t row = (int64_t)blockIdx.x * (kNT / 64) + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  float top = -INFINITY;
+  for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.part_b[((int64_t)s * rows + row) * 2]);
+  top = lanes_reduce<64>(top, [](float x, float y) { return fmaxf(x, y); });
+  const float base = top == -INFINITY ? 0.f : top;
+  float total = 0.f, o0 = 0.f, o1 = 0.f;
+  for (int s = 0; s < a.splits; ++s) {
+    const int64_t at = (int64_t)s * rows + row;
+    const float f = __builtin_amdgcn_exp2f(a.part_b[at * 2] - base);
+    total += f * a.part_b[at * 2 + 1];
+    const float* po = a.part_a + at * a.dim;
+    if (lane < a.dim) o0 += f * po[lane];
+    if (lane + 64 < a.dim) o1 += f * po[lane + 64];
+  }
+  const float f = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;
+  T* out = (T*)a.out + row * a.dim;
+  if (lane < a.dim) out[lane] = (T)(o0 * f);
+  if (lane + 64 < a.dim) out[lane + 64] = (T)(o1 * f);
+  if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
+}
+
+template <typename T, int DP>
+struct FwdShape;  // NQ, BN
+template <int DP>
+struct FwdShape<bf16_t, DP> {
+  static constexpr int NQ = DP <= 64 ? 2 : 1, BN = 64;
+};
+template <int DP>
+struct FwdShape<float, DP> {
+  static constexpr int NQ = 1, BN = 32;
+};
+
+int64_t fwd_slots(const AttnArgs& a, int bm) { return a.nq * a.group / bm + a.batch; }
+
+// Row tiles of the forward kernel for this problem.
+int fwd_bm(int dtype, int dim) { return dtype == IGC_BF16 && dim <= 64 ? 256 : 128; }
+
+template <typename T, int DP>
+void fwd_go(const AttnArgs& a, hipStream_t s) {
+  constexpr int NQ = FwdShape<T, DP>::NQ, BN = FwdShape<T, DP>::BN;
+  const int64_t wgs = fwd_slots(a, 128 * NQ) * a.kv_heads * a.splits;
+  k_attn_fwd<T, DP, NQ, BN><<<(unsigned)wgs, kNT, 0, s>>>(a);
+  if (a.splits > 1) k_attn_join<T><<<(unsigned)((a.nq * a.heads + kNT / 64 - 1) / (kNT / 64)), kNT, 0, s>>>(a);
+}
+
+template <typename T>
+void fwd_t(const AttnArgs& a, hipStream_t s) {
+  if (a.dim <= 32) return fwd_go<T, 32>(a, s);
+  if (a.dim <= 64) return fwd_go<T, 64>(a, s);
+  if (a.dim <= 96) return fwd_go<T, 96>(a, s);
+  fwd_go<T, 128>(a, s);
+}
+
+}  // namespace
+
+int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim) {
+  // Parts of the key axis: none while the query tiles alone fill the GPU twice over, else enough for
+  // that, each of at least 256 keys.
+  const int bm = fwd_bm(dtype, dim);
+  const int64_t per_seq = (nq / batch) * (heads / kv_heads);
+  const int64_t wgs = batch * ((per_seq + bm - 1) / bm) * kv_heads;
+  const int64_t want = wgs >= 512 ? 1 : 512 / std::max<int64_t>(1, wgs);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 128), nk / batch / 256));
+}
+
+int launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s) {
+  if (dtype == IGC_BF16) fwd_t<bf16_t>(a, s);
+  else fwd_t<float>(a, s);
+  IGC_HIP(hipGetLastError(), a.fn);
+  return IGC_OK;
+}
+
+}  // namespace igc

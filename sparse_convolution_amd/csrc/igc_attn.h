@@ -1,0 +1,203 @@
+// Pieces shared by the cross-attention kernels: ragged tiles, matrix-core fragments and staging.
+//
+// Fragments. All products run on 32x32 matrix instructions whose result puts one column in each
+// lane (lane % 32) and 16 rows in its registers: register r of lane half h = lane / 32 is row
+// 8 (r / 4) + 4 h + r % 4. Scores are computed transposed where the next product sums over keys (so
+// that a lane owns a query: softmax statistics stay in the lane) and straight where it sums over
+// queries; either way, registers 8 m .. 8 m + 7 of a score tile are, without any exchange between lanes,
+// the second operand of the next product over the tile's 16 rows m, provided its first operand lists
+// the same rows: 16 m + 4 h + 0..3, then 16 m + 8 + 4 h + 0..3. load_tr reads that operand.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "igc_host.h"
+#include "igc_row.h"
+#include "igc_wave.h"
+
+namespace igc {
+
+typedef bf16_t bf16x4 __attribute__((ext_vector_type(4)));
+typedef bf16_t bf16x8v __attribute__((ext_vector_type(8)));
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+typedef float f32x8v __attribute__((ext_vector_type(8), aligned(16)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+// Rows [begin, end) of sequence b; whatever the offsets hold, within [0, n].
+__device__ __forceinline__ void seq_rows(const int32_t* off, int b, int64_t n, int64_t& begin, int64_t& end) {
+  if (!off) {
+    begin = 0, end = n;
+    return;
+  }
+  begin = clamp64(off[b], 0, n);
+  end = clamp64(off[b + 1], begin, n);
+}
+
+// Tiles of `bm` rows over ragged sequences without a plan: sequence b of rows [begin, end) (times mul)
+// owns the slots from begin * mul / bm + b on, which are at least as many as its tiles, so that
+// n * mul / bm + batch slots cover everything and a slot finds its sequence by a binary search.
+// Returns the tile in sequence b (it may lie past the sequence's end).
+__device__ __forceinline__ int64_t find_tile(const int32_t* off, int batch, int64_t n, int mul, int bm, int64_t slot,
+                                             int& b) {
+  b = 0;
+  if (!off) return slot;
+  int hi = batch;  // slots of hi and beyond start after `slot`
+  while (hi - b > 1) {
+    const int mid = (b + hi) >> 1;
+    if (clamp64(off[mid], 0, n) * mul / bm + mid <= slot) b = mid;
+    else hi = mid;
+  }
+  return slot - (clamp64(off[b], 0, n) * mul / bm + b);
+}
+
+// Query and head of the group of row r of a sequence (rows of all sequences together stay below 2^31).
+__device__ __forceinline__ void split_row(int64_t r, int group, int64_t& query, int& g) {
+  const uint32_t x = (uint32_t)r, q = group == 1 ? x : x / (uint32_t)group;
+  query = q;
+  g = (int)(x - q * (uint32_t)group);
+}
+
+template <typename T>
+struct Frag;  // 8 values of one lane along the summed axis
+template <>
+struct Frag<bf16_t> {
+  typedef bf16x8v type;
+};
+template <>
+struct Frag<float> {
+  typedef f32x8v type;
+};
+
+// c += a b over 16 values of the summed axis.
+__device__ __forceinline__ f32x16 mma(const bf16x8v& a, const bf16x8v& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(const f32x8v& a, const f32x8v& b, f32x16 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// 8 values at p; only the first `have` exist. vec: p is 16-byte aligned and all 8 or none exist.
+template <typename T>
+__device__ __forceinline__ typename Frag<T>::type load8(const T* p, int have, bool vec) {
+  typename Frag<T>::type f;
+  if (vec && have >= 8) {
+    f = *(const typename Frag<T>::type*)p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < have ? p[i] : (T)0.f;
+  }
+  return f;
+}
+
+// First operand from LDS rows (row-major, the summed axis contiguous).
+template <typename T>
+__device__ __forceinline__ typename Frag<T>::type load_row(const T* p) {
+  return *(const typename Frag<T>::type*)p;
+}
+
+// First operand whose summed axis runs over LDS rows: this lane's column col0 + lane % 32 of rows
+// row0 + 4 h + 0..3 and row0 + 8 + 4 h + 0..3. bf16: the transposing LDS read, in which 16 lanes give
+// the addresses of a 4 x 16 block (4 values each) and get a column of 4 each (layout measured).
+template <int LD>
+__device__ __forceinline__ bf16x8v load_tr(const bf16_t* s, int row0, int col0) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  const int lane = lane_id();
+  const bf16_t* p = s + (row0 + 4 * (lane >> 5) + ((lane & 15) >> 2)) * LD + col0 + (lane & 16) + (lane & 3) * 4;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 8 * LD));
+  const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
+  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <int LD>
+__device__ __forceinline__ f32x8v load_tr(const float* s, int row0, int col0) {
+  const int lane = lane_id();
+  const float* p = s + (row0 + 4 * (lane >> 5)) * LD + col0 + (lane & 31);
+  f32x8v f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = p[((i & 3) + (i >> 2) * 8) * LD];
+  return f;
+}
+
+// Registers 8 m .. 8 m + 7 of a score tile as the second operand.
+__device__ __forceinline__ void to_frag(const f32x16& s, int m, bf16x8v& f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = (bf16_t)s[8 * m + i];
+}
+__device__ __forceinline__ void to_frag(const f32x16& s, int m, f32x8v& f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = s[8 * m + i];
+}
+
+// Row of register r within a 32-row result tile, for lane half h.
+__device__ __forceinline__ int reg_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
+
+// Row stride of an LDS tile of DP columns.
+template <typename T, int DP>
+constexpr int lds_ld() {
+  return DP + (sizeof(T) == 2 ? 8 : 4);
+}
+
+// Copies rows of [ROWS][DP] from global memory into an LDS tile of row stride LD in two steps: the
+// loads into registers, and the writes. Rows that `ok` rejects and columns from dim on are zero.
+template <typename T, int ROWS, int DP, int NT>
+struct Stage {
+  static constexpr int CG = DP / 8;                         // 8-value granules of a row
+  static constexpr int N = (ROWS * CG + NT - 1) / NT;       // granules of a thread
+  typename Frag<T>::type r[N];
+  template <typename Src>
+  __device__ __forceinline__ void load(Src src, int dim, bool vec) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * NT;
+      const int row = e / CG, col = (e % CG) * 8;
+      const T* p = (ROWS * CG) % NT == 0 || e < ROWS * CG ? src(row) : nullptr;
+      r[i] = load8<T>(p ? p + col : nullptr, p ? dim - col : 0, vec);
+    }
+  }
+  template <int LD>
+  __device__ __forceinline__ void store(T* s) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * NT;
+      if ((ROWS * CG) % NT == 0 || e < ROWS * CG) *(typename Frag<T>::type*)(s + (e / CG) * LD + (e % CG) * 8) = r[i];
+    }
+  }
+};
+
+// Stores a lane's 32-row result tile column (rows are consecutive values of the output row p, from
+// `first` on) scaled by f; only values below `dim` exist. vec: groups of 4 are aligned.
+template <typename T>
+__device__ __forceinline__ void store_col(T* p, int first, int dim, const f32x16& c, float f, bool vec) {
+  const int h = lane_id() >> 5;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int d = first + 8 * g + 4 * h;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = c[4 * g + i] * f;
+    if (vec && d + 4 <= dim) {
+      store_vec<T, 4>(p + d, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (d + i < dim) p[d + i] = (T)v[i];
+    }
+  }
+}
+
+}  // namespace igc

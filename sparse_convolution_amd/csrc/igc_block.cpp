@@ -1,5 +1,5 @@
-// extern "C" entry points of the operators between convolutions: layer norm and 8-bit activation
-// checkpoints. Every check runs on the host before any launch.
+// extern "C" entry points of the operators between convolutions: layer norm, 8-bit activation
+// checkpoints and cross attention. Every check runs on the host before any launch.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -61,9 +61,125 @@ int norm_backward(const NormArgs& a, int32_t wdtype, void* ws, size_t ws_bytes, 
   return launch_norm_bwd(a, ws, s);
 }
 
+bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+// Checks the problem's description and fills the device arguments (fn names the call).
+int attention_args(const char* fn, const igc_attention_t* p, AttnArgs& a) {
+  clear_error();
+  const std::string f(fn);
+  if (!p) return set_error(IGC_ERR_INVALID_ARG, f + ": the problem is null");
+  if (p->dtype != IGC_F32 && p->dtype != IGC_BF16) return set_error(IGC_ERR_INVALID_ARG, f + ": bad dtype");
+  if (p->n_q < 0 || p->n_k < 0) return set_error(IGC_ERR_INVALID_ARG, f + ": n_q or n_k is negative");
+  if (p->batch < 1 || p->heads < 1 || p->kv_heads < 1 || p->dim < 1)
+    return set_error(IGC_ERR_INVALID_ARG, f + ": batch, heads, kv_heads and dim must be positive");
+  if (p->heads % p->kv_heads)
+    return set_error(IGC_ERR_INVALID_ARG, f + ": heads must be a multiple of kv_heads");
+  if (p->dim > kAttnMaxDim)
+    return set_error(IGC_ERR_UNSUPPORTED, f + ": at most " + std::to_string(kAttnMaxDim) + " channels a head");
+  if (p->batch > 1 && (!p->d_q_offsets || !p->d_kv_offsets))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": several sequences need d_q_offsets and d_kv_offsets");
+  if (!(p->scale > 0.f) || std::isinf(p->scale))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": scale must be positive and finite");
+  const int64_t group = p->heads / p->kv_heads;
+  if (p->n_k > INT32_MAX || p->n_q > INT32_MAX / group)
+    return set_error(IGC_ERR_RANGE, f + ": n_q times heads per key head, and n_k, must stay below 2^31");
+  // Workgroups: at most 128 parts of each tile of 128 rows.
+  if ((p->n_q * group / 128 + p->batch) * p->kv_heads > INT32_MAX / 128 ||
+      (p->n_k / 128 + p->batch) * (int64_t)p->kv_heads > INT32_MAX / 128)
+    return set_error(IGC_ERR_RANGE, f + ": too many rows and heads for one launch");
+  a.fn = fn;
+  a.qo = p->d_q_offsets, a.ko = p->d_kv_offsets, a.mask = p->d_key_mask;
+  a.nq = p->n_q, a.nk = p->n_k;
+  for (int i = 0; i < 2; ++i) a.qs[i] = p->q_stride[i], a.ks[i] = p->k_stride[i], a.vs[i] = p->v_stride[i];
+  a.batch = p->batch, a.heads = p->heads, a.kv_heads = p->kv_heads, a.group = (int)group, a.dim = p->dim;
+  a.scale = p->scale;
+  return IGC_OK;
+}
+
+// Which operands may be read 16 bytes at a time.
+void attention_alignment(const igc_attention_t* p, AttnArgs& a, const void* dense) {
+  const int64_t e = p->dtype == IGC_BF16 ? 8 : 4;
+  const bool d = p->dim % 8 == 0;
+  a.qvec = d && aligned16(a.q) && a.qs[0] % e == 0 && a.qs[1] % e == 0;
+  a.kvec = d && aligned16(a.k) && aligned16(a.v) && a.ks[0] % e == 0 && a.ks[1] % e == 0 && a.vs[0] % e == 0 &&
+           a.vs[1] % e == 0;
+  a.ovec = d && aligned16(dense);
+}
+
+size_t forward_bytes(const AttnArgs& a) {
+  return a.splits > 1 ? (size_t)a.splits * a.nq * a.heads * (a.dim + 2) * sizeof(float) : 0;
+}
+
+int workspace_error(const char* fn, size_t need) {
+  return set_error(IGC_ERR_CAPACITY, std::string(fn) + ": needs " + std::to_string(need) +
+                                         " bytes of workspace (igc_cross_attention_workspace)");
+}
+
 }  // namespace
 
 extern "C" {
+
+int igc_cross_attention_workspace(const igc_attention_t* p, int32_t backward, size_t* bytes) {
+  const char* fn = "igc_cross_attention_workspace";
+  AttnArgs a;
+  const int rc = attention_args(fn, p, a);
+  if (rc) return rc;
+  if (!bytes) return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_workspace: bytes is null");
+  if (backward) {
+    *bytes = attn_bwd_plan(a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim).floats * sizeof(float);
+  } else {
+    a.splits = attn_fwd_splits(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
+    *bytes = forward_bytes(a);
+  }
+  return IGC_OK;
+}
+
+int igc_cross_attention(const igc_attention_t* p, const void* d_q, const void* d_k, const void* d_v, void* d_out,
+                        float* d_lse, void* d_ws, size_t ws_bytes, igc_stream stream) {
+  const char* fn = "igc_cross_attention";
+  AttnArgs a;
+  const int rc = attention_args(fn, p, a);
+  if (rc || a.nq == 0) return rc;
+  if (!d_q || !d_out || !d_lse || (a.nk > 0 && (!d_k || !d_v)))
+    return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention: d_q, d_k, d_v, d_out or d_lse is null");
+  if (d_out == d_q || (d_out == d_k && a.nk > 0) || (d_out == d_v && a.nk > 0))
+    return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention: d_out aliases an input");
+  a.q = d_q, a.k = d_k, a.v = d_v, a.out = d_out, a.lse = d_lse;
+  attention_alignment(p, a, d_out);
+  a.splits = attn_fwd_splits(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
+  const size_t need = forward_bytes(a);
+  if (need > 0 && (!d_ws || ws_bytes < need)) return workspace_error(fn, need);
+  a.part_a = (float*)d_ws;
+  a.part_b = a.part_a + (size_t)a.splits * a.nq * a.heads * a.dim;
+  return launch_attn_fwd(a, p->dtype, (hipStream_t)stream);
+}
+
+int igc_cross_attention_backward(const igc_attention_t* p, const void* d_q, const void* d_k, const void* d_v,
+                                 const void* d_out, const float* d_lse, const void* d_dout, void* d_dq, void* d_dk,
+                                 void* d_dv, void* d_ws, size_t ws_bytes, igc_stream stream) {
+  const char* fn = "igc_cross_attention_backward";
+  AttnArgs a;
+  const int rc = attention_args(fn, p, a);
+  if (rc) return rc;
+  if (!d_dk != !d_dv) return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_backward: d_dk and d_dv come together");
+  if ((!d_dq || a.nq == 0) && (!d_dk || a.nk == 0)) return IGC_OK;
+  if (a.nq > 0 && (!d_q || !d_out || !d_lse || !d_dout))
+    return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_backward: d_q, d_out, d_lse or d_dout is null");
+  if (a.nk > 0 && (!d_k || !d_v))
+    return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_backward: d_k or d_v is null");
+  const void* in[] = {d_q, d_k, d_v, d_out, d_dout};
+  for (const void* g : {(const void*)d_dq, (const void*)d_dk, (const void*)d_dv})
+    for (const void* x : in)
+      if (g && g == x) return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_backward: a gradient aliases an input");
+  a.q = d_q, a.k = d_k, a.v = d_v, a.out_in = d_out, a.lse_in = d_lse, a.dout = d_dout;
+  a.dq = d_dq, a.dk = d_dk, a.dv = d_dv;
+  attention_alignment(p, a, (const void*)((uintptr_t)d_out | (uintptr_t)d_dout | (uintptr_t)d_dq | (uintptr_t)d_dk |
+                                          (uintptr_t)d_dv));
+  const AttnBwdPlan plan = attn_bwd_plan(a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
+  const size_t need = plan.floats * sizeof(float);
+  if (need > 0 && (!d_ws || ws_bytes < need)) return workspace_error(fn, need);
+  return launch_attn_bwd(a, p->dtype, plan, d_ws, (hipStream_t)stream);
+}
 
 int igc_layer_norm(const void* d_x, int64_t n, int32_t c, int32_t dtype, const void* d_w, const void* d_b,
                    int32_t wdtype, float eps, void* d_y, float* d_mean, float* d_rstd, igc_stream stream) {

@@ -214,4 +214,33 @@ int launch_norm(const NormArgs& a, hipStream_t s);
 int norm_bwd_parts(int64_t n, int32_t c);
 int launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t s);
 
+// One attention problem on the device; strides in elements.
+struct AttnArgs {
+  const char* fn = "";
+  const void *q = nullptr, *k = nullptr, *v = nullptr, *dout = nullptr, *out_in = nullptr;
+  const float* lse_in = nullptr;
+  void *out = nullptr, *dq = nullptr, *dk = nullptr, *dv = nullptr;
+  float *lse = nullptr, *delta = nullptr;
+  float *part_a = nullptr, *part_b = nullptr;  // partial results of a split axis
+  const int32_t *qo = nullptr, *ko = nullptr;  // row offsets of the sequences (null: one sequence)
+  const uint8_t* mask = nullptr;               // [nk], 0 = key left out
+  int64_t nq = 0, nk = 0;
+  int64_t qs[2] = {0, 0}, ks[2] = {0, 0}, vs[2] = {0, 0};  // row and head strides
+  int batch = 1, heads = 1, kv_heads = 1, group = 1, dim = 0;
+  int splits = 1;
+  int qvec = 0, kvec = 0, ovec = 0;  // 16-byte loads of q, of k and v, of the dense outputs allowed
+  float scale = 1.f;
+};
+constexpr int32_t kAttnMaxDim = 128;
+// Parts the key axis is split into; the forward workspace holds splits * nq * heads * (dim + 2) floats
+// where there is more than one.
+int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim);
+int launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s);
+struct AttnBwdPlan {
+  int dq_splits = 1, dkv_splits = 1;
+  size_t floats = 0;  // workspace
+};
+AttnBwdPlan attn_bwd_plan(int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim);
+int launch_attn_bwd(const AttnArgs& a, int dtype, const AttnBwdPlan& p, void* ws, hipStream_t s);
+
 }  // namespace igc
