@@ -20,12 +20,13 @@ constexpr int kNT = 256;
 // Four waves of 32 NQ query rows each over tiles of BN keys. A row is a (query, head of the group
 // that shares the key head) pair, so few queries with shared key heads still fill a tile.
 // splits > 1: each workgroup takes one part of the sequence's keys and leaves an unnormalised result.
-template <typename T, int DP, int NQ, int BN>
-__global__ __launch_bounds__(kNT) void k_attn_fwd(AttnArgs a) {
+template <typename T, int DP, int NQ, int BN, int WPE, bool VEC>
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_fwd(AttnArgs a) {
   typedef typename Frag<T>::type frag;
   constexpr int LD = lds_ld<T, DP>();
   constexpr int BM = 128 * NQ;
   constexpr int KT = BN / 32, DT = DP / 32;
+  constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
   __shared__ __attribute__((aligned(16))) T s_k[2][BN * LD];
   __shared__ __attribute__((aligned(16))) T s_v[2][BN * LD];
 
@@ -44,24 +45,38 @@ __global__ __launch_bounds__(kNT) void k_attn_fwd(AttnArgs a) {
     k0 = k0 + split * part < k1 ? k0 + split * part : k1;
     k1 = k0 + part < k1 ? k0 + part : k1;
   }
+  int keys = (int)(k1 - k0);
+
+  Stage<T, BN, DP, kNT, VEC> sk, sv;
+  sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], a.ks[0], a.dim);
+  sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], a.vs[0], a.dim);
+  // Keys of the tile from k0 + j on that exist and that the mask keeps.
+  auto key_bits = [&](int j) -> uint64_t {
+    bool ok = lane < BN && j + lane < keys;
+    if (ok && a.mask) ok = a.mask[k0 + j + lane];
+    return __ballot(ok);
+  };
+  sk.load(keys, BN * a.ks[0]);
+  sv.load(keys, BN * a.vs[0]);
+  uint64_t next_bits = key_bits(0);
 
   // This lane's query rows (one per 32-column tile), and their values as second operands.
-  int64_t qi[NQ];
-  int head[NQ];
-  bool live[NQ];
+  int64_t row[NQ];  // row of out and lse, -1: none
   frag fq[NQ][DP / 16];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
-    live[n] = r < rows;
-    split_row(live[n] ? r : 0, a.group, qi[n], head[n]);
-    qi[n] += q0;
-    head[n] += kh * a.group;
-    const T* p = (const T*)a.q + qi[n] * a.qs[0] + head[n] * a.qs[1];
+    int64_t qi;
+    int head;
+    split_row(r < rows ? r : 0, a.group, qi, head);
+    qi += q0;
+    head += kh * a.group;
+    row[n] = r < rows ? qi * a.heads + head : -1;
+    const T* p = (const T*)a.q + qi * a.qs[0] + head * a.qs[1];
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
       const int d = kk * 16 + h * 8;
-      fq[n][kk] = load8<T>(p + d, live[n] ? a.dim - d : 0, a.qvec);
+      fq[n][kk] = load8<T>(p + d, r < rows ? a.dim - d : 0, VEC);
     }
   }
 
@@ -76,32 +91,20 @@ __global__ __launch_bounds__(kNT) void k_attn_fwd(AttnArgs a) {
     for (int t = 0; t < DT; ++t) o[n][t] = zero16();
   }
 
-  Stage<T, BN, DP, kNT> sk, sv;
-  const T* kp = (const T*)a.k + kh * a.ks[1];
-  const T* vp = (const T*)a.v + kh * a.vs[1];
-  auto fetch = [&](int64_t j0) {
-    auto row_ok = [&](int row) { return j0 + row < k1 && (!a.mask || a.mask[j0 + row]); };
-    sk.load([&](int row) { return row_ok(row) ? kp + (j0 + row) * a.ks[0] : nullptr; }, a.dim, a.kvec);
-    sv.load([&](int row) { return row_ok(row) ? vp + (j0 + row) * a.vs[0] : nullptr; }, a.dim, a.kvec);
-  };
-  auto key_bits = [&](int64_t j0) -> uint64_t {
-    const bool ok = lane < BN && j0 + lane < k1 && (!a.mask || a.mask[j0 + lane]);
-    return __ballot(ok);
-  };
-
-  uint64_t next_bits = 0;
-  if (k0 < k1) {
-    fetch(k0);
-    next_bits = key_bits(k0);
-  }
   int buf = 0;
-  for (int64_t j0 = k0; j0 < k1; j0 += BN, buf ^= 1) {
-    sk.template store<LD>(s_k[buf]);
-    sv.template store<LD>(s_v[buf]);
+  for (int j = 0; j < keys; j += BN, buf ^= 1) {
     const uint64_t bits = next_bits;
-    if (j0 + BN < k1) {
-      fetch(j0 + BN);
-      next_bits = key_bits(j0 + BN);
+    if (a.mask) {  // what a masked place holds must not meet a zero probability
+      sk.template store<LD>(s_k[buf], bits);
+      sv.template store<LD>(s_v[buf], bits);
+    } else {
+      sk.template store<LD>(s_k[buf]);
+      sv.template store<LD>(s_v[buf]);
+    }
+    if (j + BN < keys) {
+      sk.load(keys - j - BN, BN * a.ks[0]);
+      sv.load(keys - j - BN, BN * a.vs[0]);
+      next_bits = key_bits(j + BN);
     }
     // Two buffers: the barrier of the last tile already had every wave past reading this one.
     __syncthreads();
@@ -117,16 +120,16 @@ __global__ __launch_bounds__(kNT) void k_attn_fwd(AttnArgs a) {
         for (int n = 0; n < NQ; ++n) s[n][t] = mma(fk, fq[n][kk], s[n][t]);
       }
     }
-    if (bits != (BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1)) {
+    if (bits != kAll) {
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
         const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (!(w >> (8 * (r >> 2) + (r & 3)) & 1)) {
+        for (int r = 0; r < 16; ++r) {
+          const bool keep = w & (1u << (8 * (r >> 2) + (r & 3)));
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) s[n][t][r] = -INFINITY;
-          }
+          for (int n = 0; n < NQ; ++n) s[n][t][r] = keep ? s[n][t][r] : -INFINITY;
+        }
       }
     }
 #pragma unroll
@@ -175,23 +178,21 @@ __global__ __launch_bounds__(kNT) void k_attn_fwd(AttnArgs a) {
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const float total = l[n] + __shfl_xor(l[n], 32, 64);
-    if (!live[n]) continue;
-    const int64_t row = qi[n] * a.heads + head[n];
+    if (row[n] < 0) continue;
     if (a.splits > 1) {
-      float* po = a.part_a + ((int64_t)split * a.nq * a.heads + row) * a.dim;
+      const int64_t at = (int64_t)split * a.nq * a.heads + row[n];
 #pragma unroll
-      for (int d = 0; d < DT; ++d) store_col<float>(po, d * 32, a.dim, o[n][d], 1.f, a.dim % 4 == 0);
+      for (int d = 0; d < DT; ++d) store_col<float>(a.part_a + at * a.dim, d * 32, a.dim, o[n][d], 1.f, a.dim % 4 == 0);
       if (h == 0) {
-        float* ml = a.part_b + ((int64_t)split * a.nq * a.heads + row) * 2;
-        ml[0] = m[n];
-        ml[1] = total;
+        a.part_b[at * 2] = m[n];
+        a.part_b[at * 2 + 1] = total;
       }
     } else {
       const float f = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        store_col<T>((T*)a.out + row * a.dim, d * 32, a.dim, o[n][d], f, a.ovec);
-      if (h == 0) a.lse[row] = total == 0.f ? -INFINITY : kLn2 * (m[n] + log2f(total));
+        store_col<T>((T*)a.out + row[n] * a.dim, d * 32, a.dim, o[n][d], f, a.ovec);
+      if (h == 0) a.lse[row[n]] = total == 0.f ? -INFINITY : kLn2 * (m[n] + log2f(total));
     }
   }
 }
@@ -227,11 +228,11 @@ template <typename T, int DP>
 struct FwdShape;  // NQ, BN
 template <int DP>
 struct FwdShape<bf16_t, DP> {
-  static constexpr int NQ = DP <= 64 ? 2 : 1, BN = 64;
+  static constexpr int NQ = DP <= 64 ? 2 : 1, BN = 64, WPE = 2;
 };
 template <int DP>
 struct FwdShape<float, DP> {
-  static constexpr int NQ = 1, BN = 32;
+  static constexpr int NQ = 1, BN = 32, WPE = DP <= 64 ? 2 : 1;
 };
 
 int64_t fwd_slots(const AttnArgs& a, int bm) { return a.nq * a.group / bm + a.batch; }
@@ -243,7 +244,9 @@ template <typename T, int DP>
 void fwd_go(const AttnArgs& a, hipStream_t s) {
   constexpr int NQ = FwdShape<T, DP>::NQ, BN = FwdShape<T, DP>::BN;
   const int64_t wgs = fwd_slots(a, 128 * NQ) * a.kv_heads * a.splits;
-  k_attn_fwd<T, DP, NQ, BN><<<(unsigned)wgs, kNT, 0, s>>>(a);
+  constexpr int WPE = FwdShape<T, DP>::WPE;
+  if (a.qvec && a.kvec) k_attn_fwd<T, DP, NQ, BN, WPE, true><<<(unsigned)wgs, kNT, 0, s>>>(a);
+  else k_attn_fwd<T, DP, NQ, BN, WPE, false><<<(unsigned)wgs, kNT, 0, s>>>(a);
   if (a.splits > 1) k_attn_join<T><<<(unsigned)((a.nq * a.heads + kNT / 64 - 1) / (kNT / 64)), kNT, 0, s>>>(a);
 }
 

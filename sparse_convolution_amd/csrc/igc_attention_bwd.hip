@@ -24,12 +24,13 @@ constexpr int kNT = 256;
 __device__ __forceinline__ float lse_base2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
 // dq and delta: four waves of 32 query rows over tiles of BN keys (see k_attn_fwd for rows).
-template <typename T, int DP, int BN>
-__global__ __launch_bounds__(kNT) void k_attn_dq(AttnArgs a) {
+template <typename T, int DP, int BN, int WPE, bool VEC>
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dq(AttnArgs a) {
   typedef typename Frag<T>::type frag;
   constexpr int LD = lds_ld<T, DP>();
   constexpr int BM = 128;
   constexpr int KT = BN / 32, DT = DP / 32;
+  constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
   __shared__ __attribute__((aligned(16))) T s_k[2][BN * LD];
   __shared__ __attribute__((aligned(16))) T s_v[2][BN * LD];
 
@@ -65,9 +66,9 @@ __global__ __launch_bounds__(kNT) void k_attn_dq(AttnArgs a) {
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
       const int d = kk * 16 + h * 8, have = live ? a.dim - d : 0;
-      fq[kk] = load8<T>(p + d, have, a.qvec);
-      fo[kk] = load8<T>((const T*)a.dout + row * a.dim + d, have, a.ovec);
-      const frag f = load8<T>((const T*)a.out_in + row * a.dim + d, have, a.ovec);
+      fq[kk] = load8<T>(p + d, have, VEC);
+      fo[kk] = load8<T>((const T*)a.dout + row * a.dim + d, have, VEC);
+      const frag f = load8<T>((const T*)a.out_in + row * a.dim + d, have, VEC);
 #pragma unroll
       for (int i = 0; i < 8; ++i) delta = fmaf((float)fo[kk][i], (float)f[i], delta);
     }
@@ -80,31 +81,32 @@ __global__ __launch_bounds__(kNT) void k_attn_dq(AttnArgs a) {
 #pragma unroll
   for (int t = 0; t < DT; ++t) dq[t] = zero16();
 
-  Stage<T, BN, DP, kNT> sk, sv;
-  const T* kp = (const T*)a.k + kh * a.ks[1];
-  const T* vp = (const T*)a.v + kh * a.vs[1];
-  auto fetch = [&](int64_t j0) {
-    auto row_ok = [&](int x) { return j0 + x < k1 && (!a.mask || a.mask[j0 + x]); };
-    sk.load([&](int x) { return row_ok(x) ? kp + (j0 + x) * a.ks[0] : nullptr; }, a.dim, a.kvec);
-    sv.load([&](int x) { return row_ok(x) ? vp + (j0 + x) * a.vs[0] : nullptr; }, a.dim, a.kvec);
-  };
-  auto key_bits = [&](int64_t j0) -> uint64_t {
-    const bool ok = lane < BN && j0 + lane < k1 && (!a.mask || a.mask[j0 + lane]);
+  int keys = (int)(k1 - k0);
+  Stage<T, BN, DP, kNT, VEC> sk, sv;
+  sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], a.ks[0], a.dim);
+  sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], a.vs[0], a.dim);
+  auto key_bits = [&](int j) -> uint64_t {
+    bool ok = lane < BN && j + lane < keys;
+    if (ok && a.mask) ok = a.mask[k0 + j + lane];
     return __ballot(ok);
   };
-  uint64_t next_bits = 0;
-  if (k0 < k1) {
-    fetch(k0);
-    next_bits = key_bits(k0);
-  }
+  sk.load(keys, BN * a.ks[0]);
+  sv.load(keys, BN * a.vs[0]);
+  uint64_t next_bits = key_bits(0);
   int buf = 0;
-  for (int64_t j0 = k0; j0 < k1; j0 += BN, buf ^= 1) {
-    sk.template store<LD>(s_k[buf]);
-    sv.template store<LD>(s_v[buf]);
+  for (int j = 0; j < keys; j += BN, buf ^= 1) {
     const uint64_t bits = next_bits;
-    if (j0 + BN < k1) {
-      fetch(j0 + BN);
-      next_bits = key_bits(j0 + BN);
+    if (a.mask) {
+      sk.template store<LD>(s_k[buf], bits);
+      sv.template store<LD>(s_v[buf], bits);
+    } else {
+      sk.template store<LD>(s_k[buf]);
+      sv.template store<LD>(s_v[buf]);
+    }
+    if (j + BN < keys) {
+      sk.load(keys - j - BN, BN * a.ks[0]);
+      sv.load(keys - j - BN, BN * a.vs[0]);
+      next_bits = key_bits(j + BN);
     }
     __syncthreads();
 #pragma unroll
@@ -116,12 +118,12 @@ __global__ __launch_bounds__(kNT) void k_attn_dq(AttnArgs a) {
         s = mma(load_row<T>(&s_k[buf][at]), fq[kk], s);
         dp = mma(load_row<T>(&s_v[buf][at]), fo[kk], dp);
       }
-      const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float p = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse));
-        if (!(w >> (8 * (i >> 2) + (i & 3)) & 1)) p = 0.f;
-        s[i] = p * (dp[i] - delta);
+      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse)) * (dp[i] - delta);
+      if (bits != kAll) {
+        const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = w & (1u << (8 * (i >> 2) + (i & 3))) ? s[i] : 0.f;
       }
 #pragma unroll
       for (int mm = 0; mm < 2; ++mm) {
@@ -144,8 +146,8 @@ __global__ __launch_bounds__(kNT) void k_attn_dq(AttnArgs a) {
 }
 
 // dk and dv: four waves of 32 keys each over tiles of BQ query rows of the sequence.
-template <typename T, int DP, int BQ>
-__global__ __launch_bounds__(kNT) void k_attn_dkv(AttnArgs a) {
+template <typename T, int DP, int BQ, int WPE, bool VEC>
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
   typedef typename Frag<T>::type frag;
   constexpr int LD = lds_ld<T, DP>();
   constexpr int BM = 128;
@@ -177,50 +179,43 @@ __global__ __launch_bounds__(kNT) void k_attn_dkv(AttnArgs a) {
 #pragma unroll
   for (int kk = 0; kk < DP / 16; ++kk) {
     const int d = kk * 16 + h * 8, have = keep ? a.dim - d : 0;
-    fk[kk] = load8<T>((const T*)a.k + (keep ? j : 0) * a.ks[0] + kh * a.ks[1] + d, have, a.kvec);
-    fv[kk] = load8<T>((const T*)a.v + (keep ? j : 0) * a.vs[0] + kh * a.vs[1] + d, have, a.kvec);
+    fk[kk] = load8<T>((const T*)a.k + (keep ? j : 0) * a.ks[0] + kh * a.ks[1] + d, have, VEC);
+    fv[kk] = load8<T>((const T*)a.v + (keep ? j : 0) * a.vs[0] + kh * a.vs[1] + d, have, VEC);
   }
   const float c = a.scale * kLog2e;
   f32x16 dk[DT], dv[DT];
 #pragma unroll
   for (int t = 0; t < DT; ++t) dk[t] = zero16(), dv[t] = zero16();
 
-  Stage<T, BQ, DP, kNT> sq, so;
+  // Rows of the tile at t0 + x; with shared key heads a tile's rows step through the group's heads.
+  const int n_rows = (int)(r1 - r0);
+  StageRows<T, BQ, DP, kNT, VEC> sq, so;
+  sq.start((const T*)a.q + q0 * a.qs[0] + kh * a.group * a.qs[1], r0, a.group, a.qs[0], a.qs[1], a.dim);
+  so.start((const T*)a.dout + (q0 * a.heads + kh * a.group) * a.dim, r0, a.group, (int64_t)a.heads * a.dim, a.dim, a.dim);
   float n_lse = 0.f, n_delta = 0.f;
-  auto fetch = [&](int64_t t0) {
-    auto at = [&](int x, int64_t& qi, int& head) {
-      const int64_t r = t0 + x;
-      if (r >= r1) return false;
-      split_row(r, a.group, qi, head);
-      qi += q0;
-      head += kh * a.group;
-      return true;
-    };
-    sq.load([&](int x) -> const T* {
-      int64_t qi;
-      int head;
-      return at(x, qi, head) ? (const T*)a.q + qi * a.qs[0] + head * a.qs[1] : nullptr;
-    }, a.dim, a.qvec);
-    so.load([&](int x) -> const T* {
-      int64_t qi;
-      int head;
-      return at(x, qi, head) ? (const T*)a.dout + (qi * a.heads + head) * a.dim : nullptr;
-    }, a.dim, a.ovec);
+  auto fetch = [&](int t0) {
+    sq.load(n_rows - t0);
+    so.load(n_rows - t0);
     if (threadIdx.x < BQ) {
-      int64_t qi;
-      int head;
-      const bool ok = at(threadIdx.x, qi, head);
-      n_lse = lse_base2(ok ? a.lse_in[qi * a.heads + head] : -INFINITY);
-      n_delta = ok ? a.delta[qi * a.heads + head] : 0.f;
+      n_lse = INFINITY;
+      n_delta = 0.f;
+      if (t0 + (int)threadIdx.x < n_rows) {
+        int64_t qi;
+        int g;
+        split_row(r0 + t0 + threadIdx.x, a.group, qi, g);
+        const int64_t at = (q0 + qi) * a.heads + kh * a.group + g;
+        n_lse = lse_base2(a.lse_in[at]);
+        n_delta = a.delta[at];
+      }
     }
   };
-  if (r0 < r1) fetch(r0);
+  if (n_rows > 0) fetch(0);
   int buf = 0;
-  for (int64_t t0 = r0; t0 < r1; t0 += BQ, buf ^= 1) {
+  for (int t0 = 0; t0 < n_rows; t0 += BQ, buf ^= 1) {
     sq.template store<LD>(s_q[buf]);
     so.template store<LD>(s_o[buf]);
     if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = n_lse, s_delta[buf][threadIdx.x] = n_delta;
-    if (t0 + BQ < r1) fetch(t0 + BQ);
+    if (t0 + BQ < n_rows) fetch(t0 + BQ);
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
@@ -291,14 +286,17 @@ void sum_go(const float* part, int splits, int64_t n, void* out, hipStream_t s) 
 
 template <typename T, int DP>
 void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
-  constexpr int B = sizeof(T) == 2 ? 64 : 32;
+  constexpr int B = sizeof(T) == 2 ? 64 : 32, W = DP <= 64 ? 2 : 1;
+  const bool vec = a.qvec && a.kvec && a.ovec;
   a.delta = ws;
   ws += (a.nq * a.heads + 63) / 64 * 64;
   if (a.nq > 0) {
     AttnArgs d = a;
     d.splits = a.dq ? p.dq_splits : 1;
     d.part_a = ws;
-    k_attn_dq<T, DP, B><<<(unsigned)((a.nq * a.group / 128 + a.batch) * a.kv_heads * d.splits), kNT, 0, s>>>(d);
+    const unsigned wgs = (unsigned)((a.nq * a.group / 128 + a.batch) * a.kv_heads * d.splits);
+    if (vec) k_attn_dq<T, DP, B, W, true><<<wgs, kNT, 0, s>>>(d);
+    else k_attn_dq<T, DP, B, W, false><<<wgs, kNT, 0, s>>>(d);
     if (a.dq && d.splits > 1) sum_go<T>(ws, d.splits, a.nq * a.heads * a.dim, a.dq, s);
   }
   if (a.dk && a.nk > 0) {
@@ -306,7 +304,9 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     a.splits = p.dkv_splits;
     a.part_a = ws;
     a.part_b = ws + (p.dkv_splits > 1 ? p.dkv_splits * n : 0);
-    k_attn_dkv<T, DP, B><<<(unsigned)((a.nk / 128 + a.batch) * a.kv_heads * a.splits), kNT, 0, s>>>(a);
+    const unsigned wgs = (unsigned)((a.nk / 128 + a.batch) * a.kv_heads * a.splits);
+    if (vec) k_attn_dkv<T, DP, B, W, true><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_dkv<T, DP, B, W, false><<<wgs, kNT, 0, s>>>(a);
     if (a.splits > 1) {
       sum_go<T>(a.part_a, a.splits, n, a.dk, s);
       sum_go<T>(a.part_b, a.splits, n, a.dv, s);

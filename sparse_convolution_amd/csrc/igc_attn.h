@@ -91,12 +91,13 @@ __device__ __forceinline__ f32x16 zero16() {
   return z;
 }
 
-// 8 values at p; only the first `have` exist. vec: p is 16-byte aligned and all 8 or none exist.
+// 8 values at p; only the first `have` exist. vec: p is 16-byte aligned and 8 or none exist.
 template <typename T>
 __device__ __forceinline__ typename Frag<T>::type load8(const T* p, int have, bool vec) {
   typename Frag<T>::type f;
-  if (vec && have >= 8) {
-    f = *(const typename Frag<T>::type*)p;
+  if (vec) {
+    f = typename Frag<T>::type{};
+    if (have > 0) f = *(const typename Frag<T>::type*)p;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = i < have ? p[i] : (T)0.f;
@@ -152,30 +153,80 @@ constexpr int lds_ld() {
   return DP + (sizeof(T) == 2 ? 8 : 4);
 }
 
-// Copies rows of [ROWS][DP] from global memory into an LDS tile of row stride LD in two steps: the
-// loads into registers, and the writes. Rows that `ok` rejects and columns from dim on are zero.
-template <typename T, int ROWS, int DP, int NT>
+// Copies tiles of ROWS rows of an operand (row stride in elements; columns from dim on are zero) into an
+// LDS tile of row stride LD in two steps, so that the loads of the next tile are in flight while this one
+// is computed on: load() into registers, store() to LDS. Each thread keeps the addresses of its
+// 8-value granules and steps them from tile to tile. VEC: 16-byte loads are allowed and dim is a
+// multiple of 8.
+template <typename T, int ROWS, int DP, int NT, bool VEC>
 struct Stage {
-  static constexpr int CG = DP / 8;                         // 8-value granules of a row
-  static constexpr int N = (ROWS * CG + NT - 1) / NT;       // granules of a thread
+  static constexpr int CG = DP / 8;                    // granules of a row
+  static constexpr int N = (ROWS * CG + NT - 1) / NT;  // granules of a thread
   typename Frag<T>::type r[N];
-  template <typename Src>
-  __device__ __forceinline__ void load(Src src, int dim, bool vec) {
+  const T* p[N];
+  int dim;
+  static __device__ __forceinline__ bool mine(int i) {
+    return (ROWS * CG) % NT == 0 || (int)threadIdx.x + i * NT < ROWS * CG;
+  }
+  static __device__ __forceinline__ int row(int i) { return (threadIdx.x + i * NT) / CG; }
+  static __device__ __forceinline__ int col(int i) { return (threadIdx.x + i * NT) % CG * 8; }
+  // first: row 0 of the first tile.
+  __device__ __forceinline__ void start(const T* first, int64_t stride, int dim_) {
+    dim = dim_;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = first + row(i) * stride + col(i);
+  }
+  // Rows from `have` on are zero. step: elements to the next tile.
+  __device__ __forceinline__ void load(int have, int64_t step) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = threadIdx.x + i * NT;
-      const int row = e / CG, col = (e % CG) * 8;
-      const T* p = (ROWS * CG) % NT == 0 || e < ROWS * CG ? src(row) : nullptr;
-      r[i] = load8<T>(p ? p + col : nullptr, p ? dim - col : 0, vec);
+      r[i] = load8<T>(p[i], mine(i) && row(i) < have ? dim - col(i) : 0, VEC);
+      p[i] += step;
     }
+  }
+  // Rows whose bit in `keep` is off are written as zeros.
+  template <int LD>
+  __device__ __forceinline__ void store(T* s, uint64_t keep) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (mine(i)) {
+        typename Frag<T>::type f = r[i];
+        if (!(keep >> row(i) & 1)) f = typename Frag<T>::type{};
+        *(typename Frag<T>::type*)(s + row(i) * LD + col(i)) = f;
+      }
   }
   template <int LD>
   __device__ __forceinline__ void store(T* s) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = threadIdx.x + i * NT;
-      if ((ROWS * CG) % NT == 0 || e < ROWS * CG) *(typename Frag<T>::type*)(s + (e / CG) * LD + (e % CG) * 8) = r[i];
+    for (int i = 0; i < N; ++i)
+      if (mine(i)) *(typename Frag<T>::type*)(s + row(i) * LD + col(i)) = r[i];
+  }
+};
+
+// The same for query rows, which step through the heads of a group before the next query: row r0 + x
+// of the sequence is query (r0 + x) / group, head (r0 + x) % group.
+template <typename T, int ROWS, int DP, int NT, bool VEC>
+struct StageRows : Stage<T, ROWS, DP, NT, VEC> {
+  typedef Stage<T, ROWS, DP, NT, VEC> Base;
+  const T* base;
+  int64_t at, row_stride, head_stride;
+  int group;
+  __device__ __forceinline__ void start(const T* first, int64_t r0, int group_, int64_t rs, int64_t hs, int dim_) {
+    base = first, at = r0, group = group_, row_stride = rs, head_stride = hs;
+    this->dim = dim_;
+    if (group == 1) Base::start(first + r0 * rs, rs, dim_);
+  }
+  __device__ __forceinline__ void load(int have) {
+    if (group == 1) return Base::load(have, ROWS * row_stride);
+#pragma unroll
+    for (int i = 0; i < Base::N; ++i) {
+      int64_t query;
+      int g;
+      split_row(at + Base::row(i), group, query, g);
+      this->r[i] = load8<T>(base + query * row_stride + g * head_stride + Base::col(i),
+                            Base::mine(i) && Base::row(i) < have ? this->dim - Base::col(i) : 0, VEC);
     }
+    at += ROWS;
   }
 };
 
