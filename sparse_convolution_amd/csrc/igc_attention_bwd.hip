@@ -83,15 +83,15 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 
   int keys = (int)(k1 - k0);
   Stage<T, BN, DP, kNT, VEC> sk, sv;
-  sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], a.ks[0], a.dim);
-  sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], a.vs[0], a.dim);
+  sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], 0, a.ks[0], 0, 1, a.dim);
+  sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], 0, a.vs[0], 0, 1, a.dim);
   auto key_bits = [&](int j) -> uint64_t {
     bool ok = lane < BN && j + lane < keys;
     if (ok && a.mask) ok = a.mask[k0 + j + lane];
     return __ballot(ok);
   };
-  sk.load(keys, BN * a.ks[0]);
-  sv.load(keys, BN * a.vs[0]);
+  sk.load(keys);
+  sv.load(keys);
   uint64_t next_bits = key_bits(0);
   int buf = 0;
   for (int j = 0; j < keys; j += BN, buf ^= 1) {
@@ -104,8 +104,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       sv.template store<LD>(s_v[buf]);
     }
     if (j + BN < keys) {
-      sk.load(keys - j - BN, BN * a.ks[0]);
-      sv.load(keys - j - BN, BN * a.vs[0]);
+      sk.load(keys - j - BN);
+      sv.load(keys - j - BN);
       next_bits = key_bits(j + BN);
     }
     __syncthreads();
@@ -189,9 +189,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 
   // Rows of the tile at t0 + x; with shared key heads a tile's rows step through the group's heads.
   const int n_rows = (int)(r1 - r0);
-  StageRows<T, BQ, DP, kNT, VEC> sq, so;
-  sq.start((const T*)a.q + q0 * a.qs[0] + kh * a.group * a.qs[1], r0, a.group, a.qs[0], a.qs[1], a.dim);
-  so.start((const T*)a.dout + (q0 * a.heads + kh * a.group) * a.dim, r0, a.group, (int64_t)a.heads * a.dim, a.dim, a.dim);
+  Stage<T, BQ, DP, kNT, VEC> sq, so;
+  sq.start((const T*)a.q + q0 * a.qs[0] + kh * a.group * a.qs[1], r0, a.qs[0], a.qs[1], a.group, a.dim);
+  so.start((const T*)a.dout + (q0 * a.heads + kh * a.group) * a.dim, r0, (int64_t)a.heads * a.dim, a.dim, a.group, a.dim);
   float n_lse = 0.f, n_delta = 0.f;
   auto fetch = [&](int t0) {
     sq.load(n_rows - t0);

@@ -12,6 +12,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "igc_host.h"
 #include "igc_row.h"
 #include "igc_wave.h"
@@ -144,6 +146,25 @@ __device__ __forceinline__ void to_frag(const f32x16& s, int m, f32x8v& f) {
   for (int i = 0; i < 8; ++i) f[i] = s[8 * m + i];
 }
 
+// Largest of a tile's 16 registers. The three-way maximum as it is: from fmaxf the compiler first
+// passes every operand through a maximum with itself.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+__device__ __forceinline__ float max16(const f32x16& x) {
+  float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]), c = max3(x[6], x[7], x[8]), d = max3(x[9], x[10], x[11]);
+  a = max3(a, x[12], x[13]), b = max3(b, x[14], x[15]);
+  return max3(max3(a, b, c), d, d);
+}
+
+// Maximum over the two lanes that hold one column.
+__device__ __forceinline__ float halves_max(float x) {
+  const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+}
+
 // Row of register r within a 32-row result tile, for lane half h.
 __device__ __forceinline__ int reg_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
@@ -153,35 +174,69 @@ constexpr int lds_ld() {
   return DP + (sizeof(T) == 2 ? 8 : 4);
 }
 
-// Copies tiles of ROWS rows of an operand (row stride in elements; columns from dim on are zero) into an
-// LDS tile of row stride LD in two steps, so that the loads of the next tile are in flight while this one
-// is computed on: load() into registers, store() to LDS. Each thread keeps the addresses of its
-// 8-value granules and steps them from tile to tile. VEC: 16-byte loads are allowed and dim is a
-// multiple of 8.
+// Copies tiles of ROWS rows of an operand (columns from dim on are zero) into an LDS tile of row stride
+// LD in two steps, so that the loads of the next tile are in flight while this one is computed on: load()
+// into registers, store() to LDS. Rows of keys step by the row stride. Rows of queries (group > 1) step
+// through the heads that share a key head before the next query: row r is query r / group, head r % group.
+// The tile's address is uniform and each thread keeps the offsets of its 8-value granules from it, which
+// cost nothing per tile while ROWS is a multiple of group (the tile starts at a multiple of ROWS).
+// VEC: 16-byte loads are allowed, dim is a multiple of 8 and a tile spans less than 2 GiB.
 template <typename T, int ROWS, int DP, int NT, bool VEC>
 struct Stage {
   static constexpr int CG = DP / 8;                    // granules of a row
   static constexpr int N = (ROWS * CG + NT - 1) / NT;  // granules of a thread
+  typedef typename std::conditional<VEC, uint32_t, int64_t>::type Off;
   typename Frag<T>::type r[N];
-  const T* p[N];
-  int dim;
+  Off off[N];  // bytes
+  const char* base;
+  int64_t row_stride, head_stride, at;
+  int dim, group;
   static __device__ __forceinline__ bool mine(int i) {
     return (ROWS * CG) % NT == 0 || (int)threadIdx.x + i * NT < ROWS * CG;
   }
   static __device__ __forceinline__ int row(int i) { return (threadIdx.x + i * NT) / CG; }
   static __device__ __forceinline__ int col(int i) { return (threadIdx.x + i * NT) % CG * 8; }
-  // first: row 0 of the first tile.
-  __device__ __forceinline__ void start(const T* first, int64_t stride, int dim_) {
-    dim = dim_;
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = first + row(i) * stride + col(i);
-  }
-  // Rows from `have` on are zero. step: elements to the next tile.
-  __device__ __forceinline__ void load(int have, int64_t step) {
+  // first: row 0 of the sequence; the first tile starts at row r0 (a multiple of ROWS).
+  __device__ __forceinline__ void start(const T* first, int64_t r0, int64_t rs, int64_t hs, int group_, int dim_) {
+    row_stride = rs * (int64_t)sizeof(T), head_stride = hs * (int64_t)sizeof(T), group = group_, dim = dim_, at = r0;
+    int64_t q;
+    int g;
+    split_row(r0, group, q, g);
+    base = (const char*)first + q * row_stride;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      r[i] = load8<T>(p[i], mine(i) && row(i) < have ? dim - col(i) : 0, VEC);
-      p[i] += step;
+      int64_t q2;
+      int g2;
+      split_row(g + row(i), group, q2, g2);
+      off[i] = (Off)(q2 * row_stride + g2 * head_stride + col(i) * (int)sizeof(T));
+    }
+  }
+  // Loads the tile and steps to the next one. Rows from `have` on are zero.
+  __device__ __forceinline__ void load(int have) {
+    if (VEC && have >= ROWS && dim == DP && (ROWS * CG) % NT == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = *(const typename Frag<T>::type*)(base + off[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        r[i] = load8<T>((const T*)(base + off[i]), mine(i) && row(i) < have ? dim - col(i) : 0, VEC);
+    }
+    if (ROWS % group == 0) {
+      base += (int64_t)(ROWS / group) * row_stride;
+    } else {
+      int64_t q, q1;
+      int g, g1;
+      split_row(at, group, q, g);
+      split_row(at + ROWS, group, q1, g1);
+      at += ROWS;
+      base += (q1 - q) * row_stride;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        int64_t q2;
+        int g2;
+        split_row(g1 + row(i), group, q2, g2);
+        off[i] = (Off)(q2 * row_stride + g2 * head_stride + col(i) * (int)sizeof(T));
+      }
     }
   }
   // Rows whose bit in `keep` is off are written as zeros.
@@ -200,33 +255,6 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (mine(i)) *(typename Frag<T>::type*)(s + row(i) * LD + col(i)) = r[i];
-  }
-};
-
-// The same for query rows, which step through the heads of a group before the next query: row r0 + x
-// of the sequence is query (r0 + x) / group, head (r0 + x) % group.
-template <typename T, int ROWS, int DP, int NT, bool VEC>
-struct StageRows : Stage<T, ROWS, DP, NT, VEC> {
-  typedef Stage<T, ROWS, DP, NT, VEC> Base;
-  const T* base;
-  int64_t at, row_stride, head_stride;
-  int group;
-  __device__ __forceinline__ void start(const T* first, int64_t r0, int group_, int64_t rs, int64_t hs, int dim_) {
-    base = first, at = r0, group = group_, row_stride = rs, head_stride = hs;
-    this->dim = dim_;
-    if (group == 1) Base::start(first + r0 * rs, rs, dim_);
-  }
-  __device__ __forceinline__ void load(int have) {
-    if (group == 1) return Base::load(have, ROWS * row_stride);
-#pragma unroll
-    for (int i = 0; i < Base::N; ++i) {
-      int64_t query;
-      int g;
-      split_row(at + Base::row(i), group, query, g);
-      this->r[i] = load8<T>(base + query * row_stride + g * head_stride + Base::col(i),
-                            Base::mine(i) && Base::row(i) < have ? this->dim - Base::col(i) : 0, VEC);
-    }
-    at += ROWS;
   }
 };
 

@@ -100,10 +100,13 @@ int attention_args(const char* fn, const igc_attention_t* p, AttnArgs& a) {
 void attention_alignment(const igc_attention_t* p, AttnArgs& a, const void* dense) {
   const int64_t e = p->dtype == IGC_BF16 ? 8 : 4;
   const bool d = p->dim % 8 == 0;
-  a.qvec = d && aligned16(a.q) && a.qs[0] % e == 0 && a.qs[1] % e == 0;
-  a.kvec = d && aligned16(a.k) && aligned16(a.v) && a.ks[0] % e == 0 && a.ks[1] % e == 0 && a.vs[0] % e == 0 &&
-           a.vs[1] % e == 0;
-  a.ovec = d && aligned16(dense);
+  // A tile of at most 64 rows (and the group's heads) is addressed with 32-bit byte offsets from its start.
+  auto strides = [&](const int64_t* s) {
+    return s[0] % e == 0 && s[1] % e == 0 && s[0] >= 0 && s[1] >= 0 && s[0] < (1 << 22) && s[1] < (1 << 28) / a.group;
+  };
+  a.qvec = d && aligned16(a.q) && strides(a.qs);
+  a.kvec = d && aligned16(a.k) && aligned16(a.v) && strides(a.ks) && strides(a.vs);
+  a.ovec = d && aligned16(dense) && (int64_t)a.heads * a.dim < (1 << 22);
 }
 
 size_t forward_bytes(const AttnArgs& a) {
