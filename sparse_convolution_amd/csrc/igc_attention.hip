@@ -201,31 +201,195 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   }
 }
 
-// Joins the parts of a split key axis: one wave per row.
+// Few query rows per sequence and key head (single tokens): reading K and V once is all the time, and a
+// matrix tile would be mostly empty rows and its waves would wait on barriers. LPK lanes hold one key, 8
+// channels each, with a share of U keys in flight and as many being worked on; every group of LPK lanes keeps
+// its own running maximum, sum and output over its keys, and they are joined at the end (lanes, waves, then
+// k_attn_join for the parts of the key axis).
+template <typename T, int LPK, int R, bool VEC>
+__global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
+  typedef typename Frag<T>::type frag;
+  constexpr int U = 4, KPW = 64 / LPK, STEP = 4 * KPW * U;  // keys of a wave's round: KPW * U
+  __shared__ float s_o[4][R][LPK * 8 + 2];
+
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const int g = lane / LPK, d = (lane % LPK) * 8;
+  const int kh = blockIdx.x % a.kv_heads;
+  const int split = (blockIdx.x / a.kv_heads) % a.splits;
+  int b;
+  const int64_t tile = find_tile(a.qo, a.batch, a.nq, a.group, R, blockIdx.x / (a.kv_heads * a.splits), b);
+  int64_t q0, q1, k0, k1;
+  seq_rows(a.qo, b, a.nq, q0, q1);
+  seq_rows(a.ko, b, a.nk, k0, k1);
+  const int64_t rows = (q1 - q0) * a.group;
+  if (tile * R >= rows) return;
+  if (a.splits > 1) {
+    const int64_t part = (k1 - k0 + a.splits - 1) / a.splits;
+    k0 = k0 + split * part < k1 ? k0 + split * part : k1;
+    k1 = k0 + part < k1 ? k0 + part : k1;
+  }
+  const int keys = (int)(k1 - k0);
+  const T* kp = (const T*)a.k + kh * a.ks[1] + k0 * a.ks[0] + d;
+  const T* vp = (const T*)a.v + kh * a.vs[1] + k0 * a.vs[0] + d;
+  frag fk[U], fv[U];
+  uint32_t ok = 0;
+  auto fetch = [&](int j) {
+    ok = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = j + u * KPW + g;
+      const bool in = x < keys && (!a.mask || a.mask[k0 + x]);
+      fk[u] = load8<T>(kp + (int64_t)x * a.ks[0], in ? a.dim - d : 0, VEC);
+      fv[u] = load8<T>(vp + (int64_t)x * a.vs[0], in ? a.dim - d : 0, VEC);
+      ok |= (in ? 1u : 0u) << u;
+    }
+  };
+  fetch(wave * KPW * U);
+
+  float q[R][8], o[R][8], m[R], l[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t x = tile * R + r;
+    int64_t qi;
+    int head;
+    split_row(x < rows ? x : 0, a.group, qi, head);
+    const frag f = load8<T>((const T*)a.q + (q0 + qi) * a.qs[0] + (kh * a.group + head) * a.qs[1] + d,
+                            x < rows ? a.dim - d : 0, VEC);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      q[r][i] = (float)f[i] * (a.scale * kLog2e);
+      o[r][i] = 0.f;
+    }
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+  }
+  for (int j = wave * KPW * U; j < keys; j += STEP) {
+    float k[U][8], v[U][8];
+    const uint32_t now = ok;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k[u][i] = (float)fk[u][i], v[u][i] = (float)fv[u][i];
+    if (j + STEP < keys) fetch(j + STEP);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float s[U], top = m[r];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        s[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[u] = fmaf(q[r][i], k[u][i], s[u]);
+        s[u] = lanes_sum<LPK>(s[u]);
+        s[u] = now >> u & 1 ? s[u] : -INFINITY;
+        top = fmaxf(top, s[u]);
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+      const float f = __builtin_amdgcn_exp2f(m[r] - base);
+      m[r] = top;
+      l[r] *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[r][i] *= f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float p = __builtin_amdgcn_exp2f(s[u] - base);
+        l[r] += p;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[r][i] = fmaf(p, v[u][i], o[r][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float top = m[r];
+#pragma unroll
+    for (int x = LPK; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
+    const float f = __builtin_amdgcn_exp2f(m[r] - (top == -INFINITY ? 0.f : top));
+    l[r] *= f;
+#pragma unroll
+    for (int x = LPK; x < 64; x <<= 1) l[r] += __shfl_xor(l[r], x, 64);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[r][i] *= f;
+#pragma unroll
+      for (int x = LPK; x < 64; x <<= 1) o[r][i] += __shfl_xor(o[r][i], x, 64);
+      if (g == 0) s_o[wave][r][d + i] = o[r][i];
+    }
+    if (lane == 0) s_o[wave][r][LPK * 8] = top, s_o[wave][r][LPK * 8 + 1] = l[r];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < R * LPK * 8; e += kNT) {
+    const int r = e / (LPK * 8), c = e % (LPK * 8);
+    const int64_t x = tile * R + r;
+    if (x >= rows || c >= a.dim) continue;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, s_o[w][r][LPK * 8]);
+    float total = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = __builtin_amdgcn_exp2f(s_o[w][r][LPK * 8] - (top == -INFINITY ? 0.f : top));
+      total += f * s_o[w][r][LPK * 8 + 1];
+      sum += f * s_o[w][r][c];
+    }
+    int64_t qi;
+    int head;
+    split_row(x, a.group, qi, head);
+    const int64_t row = (q0 + qi) * a.heads + kh * a.group + head;
+    if (a.splits > 1) {
+      const int64_t at = (int64_t)split * a.nq * a.heads + row;
+      a.part_a[at * a.dim + c] = sum;
+      if (c == 0) a.part_b[at * 2] = top, a.part_b[at * 2 + 1] = total;
+    } else {
+      const float f = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;
+      ((T*)a.out)[row * a.dim + c] = (T)(sum * f);
+      if (c == 0) a.lse[row] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
+    }
+  }
+}
+
+constexpr int kMaxParts = 128;
+
+// Joins the parts of a split key axis, one workgroup per row: a lane per part weighs it, then the waves
+// share the parts and the lanes the channels.
 template <typename T>
 __global__ __launch_bounds__(kNT) void k_attn_join(AttnArgs a) {
-  const int lane = lane_id();
-  const int64_t rows = a.nq * a.heads;
-  const int64_t row = (int64_t)blockIdx.x * (kNT / 64) + (threadIdx.x >> 6);
-  if (row >= rows) return;
-  float top = -INFINITY;
-  for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, a.part_b[((int64_t)s * rows + row) * 2]);
-  top = lanes_reduce<64>(top, [](float x, float y) { return fmaxf(x, y); });
-  const float base = top == -INFINITY ? 0.f : top;
-  float total = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const int64_t at = (int64_t)s * rows + row;
-    const float f = __builtin_amdgcn_exp2f(a.part_b[at * 2] - base);
-    total += f * a.part_b[at * 2 + 1];
-    const float* po = a.part_a + at * a.dim;
-    if (lane < a.dim) o0 += f * po[lane];
-    if (lane + 64 < a.dim) o1 += f * po[lane + 64];
+  __shared__ float s_w[kMaxParts], s_o[4][kAttnMaxDim];
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const int64_t rows = a.nq * a.heads, row = blockIdx.x;
+  float m[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int part = lane + 64 * i;
+    const float2 ml = part < a.splits ? ((const float2*)a.part_b)[part * rows + row] : make_float2(-INFINITY, 0.f);
+    m[i] = ml.x;
+    l[i] = ml.y;
   }
+  const float top = lanes_reduce<64>(fmaxf(m[0], m[1]), [](float x, float y) { return fmaxf(x, y); });
+  const float base = top == -INFINITY ? 0.f : top;
+  float total = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float w = __builtin_amdgcn_exp2f(m[i] - base);
+    total += w * l[i];
+    if (wave == 0) s_w[lane + 64 * i] = w;
+  }
+  total = lanes_sum<64>(total);
+  __syncthreads();
+  const float* po = a.part_a + row * a.dim;
+  float o0 = 0.f, o1 = 0.f;
+#pragma unroll 8
+  for (int part = wave; part < a.splits; part += 4) {
+    const float* p = po + part * rows * a.dim;
+    if (lane < a.dim) o0 += s_w[part] * p[lane];
+    if (lane + 64 < a.dim) o1 += s_w[part] * p[lane + 64];
+  }
+  s_o[wave][lane] = o0;
+  s_o[wave][lane + 64] = o1;
+  __syncthreads();
   const float f = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;
-  T* out = (T*)a.out + row * a.dim;
-  if (lane < a.dim) out[lane] = (T)(o0 * f);
-  if (lane + 64 < a.dim) out[lane + 64] = (T)(o1 * f);
-  if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
+  for (int c = threadIdx.x; c < a.dim; c += kNT)
+    ((T*)a.out)[row * a.dim + c] = (T)(((s_o[0][c] + s_o[1][c]) + (s_o[2][c] + s_o[3][c])) * f);
+  if (threadIdx.x == 0) a.lse[row] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
 }
 
 template <typename T, int DP>
@@ -239,44 +403,77 @@ struct FwdShape<float, DP> {
   static constexpr int NQ = 1, BN = 32, WPE = DP <= 64 ? 2 : 1;
 };
 
-int64_t fwd_slots(const AttnArgs& a, int bm) { return a.nq * a.group / bm + a.batch; }
+constexpr int kFewRows = 4;
 
-// Row tiles of the forward kernel for this problem.
-int fwd_bm(int dtype, int dim) { return dtype == IGC_BF16 && dim <= 64 ? 256 : 128; }
-
-template <typename T, int DP>
-void fwd_go(const AttnArgs& a, hipStream_t s) {
-  constexpr int NQ = FwdShape<T, DP>::NQ, BN = FwdShape<T, DP>::BN;
-  const int64_t wgs = fwd_slots(a, 128 * NQ) * a.kv_heads * a.splits;
-  constexpr int WPE = FwdShape<T, DP>::WPE;
-  if (a.qvec && a.kvec) k_attn_fwd<T, DP, NQ, BN, WPE, true><<<(unsigned)wgs, kNT, 0, s>>>(a);
-  else k_attn_fwd<T, DP, NQ, BN, WPE, false><<<(unsigned)wgs, kNT, 0, s>>>(a);
-  if (a.splits > 1) k_attn_join<T><<<(unsigned)((a.nq * a.heads + kNT / 64 - 1) / (kNT / 64)), kNT, 0, s>>>(a);
+// Query rows of a tile: a few (k_attn_few) or those of the matrix kernel. Decided from the average number of rows
+// that share a key head in a sequence; either kernel takes any number of rows. Measured, bf16, few / matrix: 64 x 4096
+// keys, 8 key heads of 64, 1, 2, 4 and 8 rows 115 / 192, 117 / 188, 125 / 186 and 184 / 101 us; 100,000 keys, 8 heads of
+// 128, 1 row 99 / 93, 4 rows 103 / 91; 32 x 2048 keys, 2 heads of 128, 4 rows 36 / 23.
+int fwd_rows(int dtype, int dim, int64_t nq, int batch, int group) {
+  const int64_t rows = (nq + batch - 1) / batch * group;
+  for (int r = 1; r <= (dim <= 64 ? kFewRows : 2); r *= 2)
+    if (rows <= r) return r;
+  return dtype == IGC_BF16 && dim <= 64 ? 256 : 128;
 }
 
 template <typename T>
-void fwd_t(const AttnArgs& a, hipStream_t s) {
-  if (a.dim <= 32) return fwd_go<T, 32>(a, s);
-  if (a.dim <= 64) return fwd_go<T, 64>(a, s);
-  if (a.dim <= 96) return fwd_go<T, 96>(a, s);
-  fwd_go<T, 128>(a, s);
+void join(const AttnArgs& a, hipStream_t s) {
+  if (a.splits > 1) k_attn_join<T><<<(unsigned)(a.nq * a.heads), kNT, 0, s>>>(a);
+}
+
+template <typename T, int DP>
+void fwd_go(const AttnArgs& a, unsigned wgs, hipStream_t s) {
+  constexpr int NQ = FwdShape<T, DP>::NQ, BN = FwdShape<T, DP>::BN, WPE = FwdShape<T, DP>::WPE;
+  if (a.qvec && a.kvec) k_attn_fwd<T, DP, NQ, BN, WPE, true><<<wgs, kNT, 0, s>>>(a);
+  else k_attn_fwd<T, DP, NQ, BN, WPE, false><<<wgs, kNT, 0, s>>>(a);
+}
+
+template <typename T, int LPK, int R>
+void few_go(const AttnArgs& a, unsigned wgs, hipStream_t s) {
+  if (a.qvec && a.kvec) k_attn_few<T, LPK, R, true><<<wgs, kNT, 0, s>>>(a);
+  else k_attn_few<T, LPK, R, false><<<wgs, kNT, 0, s>>>(a);
+}
+template <typename T, int LPK>
+void few_r(const AttnArgs& a, int rows, unsigned wgs, hipStream_t s) {
+  if (rows == 1) return few_go<T, LPK, 1>(a, wgs, s);
+  if (rows == 2) return few_go<T, LPK, 2>(a, wgs, s);
+  few_go<T, LPK, 4>(a, wgs, s);
+}
+
+template <typename T>
+void fwd_t(const AttnArgs& a, int dtype, hipStream_t s) {
+  const int rows = fwd_rows(dtype, a.dim, a.nq, a.batch, a.group);
+  const unsigned wgs = (unsigned)((a.nq * a.group / rows + a.batch) * a.kv_heads * a.splits);
+  if (rows <= kFewRows) {
+    if (a.dim <= 32) few_r<T, 4>(a, rows, wgs, s);
+    else if (a.dim <= 64) few_r<T, 8>(a, rows, wgs, s);
+    else if (rows == 1) few_go<T, 16, 1>(a, wgs, s);
+    else few_go<T, 16, 2>(a, wgs, s);
+  } else {
+    if (a.dim <= 32) fwd_go<T, 32>(a, wgs, s);
+    else if (a.dim <= 64) fwd_go<T, 64>(a, wgs, s);
+    else if (a.dim <= 96) fwd_go<T, 96>(a, wgs, s);
+    else fwd_go<T, 128>(a, wgs, s);
+  }
+  join<T>(a, s);
 }
 
 }  // namespace
 
 int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim) {
-  // Parts of the key axis: none while the query tiles alone fill the GPU twice over, else enough for
-  // that, each of at least 256 keys.
-  const int bm = fwd_bm(dtype, dim);
-  const int64_t per_seq = (nq / batch) * (heads / kv_heads);
+  // Parts of the key axis: none while the query tiles alone fill the GPU, else enough for that, each of
+  // at least 256 keys.
+  const int bm = fwd_rows(dtype, dim, nq, batch, heads / kv_heads);
+  const int64_t per_seq = (nq + batch - 1) / batch * (heads / kv_heads);
   const int64_t wgs = batch * ((per_seq + bm - 1) / bm) * kv_heads;
-  const int64_t want = wgs >= 512 ? 1 : 512 / std::max<int64_t>(1, wgs);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 128), nk / batch / 256));
+  const int64_t fill = bm <= kFewRows ? 2048 : 512;
+  const int64_t want = wgs >= fill ? 1 : fill / std::max<int64_t>(1, wgs);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxParts), nk / batch / 256));
 }
 
 int launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s) {
-  if (dtype == IGC_BF16) fwd_t<bf16_t>(a, s);
-  else fwd_t<float>(a, s);
+  if (dtype == IGC_BF16) fwd_t<bf16_t>(a, dtype, s);
+  else fwd_t<float>(a, dtype, s);
   IGC_HIP(hipGetLastError(), a.fn);
   return IGC_OK;
 }

@@ -2,6 +2,7 @@
 // checkpoints and cross attention. Every check runs on the host before any launch.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -83,8 +84,8 @@ int attention_args(const char* fn, const igc_attention_t* p, AttnArgs& a) {
   const int64_t group = p->heads / p->kv_heads;
   if (p->n_k > INT32_MAX || p->n_q > INT32_MAX / group)
     return set_error(IGC_ERR_RANGE, f + ": n_q times heads per key head, and n_k, must stay below 2^31");
-  // Workgroups: at most 128 parts of each tile of 128 rows.
-  if ((p->n_q * group / 128 + p->batch) * p->kv_heads > INT32_MAX / 128 ||
+  // Workgroups: at most 128 parts of each tile (of 128 rows, or of a few where sequences have only those).
+  if ((std::min(p->n_q * group / 128, INT64_C(1) << 31) + (int64_t)p->batch * 9) * p->kv_heads > INT32_MAX / 128 ||
       (p->n_k / 128 + p->batch) * (int64_t)p->kv_heads > INT32_MAX / 128)
     return set_error(IGC_ERR_RANGE, f + ": too many rows and heads for one launch");
   a.fn = fn;

@@ -201,6 +201,30 @@ def test_large_scores_and_given_scale(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [1, 2, 70])
+@pytest.mark.parametrize("step,first", [(3.0, 0.0), (40.0, 0.0), (-5.0, 0.0), (400.0, -200.0)])
+def test_scores_that_grow_or_fall_along_the_keys(step, first, rows, dtype):
+    # Scores first + step * (block of 50 keys) + noise, up to several thousand: the running reference must follow them,
+    # within a tile and from one to the next. q has one channel of 1 and keys carry the ramp there, so the ramp is exact
+    # in bf16 (multiples of the step below 2^8 steps); the rest are small values. The ramp's fp32 rounding in exp's
+    # argument is up to 2^-22 of the largest score, 1e-3 here: rows are compared at 4e-3 of the largest value.
+    igc = _igc()
+    n, d = 400, 32
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn(rows, 1, d, generator=g)
+    k = torch.randn(n, 1, d, generator=g)
+    v = torch.randn(n, 1, d, generator=g)
+    q[:, :, 0] = 1.0
+    k[:, 0, 0] = (first + step * (torch.arange(n) // 50)).to(BF16).float()
+    q, k, v = [t.to(dtype).cuda() for t in (q, k, v)]
+    out, lse = igc.cross_attention(q, k, v, scale=1.0)
+    s = q[:, 0].double().cpu() @ k[:, 0].double().cpu().T
+    ref = torch.softmax(s, 1) @ v[:, 0].double().cpu()
+    assert bool(((lse[:, 0].double().cpu() - torch.logsumexp(s, 1)).abs() <= 1e-3 + 2.0 ** -22 * s.abs().max()).all())
+    assert bool(((out[:, 0].double().cpu() - ref).abs() <= (4e-3 + 2 * U[dtype]) * v.double().abs().max().cpu()).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_nan_and_infinite_queries_stay_in_their_rows(dtype):
     igc = _igc()
     for lq, lk in (([150], [90]), ([2], [900])):
