@@ -27,13 +27,13 @@ constexpr float kSlack = 8.f;
 // splits > 1: each workgroup takes one part of the sequence's keys and leaves an unnormalised result.
 template <typename T, int DP, int NQ, int BN, int WPE, bool VEC>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_fwd(AttnArgs a) {
-  typedef typename Frag<T>::type frag;
-  constexpr int LD = lds_ld<T, DP>();
+  typedef Frag<T> frag;
+  constexpr int LD = lds_ld<DP>(), PS = BN * LD;
   constexpr int BM = 128 * NQ;
   constexpr int KT = BN / 32, DT = DP / 32;
   constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
-  __shared__ __attribute__((aligned(16))) T s_k[2][BN * LD];
-  __shared__ __attribute__((aligned(16))) T s_v[2][BN * LD];
+  __shared__ __attribute__((aligned(16))) bf16_t s_k[2][kParts<T> * PS];
+  __shared__ __attribute__((aligned(16))) bf16_t s_v[2][kParts<T> * PS];
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
   const int kh = blockIdx.x % a.kv_heads;
@@ -81,13 +81,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
       const int d = kk * 16 + h * 8;
-      fq[n][kk] = load8<T>(p + d, r < rows ? a.dim - d : 0, VEC);
+      fq[n][kk] = to_parts(load8<T>(p + d, r < rows ? a.dim - d : 0, VEC));
     }
   }
 
-  const float c = a.scale * kLog2e;
+  const float c = a.scale * kLog2e, slack = kSlack / c;
   f32x16 o[NQ][DT];
-  float m[NQ], l[NQ];
+  float m[NQ], l[NQ];  // references (in the scores' units) and this lane's part of the sums
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     m[n] = -INFINITY;
@@ -100,11 +100,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   for (int j = 0; j < keys; j += BN, buf ^= 1) {
     const uint64_t bits = next_bits;
     if (a.mask) {  // what a masked place holds must not meet a zero probability
-      sk.template store<LD>(s_k[buf], bits);
-      sv.template store<LD>(s_v[buf], bits);
+      sk.template store<LD, PS>(s_k[buf], bits);
+      sv.template store<LD, PS>(s_v[buf], bits);
     } else {
-      sk.template store<LD>(s_k[buf]);
-      sv.template store<LD>(s_v[buf]);
+      sk.template store<LD, PS>(s_k[buf]);
+      sv.template store<LD, PS>(s_v[buf]);
     }
     if (j + BN < keys) {
       sk.load(keys - j - BN);
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       for (int n = 0; n < NQ; ++n) s[n][t] = zero16();
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
-        const frag fk = load_row<T>(&s_k[buf][(t * 32 + (lane & 31)) * LD + kk * 16 + h * 8]);
+        const frag fk = load_row<T, PS>(&s_k[buf][(t * 32 + (lane & 31)) * LD + kk * 16 + h * 8]);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) s[n][t] = mma(fk, fq[n][kk], s[n][t]);
       }
@@ -142,11 +142,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       float top = max16(s[n][0]);
 #pragma unroll
       for (int t = 1; t < KT; ++t) top = fmaxf(top, max16(s[n][t]));
-      top = halves_max(top) * c;
-      const float m_new = fmaxf(m[n], top);
-      if (__any(m_new > m[n] + kSlack)) {
+      const float m_new = fmaxf(m[n], halves_max(top));
+      if (__any(m_new > m[n] + slack)) {
         asm volatile("");  // a branch: the compiler would multiply always and select
-        const float f = m[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[n] - m_new);
+        const float f = m[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[n] - m_new) * c);
         l[n] *= f;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
@@ -159,7 +158,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          s[n][t][r] = __builtin_amdgcn_exp2f(fmaf(s[n][t][r], c, -base));
+          // bf16 data: one instruction. fp32: the difference first, which is exact near the reference.
+          s[n][t][r] = __builtin_amdgcn_exp2f(sizeof(T) == 2 ? fmaf(s[n][t][r], c, -base * c) : (s[n][t][r] - base) * c);
           l[n] += s[n][t][r];
         }
     }
@@ -169,10 +169,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       for (int mm = 0; mm < 2; ++mm) {
         frag p[NQ];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) to_frag(s[n][t], mm, p[n]);
+        for (int n = 0; n < NQ; ++n) p[n] = to_frag<T>(s[n][t], mm);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const frag fv = load_tr<LD>(s_v[buf], t * 32 + mm * 16, d * 32);
+          const frag fv = load_tr<T, LD, PS>(s_v[buf], t * 32 + mm * 16, d * 32);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) o[n][d] = mma(fv, p[n], o[n][d]);
         }
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
       for (int d = 0; d < DT; ++d) store_col<float>(a.part_a + at * a.dim, d * 32, a.dim, o[n][d], 1.f, a.dim % 4 == 0);
       if (h == 0) {
-        a.part_b[at * 2] = m[n];
+        a.part_b[at * 2] = m[n] * c;
         a.part_b[at * 2 + 1] = total;
       }
     } else {
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
       for (int d = 0; d < DT; ++d)
         store_col<T>((T*)a.out + row[n] * a.dim, d * 32, a.dim, o[n][d], f, a.ovec);
-      if (h == 0) a.lse[row[n]] = total == 0.f ? -INFINITY : kLn2 * (m[n] + log2f(total));
+      if (h == 0) a.lse[row[n]] = total == 0.f ? -INFINITY : kLn2 * (m[n] * c + log2f(total));
     }
   }
 }
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 // k_attn_join for the parts of the key axis).
 template <typename T, int LPK, int R, bool VEC>
 __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
-  typedef typename Frag<T>::type frag;
+  typedef typename Raw8<T>::type frag;
   constexpr int U = 4, KPW = 64 / LPK, STEP = 4 * KPW * U;  // keys of a wave's round: KPW * U
   __shared__ float s_o[4][R][LPK * 8 + 2];
 

@@ -23,16 +23,16 @@ constexpr int kNT = 256;
 // lse in base 2; +infinity for rows without keys, whose probabilities are then exp2(-infinity) = 0.
 __device__ __forceinline__ float lse_base2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-// dq and delta: four waves of 32 query rows over tiles of BN keys (see k_attn_fwd for rows).
-template <typename T, int DP, int BN, int WPE, bool VEC>
+// dq and delta: four waves of 32 NQ query rows over tiles of BN keys (see k_attn_fwd for rows).
+template <typename T, int DP, int NQ, int BN, int WPE, bool VEC>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dq(AttnArgs a) {
-  typedef typename Frag<T>::type frag;
-  constexpr int LD = lds_ld<T, DP>();
-  constexpr int BM = 128;
+  typedef Frag<T> frag;
+  constexpr int LD = lds_ld<DP>(), PS = BN * LD;
+  constexpr int BM = 128 * NQ;
   constexpr int KT = BN / 32, DT = DP / 32;
   constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
-  __shared__ __attribute__((aligned(16))) T s_k[2][BN * LD];
-  __shared__ __attribute__((aligned(16))) T s_v[2][BN * LD];
+  __shared__ __attribute__((aligned(16))) bf16_t s_k[2][kParts<T> * PS];
+  __shared__ __attribute__((aligned(16))) bf16_t s_v[2][kParts<T> * PS];
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
   const int kh = blockIdx.x % a.kv_heads;
@@ -50,38 +50,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     k0 = k0 + split * part < k1 ? k0 + split * part : k1;
     k1 = k0 + part < k1 ? k0 + part : k1;
   }
-
-  const int64_t r = tile * BM + wave * 32 + (lane & 31);
-  const bool live = r < rows;
-  int64_t qi;
-  int head;
-  split_row(live ? r : 0, a.group, qi, head);
-  qi += q0;
-  head += kh * a.group;
-  const int64_t row = qi * a.heads + head;
-  frag fq[DP / 16], fo[DP / 16];
-  float delta = 0.f;
-  {
-    const T* p = (const T*)a.q + qi * a.qs[0] + head * a.qs[1];
-#pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) {
-      const int d = kk * 16 + h * 8, have = live ? a.dim - d : 0;
-      fq[kk] = load8<T>(p + d, have, VEC);
-      fo[kk] = load8<T>((const T*)a.dout + row * a.dim + d, have, VEC);
-      const frag f = load8<T>((const T*)a.out_in + row * a.dim + d, have, VEC);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) delta = fmaf((float)fo[kk][i], (float)f[i], delta);
-    }
-    delta += __shfl_xor(delta, 32, 64);
-    if (live && h == 0 && split == 0) a.delta[row] = delta;
-  }
-  const float lse = lse_base2(live ? a.lse_in[row] : -INFINITY);
-  const float c = a.scale * kLog2e;
-  f32x16 dq[DT];
-#pragma unroll
-  for (int t = 0; t < DT; ++t) dq[t] = zero16();
-
-  int keys = (int)(k1 - k0);
+  const int keys = (int)(k1 - k0);
   Stage<T, BN, DP, kNT, VEC> sk, sv;
   sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], 0, a.ks[0], 0, 1, a.dim);
   sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], 0, a.vs[0], 0, 1, a.dim);
@@ -93,15 +62,52 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   sk.load(keys);
   sv.load(keys);
   uint64_t next_bits = key_bits(0);
+
+  int64_t row[NQ];  // row of out and lse, -1: none
+  frag fq[NQ][DP / 16], fo[NQ][DP / 16];
+  float delta[NQ], lse[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
+    int64_t qi;
+    int head;
+    split_row(r < rows ? r : 0, a.group, qi, head);
+    qi += q0;
+    head += kh * a.group;
+    const int64_t at = qi * a.heads + head;
+    row[n] = r < rows ? at : -1;
+    const T* p = (const T*)a.q + qi * a.qs[0] + head * a.qs[1];
+    delta[n] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+      const int d = kk * 16 + h * 8, have = r < rows ? a.dim - d : 0;
+      fq[n][kk] = to_parts(load8<T>(p + d, have, VEC));
+      const auto g = load8<T>((const T*)a.dout + at * a.dim + d, have, VEC);
+      const auto f = load8<T>((const T*)a.out_in + at * a.dim + d, have, VEC);
+      fo[n][kk] = to_parts(g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) delta[n] = fmaf((float)g[i], (float)f[i], delta[n]);
+    }
+    delta[n] += __shfl_xor(delta[n], 32, 64);
+    if (row[n] >= 0 && h == 0 && split == 0) a.delta[row[n]] = delta[n];
+    lse[n] = lse_base2(row[n] >= 0 ? a.lse_in[row[n]] : -INFINITY);
+  }
+  const float c = a.scale * kLog2e;
+  f32x16 dq[NQ][DT];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+    for (int t = 0; t < DT; ++t) dq[n][t] = zero16();
+
   int buf = 0;
   for (int j = 0; j < keys; j += BN, buf ^= 1) {
     const uint64_t bits = next_bits;
     if (a.mask) {
-      sk.template store<LD>(s_k[buf], bits);
-      sv.template store<LD>(s_v[buf], bits);
+      sk.template store<LD, PS>(s_k[buf], bits);
+      sv.template store<LD, PS>(s_v[buf], bits);
     } else {
-      sk.template store<LD>(s_k[buf]);
-      sv.template store<LD>(s_v[buf]);
+      sk.template store<LD, PS>(s_k[buf]);
+      sv.template store<LD, PS>(s_v[buf]);
     }
     if (j + BN < keys) {
       sk.load(keys - j - BN);
@@ -111,49 +117,71 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      f32x16 s = zero16(), dp = zero16();
+      f32x16 s[NQ], dp[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) s[n] = zero16(), dp[n] = zero16();
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
         const int at = (t * 32 + (lane & 31)) * LD + kk * 16 + h * 8;
-        s = mma(load_row<T>(&s_k[buf][at]), fq[kk], s);
-        dp = mma(load_row<T>(&s_v[buf][at]), fo[kk], dp);
+        const frag fk = load_row<T, PS>(&s_k[buf][at]), fv = load_row<T, PS>(&s_v[buf][at]);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          s[n] = mma(fk, fq[n][kk], s[n]);
+          dp[n] = mma(fv, fo[n][kk], dp[n]);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse)) * (dp[i] - delta);
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], c, -lse[n])) * (dp[n][i] - delta[n]);
       if (bits != kAll) {
         const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = w & (1u << (8 * (i >> 2) + (i & 3))) ? s[i] : 0.f;
+        for (int i = 0; i < 16; ++i) {
+          const bool keep = w & (1u << (8 * (i >> 2) + (i & 3)));
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) s[n][i] = keep ? s[n][i] : 0.f;
+        }
       }
 #pragma unroll
       for (int mm = 0; mm < 2; ++mm) {
-        frag f;
-        to_frag(s, mm, f);
+        frag f[NQ];
 #pragma unroll
-        for (int d = 0; d < DT; ++d) dq[d] = mma(load_tr<LD>(s_k[buf], t * 32 + mm * 16, d * 32), f, dq[d]);
+        for (int n = 0; n < NQ; ++n) f[n] = to_frag<T>(s[n], mm);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const frag fk = load_tr<T, LD, PS>(s_k[buf], t * 32 + mm * 16, d * 32);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) dq[n][d] = mma(fk, f[n], dq[n][d]);
+        }
       }
     }
   }
-  if (!live || !a.dq) return;
-  if (a.splits > 1) {
-    float* p = a.part_a + ((int64_t)split * a.nq * a.heads + row) * a.dim;
+  if (!a.dq) return;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) store_col<float>(p, d * 32, a.dim, dq[d], a.scale, a.dim % 4 == 0);
-  } else {
+  for (int n = 0; n < NQ; ++n) {
+    if (row[n] < 0) continue;
+    if (a.splits > 1) {
+      float* p = a.part_a + ((int64_t)split * a.nq * a.heads + row[n]) * a.dim;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) store_col<T>((T*)a.dq + row * a.dim, d * 32, a.dim, dq[d], a.scale, a.ovec);
+      for (int d = 0; d < DT; ++d) store_col<float>(p, d * 32, a.dim, dq[n][d], a.scale, a.dim % 4 == 0);
+    } else {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) store_col<T>((T*)a.dq + row[n] * a.dim, d * 32, a.dim, dq[n][d], a.scale, a.ovec);
+    }
   }
 }
 
-// dk and dv: four waves of 32 keys each over tiles of BQ query rows of the sequence.
-template <typename T, int DP, int BQ, int WPE, bool VEC>
+// dk and dv: four waves of 32 NK keys each over tiles of BQ query rows of the sequence.
+template <typename T, int DP, int NK, int BQ, int WPE, bool VEC>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
-  typedef typename Frag<T>::type frag;
-  constexpr int LD = lds_ld<T, DP>();
-  constexpr int BM = 128;
+  typedef Frag<T> frag;
+  constexpr int LD = lds_ld<DP>(), PS = BQ * LD;
+  constexpr int BM = 128 * NK;
   constexpr int QT = BQ / 32, DT = DP / 32;
-  __shared__ __attribute__((aligned(16))) T s_q[2][BQ * LD];
-  __shared__ __attribute__((aligned(16))) T s_o[2][BQ * LD];
+  __shared__ __attribute__((aligned(16))) bf16_t s_q[2][kParts<T> * PS];
+  __shared__ __attribute__((aligned(16))) bf16_t s_o[2][kParts<T> * PS];
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
@@ -171,27 +199,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     r0 = split * part < r1 ? split * part : r1;
     r1 = r0 + part < r1 ? r0 + part : r1;
   }
-
-  const int64_t j = k0 + tile * BM + wave * 32 + (lane & 31);
-  const bool live = j < k1;
-  const bool keep = live && (!a.mask || a.mask[j]);
-  frag fk[DP / 16], fv[DP / 16];
-#pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) {
-    const int d = kk * 16 + h * 8, have = keep ? a.dim - d : 0;
-    fk[kk] = load8<T>((const T*)a.k + (keep ? j : 0) * a.ks[0] + kh * a.ks[1] + d, have, VEC);
-    fv[kk] = load8<T>((const T*)a.v + (keep ? j : 0) * a.vs[0] + kh * a.vs[1] + d, have, VEC);
-  }
-  const float c = a.scale * kLog2e;
-  f32x16 dk[DT], dv[DT];
-#pragma unroll
-  for (int t = 0; t < DT; ++t) dk[t] = zero16(), dv[t] = zero16();
-
-  // Rows of the tile at t0 + x; with shared key heads a tile's rows step through the group's heads.
+  // Query rows step through the heads of the group before the next query.
   const int n_rows = (int)(r1 - r0);
   Stage<T, BQ, DP, kNT, VEC> sq, so;
-  sq.start((const T*)a.q + q0 * a.qs[0] + kh * a.group * a.qs[1], r0, a.qs[0], a.qs[1], a.group, a.dim);
-  so.start((const T*)a.dout + (q0 * a.heads + kh * a.group) * a.dim, r0, (int64_t)a.heads * a.dim, a.dim, a.group, a.dim);
   float n_lse = 0.f, n_delta = 0.f;
   auto fetch = [&](int t0) {
     sq.load(n_rows - t0);
@@ -209,61 +219,108 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       }
     }
   };
-  if (n_rows > 0) fetch(0);
+  if (n_rows > 0) {
+    sq.start((const T*)a.q + q0 * a.qs[0] + kh * a.group * a.qs[1], r0, a.qs[0], a.qs[1], a.group, a.dim);
+    so.start((const T*)a.dout + (q0 * a.heads + kh * a.group) * a.dim, r0, (int64_t)a.heads * a.dim, a.dim, a.group, a.dim);
+    fetch(0);
+  }
+
+  int64_t key[NK];
+  bool keep[NK];
+  frag fk[NK][DP / 16], fv[NK][DP / 16];
+#pragma unroll
+  for (int n = 0; n < NK; ++n) {
+    const int64_t j = k0 + tile * BM + (wave * NK + n) * 32 + (lane & 31);
+    key[n] = j < k1 ? j : -1;
+    keep[n] = j < k1 && (!a.mask || a.mask[j]);
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+      const int d = kk * 16 + h * 8, have = keep[n] ? a.dim - d : 0;
+      const int64_t at = keep[n] ? j : 0;
+      fk[n][kk] = to_parts(load8<T>((const T*)a.k + at * a.ks[0] + kh * a.ks[1] + d, have, VEC));
+      fv[n][kk] = to_parts(load8<T>((const T*)a.v + at * a.vs[0] + kh * a.vs[1] + d, have, VEC));
+    }
+  }
+  const float c = a.scale * kLog2e;
+  f32x16 dk[NK][DT], dv[NK][DT];
+#pragma unroll
+  for (int n = 0; n < NK; ++n)
+#pragma unroll
+    for (int t = 0; t < DT; ++t) dk[n][t] = zero16(), dv[n][t] = zero16();
+
   int buf = 0;
   for (int t0 = 0; t0 < n_rows; t0 += BQ, buf ^= 1) {
-    sq.template store<LD>(s_q[buf]);
-    so.template store<LD>(s_o[buf]);
+    sq.template store<LD, PS>(s_q[buf]);
+    so.template store<LD, PS>(s_o[buf]);
     if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = n_lse, s_delta[buf][threadIdx.x] = n_delta;
     if (t0 + BQ < n_rows) fetch(t0 + BQ);
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      f32x16 s = zero16(), dp = zero16();
+      f32x16 s[NK], dp[NK];
+#pragma unroll
+      for (int n = 0; n < NK; ++n) s[n] = zero16(), dp[n] = zero16();
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
         const int at = (t * 32 + (lane & 31)) * LD + kk * 16 + h * 8;
-        s = mma(load_row<T>(&s_q[buf][at]), fk[kk], s);
-        dp = mma(load_row<T>(&s_o[buf][at]), fv[kk], dp);
+        const frag fq = load_row<T, PS>(&s_q[buf][at]), fo = load_row<T, PS>(&s_o[buf][at]);
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+          s[n] = mma(fq, fk[n][kk], s[n]);
+          dp[n] = mma(fo, fv[n][kk], dp[n]);
+        }
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4v lse = *(const f32x4v*)&s_lse[buf][t * 32 + 8 * g + 4 * h];
         const f32x4v delta = *(const f32x4v*)&s_delta[buf][t * 32 + 8 * g + 4 * h];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = keep ? __builtin_amdgcn_exp2f(fmaf(s[4 * g + i], c, -lse[i])) : 0.f;
-          dp[4 * g + i] = p * (dp[4 * g + i] - delta[i]);
-          s[4 * g + i] = p;
-        }
+        for (int n = 0; n < NK; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = keep[n] ? __builtin_amdgcn_exp2f(fmaf(s[n][4 * g + i], c, -lse[i])) : 0.f;
+            dp[n][4 * g + i] = p * (dp[n][4 * g + i] - delta[i]);
+            s[n][4 * g + i] = p;
+          }
       }
 #pragma unroll
       for (int mm = 0; mm < 2; ++mm) {
-        frag fp, fs;
-        to_frag(s, mm, fp);
-        to_frag(dp, mm, fs);
+        frag fp[NK], fs[NK];
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+          fp[n] = to_frag<T>(s[n], mm);
+          fs[n] = to_frag<T>(dp[n], mm);
+        }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          dv[d] = mma(load_tr<LD>(s_o[buf], t * 32 + mm * 16, d * 32), fp, dv[d]);
-          dk[d] = mma(load_tr<LD>(s_q[buf], t * 32 + mm * 16, d * 32), fs, dk[d]);
+          const frag go = load_tr<T, LD, PS>(s_o[buf], t * 32 + mm * 16, d * 32);
+          const frag gq = load_tr<T, LD, PS>(s_q[buf], t * 32 + mm * 16, d * 32);
+#pragma unroll
+          for (int n = 0; n < NK; ++n) {
+            dv[n][d] = mma(go, fp[n], dv[n][d]);
+            dk[n][d] = mma(gq, fs[n], dk[n][d]);
+          }
         }
       }
     }
   }
-  if (!live) return;
-  const int64_t row = j * a.kv_heads + kh;
-  if (a.splits > 1) {
-    const int64_t at = ((int64_t)split * a.nk * a.kv_heads + row) * a.dim;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      store_col<float>(a.part_a + at, d * 32, a.dim, dk[d], a.scale, a.dim % 4 == 0);
-      store_col<float>(a.part_b + at, d * 32, a.dim, dv[d], 1.f, a.dim % 4 == 0);
-    }
-  } else {
+  for (int n = 0; n < NK; ++n) {
+    if (key[n] < 0) continue;
+    const int64_t row = key[n] * a.kv_heads + kh;
+    if (a.splits > 1) {
+      const int64_t at = ((int64_t)split * a.nk * a.kv_heads + row) * a.dim;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      store_col<T>((T*)a.dk + row * a.dim, d * 32, a.dim, dk[d], a.scale, a.ovec);
-      store_col<T>((T*)a.dv + row * a.dim, d * 32, a.dim, dv[d], 1.f, a.ovec);
+      for (int d = 0; d < DT; ++d) {
+        store_col<float>(a.part_a + at, d * 32, a.dim, dk[n][d], a.scale, a.dim % 4 == 0);
+        store_col<float>(a.part_b + at, d * 32, a.dim, dv[n][d], 1.f, a.dim % 4 == 0);
+      }
+    } else {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        store_col<T>((T*)a.dk + row * a.dim, d * 32, a.dim, dk[n][d], a.scale, a.ovec);
+        store_col<T>((T*)a.dv + row * a.dim, d * 32, a.dim, dv[n][d], 1.f, a.ovec);
+      }
     }
   }
 }
@@ -284,9 +341,38 @@ void sum_go(const float* part, int splits, int64_t n, void* out, hipStream_t s) 
   k_attn_sum<T><<<(unsigned)std::min<int64_t>((n + kNT - 1) / kNT, 8192), kNT, 0, s>>>(part, splits, n, (T*)out);
 }
 
+// Tiles of the two kernels: 32 NQ (NK) rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
+#ifndef QN
+#define QN 1
+#define QW (DP <= 64 ? 2 : 1)
+#define KN 1
+#define KW (DP <= 64 ? 2 : 1)
+#define BB 64
+#endif
+template <typename T, int DP>
+struct BwdShape;
+template <int DP>
+struct BwdShape<bf16_t, DP> {
+  static constexpr int NQ = QN, QWPE = QW, NK = KN, KWPE = KW, B = BB;
+};
+template <int DP>
+struct BwdShape<float, DP> {
+  static constexpr int NQ = 1, QWPE = DP <= 64 ? 2 : 1, NK = 1, KWPE = DP <= 32 ? 2 : 1, B = 32;
+};
+struct BwdRows {
+  int q, k;
+};
+BwdRows bwd_rows(int dtype, int dim) {
+  if (dtype == IGC_BF16) {
+    constexpr int DP = 64;
+    return {128 * QN, 128 * KN};
+  }
+  return {128, 128};
+}
+
 template <typename T, int DP>
 void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
-  constexpr int B = sizeof(T) == 2 ? 64 : 32, W = DP <= 64 ? 2 : 1;
+  typedef BwdShape<T, DP> S;
   const bool vec = a.qvec && a.kvec && a.ovec;
   a.delta = ws;
   ws += (a.nq * a.heads + 63) / 64 * 64;
@@ -294,9 +380,9 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     AttnArgs d = a;
     d.splits = a.dq ? p.dq_splits : 1;
     d.part_a = ws;
-    const unsigned wgs = (unsigned)((a.nq * a.group / 128 + a.batch) * a.kv_heads * d.splits);
-    if (vec) k_attn_dq<T, DP, B, W, true><<<wgs, kNT, 0, s>>>(d);
-    else k_attn_dq<T, DP, B, W, false><<<wgs, kNT, 0, s>>>(d);
+    const unsigned wgs = (unsigned)((a.nq * a.group / (128 * S::NQ) + a.batch) * a.kv_heads * d.splits);
+    if (vec) k_attn_dq<T, DP, S::NQ, S::B, S::QWPE, true><<<wgs, kNT, 0, s>>>(d);
+    else k_attn_dq<T, DP, S::NQ, S::B, S::QWPE, false><<<wgs, kNT, 0, s>>>(d);
     if (a.dq && d.splits > 1) sum_go<T>(ws, d.splits, a.nq * a.heads * a.dim, a.dq, s);
   }
   if (a.dk && a.nk > 0) {
@@ -304,9 +390,9 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     a.splits = p.dkv_splits;
     a.part_a = ws;
     a.part_b = ws + (p.dkv_splits > 1 ? p.dkv_splits * n : 0);
-    const unsigned wgs = (unsigned)((a.nk / 128 + a.batch) * a.kv_heads * a.splits);
-    if (vec) k_attn_dkv<T, DP, B, W, true><<<wgs, kNT, 0, s>>>(a);
-    else k_attn_dkv<T, DP, B, W, false><<<wgs, kNT, 0, s>>>(a);
+    const unsigned wgs = (unsigned)((a.nk / (128 * S::NK) + a.batch) * a.kv_heads * a.splits);
+    if (vec) k_attn_dkv<T, DP, S::NK, S::B, S::KWPE, true><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_dkv<T, DP, S::NK, S::B, S::KWPE, false><<<wgs, kNT, 0, s>>>(a);
     if (a.splits > 1) {
       sum_go<T>(a.part_a, a.splits, n, a.dk, s);
       sum_go<T>(a.part_b, a.splits, n, a.dv, s);
@@ -329,11 +415,12 @@ int parts(int64_t wgs, int64_t axis) {
 
 }  // namespace
 
-AttnBwdPlan attn_bwd_plan(int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim) {
+AttnBwdPlan attn_bwd_plan(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim) {
   AttnBwdPlan p;
-  const int64_t rows = (nq / batch) * (heads / kv_heads), keys = nk / batch;
-  p.dq_splits = parts(batch * ((rows + 127) / 128) * kv_heads, keys);
-  p.dkv_splits = parts(batch * ((keys + 127) / 128) * kv_heads, rows);
+  const BwdRows t = bwd_rows(dtype, dim);
+  const int64_t rows = (nq + batch - 1) / batch * (heads / kv_heads), keys = (nk + batch - 1) / batch;
+  p.dq_splits = parts(batch * ((rows + t.q - 1) / t.q) * kv_heads, keys);
+  p.dkv_splits = parts(batch * ((keys + t.k - 1) / t.k) * kv_heads, rows);
   const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * nq * heads * dim : 0;
   const size_t dkv = p.dkv_splits > 1 ? (size_t)2 * p.dkv_splits * nk * kv_heads * dim : 0;
   // The two kernels run one after the other, so their partial results share the space.

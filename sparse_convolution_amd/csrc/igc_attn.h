@@ -65,25 +65,63 @@ __device__ __forceinline__ void split_row(int64_t r, int group, int64_t& query, 
   g = (int)(x - q * (uint32_t)group);
 }
 
+// Operands of the matrix instructions are bf16. An fp32 value is split into three parts of 8 significant
+// bits each, x = x0 + x1 + x2 exactly, and a product takes the six part products down to 2^-16 of it, which
+// leaves out 2^-24: fp32 results at six bf16 instructions instead of eight fp32 ones that each take twice as
+// long (fp32 tiles of 32 x 32 x 16: 192 cycles instead of 512). An infinite operand gives NaN.
 template <typename T>
-struct Frag;  // 8 values of one lane along the summed axis
+constexpr int kParts = sizeof(T) == 2 ? 1 : 3;
+
+// 8 values of one lane along the summed axis, as operands.
+template <typename T>
+struct Frag {
+  bf16x8v p[kParts<T>];
+};
+// The same as they are in memory.
+template <typename T>
+struct Raw8;
 template <>
-struct Frag<bf16_t> {
+struct Raw8<bf16_t> {
   typedef bf16x8v type;
 };
 template <>
-struct Frag<float> {
+struct Raw8<float> {
   typedef f32x8v type;
 };
+
+__device__ __forceinline__ Frag<bf16_t> to_parts(const bf16x8v& x) { return {{x}}; }
+__device__ __forceinline__ Frag<float> to_parts(f32x8v x) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  Frag<float> f;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    u32x4 w;  // the upper halves of two values each: truncation to bf16
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __builtin_amdgcn_perm(__float_as_uint(x[2 * i + 1]), __float_as_uint(x[2 * i]), 0x07060302u);
+    f.p[k] = __builtin_bit_cast(bf16x8v, w);
+    if (k < 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] -= __uint_as_float(__float_as_uint(x[i]) & 0xFFFF0000u);
+    }
+  }
+  return f;
+}
 
 // c += a b over 16 values of the summed axis.
 __device__ __forceinline__ f32x16 mma(const bf16x8v& a, const bf16x8v& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x16 mma(const f32x8v& a, const f32x8v& b, f32x16 c) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
-  return c;
+__device__ __forceinline__ f32x16 mma(const Frag<bf16_t>& a, const Frag<bf16_t>& b, const f32x16& c) {
+  return mma(a.p[0], b.p[0], c);
+}
+__device__ __forceinline__ f32x16 mma(const Frag<float>& a, const Frag<float>& b, f32x16 c) {
+  c = mma(a.p[1], b.p[1], c);
+  c = mma(a.p[0], b.p[2], c);
+  c = mma(a.p[2], b.p[0], c);
+  c = mma(a.p[0], b.p[1], c);
+  c = mma(a.p[1], b.p[0], c);
+  return mma(a.p[0], b.p[0], c);
 }
 
 __device__ __forceinline__ f32x16 zero16() {
@@ -95,11 +133,11 @@ __device__ __forceinline__ f32x16 zero16() {
 
 // 8 values at p; only the first `have` exist. vec: p is 16-byte aligned and 8 or none exist.
 template <typename T>
-__device__ __forceinline__ typename Frag<T>::type load8(const T* p, int have, bool vec) {
-  typename Frag<T>::type f;
+__device__ __forceinline__ typename Raw8<T>::type load8(const T* p, int have, bool vec) {
+  typename Raw8<T>::type f;
   if (vec) {
-    f = typename Frag<T>::type{};
-    if (have > 0) f = *(const typename Frag<T>::type*)p;
+    f = typename Raw8<T>::type{};
+    if (have > 0) f = *(const typename Raw8<T>::type*)p;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = i < have ? p[i] : (T)0.f;
@@ -107,43 +145,49 @@ __device__ __forceinline__ typename Frag<T>::type load8(const T* p, int have, bo
   return f;
 }
 
-// First operand from LDS rows (row-major, the summed axis contiguous).
-template <typename T>
-__device__ __forceinline__ typename Frag<T>::type load_row(const T* p) {
-  return *(const typename Frag<T>::type*)p;
-}
-
-// First operand whose summed axis runs over LDS rows: this lane's column col0 + lane % 32 of rows
-// row0 + 4 h + 0..3 and row0 + 8 + 4 h + 0..3. bf16: the transposing LDS read, in which 16 lanes give
-// the addresses of a 4 x 16 block (4 values each) and get a column of 4 each (layout measured).
-template <int LD>
-__device__ __forceinline__ bf16x8v load_tr(const bf16_t* s, int row0, int col0) {
-  typedef short s16x4 __attribute__((ext_vector_type(4)));
-  const int lane = lane_id();
-  const bf16_t* p = s + (row0 + 4 * (lane >> 5) + ((lane & 15) >> 2)) * LD + col0 + (lane & 16) + (lane & 3) * 4;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 8 * LD));
-  const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
-  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-template <int LD>
-__device__ __forceinline__ f32x8v load_tr(const float* s, int row0, int col0) {
-  const int lane = lane_id();
-  const float* p = s + (row0 + 4 * (lane >> 5)) * LD + col0 + (lane & 31);
-  f32x8v f;
+// An LDS tile holds its parts one after the other, PS values apart, each row-major with row stride LD.
+// First operand from rows (the summed axis along the row).
+template <typename T, int PS>
+__device__ __forceinline__ Frag<T> load_row(const bf16_t* p) {
+  Frag<T> f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = p[((i & 3) + (i >> 2) * 8) * LD];
+  for (int k = 0; k < kParts<T>; ++k) f.p[k] = *(const bf16x8v*)(p + k * PS);
   return f;
 }
 
-// Registers 8 m .. 8 m + 7 of a score tile as the second operand.
-__device__ __forceinline__ void to_frag(const f32x16& s, int m, bf16x8v& f) {
+// First operand whose summed axis runs over rows: this lane's column col0 + lane % 32 of rows
+// row0 + 4 h + 0..3 and row0 + 8 + 4 h + 0..3, by the transposing LDS read: 16 lanes give the addresses
+// of a 4 x 16 block (4 values each) and get a column of 4 each (layout measured).
+template <typename T, int LD, int PS>
+__device__ __forceinline__ Frag<T> load_tr(const bf16_t* s, int row0, int col0) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4* lds;
+  const int lane = lane_id();
+  const bf16_t* p = s + (row0 + 4 * (lane >> 5) + ((lane & 15) >> 2)) * LD + col0 + (lane & 16) + (lane & 3) * 4;
+  Frag<T> f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = (bf16_t)s[8 * m + i];
+  for (int k = 0; k < kParts<T>; ++k) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + k * PS));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + k * PS + 8 * LD));
+    f.p[k] = __builtin_shufflevector(__builtin_bit_cast(bf16x4, a), __builtin_bit_cast(bf16x4, b), 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  return f;
 }
-__device__ __forceinline__ void to_frag(const f32x16& s, int m, f32x8v& f) {
+
+// Registers 8 m .. 8 m + 7 of a score tile as the second operand (bf16 data: rounded to nearest).
+template <typename T>
+__device__ __forceinline__ Frag<T> to_frag(const f32x16& s, int m) {
+  if constexpr (sizeof(T) == 2) {
+    Frag<T> f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = s[8 * m + i];
+    for (int i = 0; i < 8; ++i) f.p[0][i] = (bf16_t)s[8 * m + i];
+    return f;
+  } else {
+    f32x8v x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = s[8 * m + i];
+    return to_parts(x);
+  }
 }
 
 // Largest of a tile's 16 registers. The three-way maximum as it is: from fmaxf the compiler first
@@ -169,9 +213,9 @@ __device__ __forceinline__ float halves_max(float x) {
 __device__ __forceinline__ int reg_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
 // Row stride of an LDS tile of DP columns.
-template <typename T, int DP>
+template <int DP>
 constexpr int lds_ld() {
-  return DP + (sizeof(T) == 2 ? 8 : 4);
+  return DP + 8;
 }
 
 // Copies tiles of ROWS rows of an operand (columns from dim on are zero) into an LDS tile of row stride
@@ -186,7 +230,7 @@ struct Stage {
   static constexpr int CG = DP / 8;                    // granules of a row
   static constexpr int N = (ROWS * CG + NT - 1) / NT;  // granules of a thread
   typedef typename std::conditional<VEC, uint32_t, int64_t>::type Off;
-  typename Frag<T>::type r[N];
+  typename Raw8<T>::type r[N];
   Off off[N];  // bytes
   const char* base;
   int64_t row_stride, head_stride, at;
@@ -215,7 +259,7 @@ struct Stage {
   __device__ __forceinline__ void load(int have) {
     if (VEC && have >= ROWS && dim == DP && (ROWS * CG) % NT == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = *(const typename Frag<T>::type*)(base + off[i]);
+      for (int i = 0; i < N; ++i) r[i] = *(const typename Raw8<T>::type*)(base + off[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -240,21 +284,27 @@ struct Stage {
     }
   }
   // Rows whose bit in `keep` is off are written as zeros.
-  template <int LD>
-  __device__ __forceinline__ void store(T* s, uint64_t keep) const {
+  template <int LD, int PS>
+  __device__ __forceinline__ void store(bf16_t* s, uint64_t keep) const {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (mine(i)) {
-        typename Frag<T>::type f = r[i];
-        if (!(keep >> row(i) & 1)) f = typename Frag<T>::type{};
-        *(typename Frag<T>::type*)(s + row(i) * LD + col(i)) = f;
+        typename Raw8<T>::type x = r[i];
+        if (!(keep >> row(i) & 1)) x = typename Raw8<T>::type{};
+        put<LD, PS>(s, i, x);
       }
   }
-  template <int LD>
-  __device__ __forceinline__ void store(T* s) const {
+  template <int LD, int PS>
+  __device__ __forceinline__ void store(bf16_t* s) const {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (mine(i)) *(typename Frag<T>::type*)(s + row(i) * LD + col(i)) = r[i];
+      if (mine(i)) put<LD, PS>(s, i, r[i]);
+  }
+  template <int LD, int PS>
+  static __device__ __forceinline__ void put(bf16_t* s, int i, const typename Raw8<T>::type& x) {
+    const Frag<T> f = to_parts(x);
+#pragma unroll
+    for (int k = 0; k < kParts<T>; ++k) *(bf16x8v*)(s + k * PS + row(i) * LD + col(i)) = f.p[k];
   }
 };
 

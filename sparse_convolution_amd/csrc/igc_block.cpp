@@ -130,7 +130,7 @@ int igc_cross_attention_workspace(const igc_attention_t* p, int32_t backward, si
   if (rc) return rc;
   if (!bytes) return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_workspace: bytes is null");
   if (backward) {
-    *bytes = attn_bwd_plan(a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim).floats * sizeof(float);
+    *bytes = attn_bwd_plan(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim).floats * sizeof(float);
   } else {
     a.splits = attn_fwd_splits(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
     *bytes = forward_bytes(a);
@@ -179,7 +179,7 @@ int igc_cross_attention_backward(const igc_attention_t* p, const void* d_q, cons
   a.dq = d_dq, a.dk = d_dk, a.dv = d_dv;
   attention_alignment(p, a, (const void*)((uintptr_t)d_out | (uintptr_t)d_dout | (uintptr_t)d_dq | (uintptr_t)d_dk |
                                           (uintptr_t)d_dv));
-  const AttnBwdPlan plan = attn_bwd_plan(a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
+  const AttnBwdPlan plan = attn_bwd_plan(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
   const size_t need = plan.floats * sizeof(float);
   if (need > 0 && (!d_ws || ws_bytes < need)) return workspace_error(fn, need);
   return launch_attn_bwd(a, p->dtype, plan, d_ws, (hipStream_t)stream);

@@ -240,7 +240,7 @@ struct AttnBwdPlan {
   int dq_splits = 1, dkv_splits = 1;
   size_t floats = 0;  // workspace
 };
-AttnBwdPlan attn_bwd_plan(int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim);
+AttnBwdPlan attn_bwd_plan(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim);
 int launch_attn_bwd(const AttnArgs& a, int dtype, const AttnBwdPlan& p, void* ws, hipStream_t s);
 
 }  // namespace igc
