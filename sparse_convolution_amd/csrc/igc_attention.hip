@@ -32,8 +32,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   constexpr int BM = 128 * NQ;
   constexpr int KT = BN / 32, DT = DP / 32;
   constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
-  __shared__ __attribute__((aligned(16))) bf16_t s_k[2][kParts<T> * PS];
-  __shared__ __attribute__((aligned(16))) bf16_t s_v[2][kParts<T> * PS];
+  constexpr int TILE = kParts<T> * PS;
+  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE)];
+  auto s_k = [&](int buf) { return (bf16_t*)s_mem + buf * TILE; };
+  auto s_v = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
   const int kh = blockIdx.x % a.kv_heads;
@@ -100,11 +102,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   for (int j = 0; j < keys; j += BN, buf ^= 1) {
     const uint64_t bits = next_bits;
     if (a.mask) {  // what a masked place holds must not meet a zero probability
-      sk.template store<LD, PS>(s_k[buf], bits);
-      sv.template store<LD, PS>(s_v[buf], bits);
+      sk.template store<LD, PS>(s_k(buf), bits);
+      sv.template store<LD, PS>(s_v(buf), bits);
     } else {
-      sk.template store<LD, PS>(s_k[buf]);
-      sv.template store<LD, PS>(s_v[buf]);
+      sk.template store<LD, PS>(s_k(buf));
+      sv.template store<LD, PS>(s_v(buf));
     }
     if (j + BN < keys) {
       sk.load(keys - j - BN);
@@ -120,7 +122,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       for (int n = 0; n < NQ; ++n) s[n][t] = zero16();
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
-        const frag fk = load_row<T, PS>(&s_k[buf][(t * 32 + (lane & 31)) * LD + kk * 16 + h * 8]);
+        const frag fk = load_row<T, PS>(s_k(buf) + (t * 32 + (lane & 31)) * LD + kk * 16 + h * 8);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) s[n][t] = mma(fk, fq[n][kk], s[n][t]);
       }
@@ -172,31 +174,29 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         for (int n = 0; n < NQ; ++n) p[n] = to_frag<T>(s[n][t], mm);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const frag fv = load_tr<T, LD, PS>(s_v[buf], t * 32 + mm * 16, d * 32);
+          const frag fv = load_tr<T, LD, PS>(s_v(buf), t * 32 + mm * 16, d * 32);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) o[n][d] = mma(fv, p[n], o[n][d]);
         }
       }
   }
 
+  __syncthreads();  // every wave is past reading the tiles: their space takes the results
+  void* const s_out = s_mem + wave * (32 * (DP + 4) * 4);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const float total = l[n] + __shfl_xor(l[n], 32, 64);
-    if (row[n] < 0) continue;
     if (a.splits > 1) {
-      const int64_t at = (int64_t)split * a.nq * a.heads + row[n];
-#pragma unroll
-      for (int d = 0; d < DT; ++d) store_col<float>(a.part_a + at * a.dim, d * 32, a.dim, o[n][d], 1.f, a.dim % 4 == 0);
-      if (h == 0) {
-        a.part_b[at * 2] = m[n] * c;
-        a.part_b[at * 2 + 1] = total;
+      const int64_t first = (int64_t)split * a.nq * a.heads;
+      store_tile<float, DP>(a.part_a + first * a.dim, s_out, o[n], 1.f, row[n], a.dim, a.dim % 4 == 0);
+      if (row[n] >= 0 && h == 0) {
+        a.part_b[(first + row[n]) * 2] = m[n] * c;
+        a.part_b[(first + row[n]) * 2 + 1] = total;
       }
     } else {
       const float f = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-        store_col<T>((T*)a.out + row[n] * a.dim, d * 32, a.dim, o[n][d], f, a.ovec);
-      if (h == 0) a.lse[row[n]] = total == 0.f ? -INFINITY : kLn2 * (m[n] * c + log2f(total));
+      store_tile<T, DP>((T*)a.out, s_out, o[n], f, row[n], a.dim, a.ovec);
+      if (row[n] >= 0 && h == 0) a.lse[row[n]] = total == 0.f ? -INFINITY : kLn2 * (m[n] * c + log2f(total));
     }
   }
 }

@@ -31,8 +31,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   constexpr int BM = 128 * NQ;
   constexpr int KT = BN / 32, DT = DP / 32;
   constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
-  __shared__ __attribute__((aligned(16))) bf16_t s_k[2][kParts<T> * PS];
-  __shared__ __attribute__((aligned(16))) bf16_t s_v[2][kParts<T> * PS];
+  constexpr int TILE = kParts<T> * PS;
+  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE)];
+  auto s_k = [&](int buf) { return (bf16_t*)s_mem + buf * TILE; };
+  auto s_v = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
   const int kh = blockIdx.x % a.kv_heads;
@@ -103,11 +105,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   for (int j = 0; j < keys; j += BN, buf ^= 1) {
     const uint64_t bits = next_bits;
     if (a.mask) {
-      sk.template store<LD, PS>(s_k[buf], bits);
-      sv.template store<LD, PS>(s_v[buf], bits);
+      sk.template store<LD, PS>(s_k(buf), bits);
+      sv.template store<LD, PS>(s_v(buf), bits);
     } else {
-      sk.template store<LD, PS>(s_k[buf]);
-      sv.template store<LD, PS>(s_v[buf]);
+      sk.template store<LD, PS>(s_k(buf));
+      sv.template store<LD, PS>(s_v(buf));
     }
     if (j + BN < keys) {
       sk.load(keys - j - BN);
@@ -123,7 +125,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
         const int at = (t * 32 + (lane & 31)) * LD + kk * 16 + h * 8;
-        const frag fk = load_row<T, PS>(&s_k[buf][at]), fv = load_row<T, PS>(&s_v[buf][at]);
+        const frag fk = load_row<T, PS>(s_k(buf) + at), fv = load_row<T, PS>(s_v(buf) + at);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
           s[n] = mma(fk, fq[n][kk], s[n]);
@@ -151,7 +153,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         for (int n = 0; n < NQ; ++n) f[n] = to_frag<T>(s[n], mm);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const frag fk = load_tr<T, LD, PS>(s_k[buf], t * 32 + mm * 16, d * 32);
+          const frag fk = load_tr<T, LD, PS>(s_k(buf), t * 32 + mm * 16, d * 32);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) dq[n][d] = mma(fk, f[n], dq[n][d]);
         }
@@ -159,17 +161,15 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     }
   }
   if (!a.dq) return;
+  __syncthreads();  // every wave is past reading the tiles: their space takes the results
+  void* const s_out = s_mem + wave * (32 * (DP + 4) * 4);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    if (row[n] < 0) continue;
-    if (a.splits > 1) {
-      float* p = a.part_a + ((int64_t)split * a.nq * a.heads + row[n]) * a.dim;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) store_col<float>(p, d * 32, a.dim, dq[n][d], a.scale, a.dim % 4 == 0);
-    } else {
-#pragma unroll
-      for (int d = 0; d < DT; ++d) store_col<T>((T*)a.dq + row[n] * a.dim, d * 32, a.dim, dq[n][d], a.scale, a.ovec);
-    }
+    if (a.splits > 1)
+      store_tile<float, DP>(a.part_a + (int64_t)split * a.nq * a.heads * a.dim, s_out, dq[n], a.scale, row[n], a.dim,
+                            a.dim % 4 == 0);
+    else
+      store_tile<T, DP>((T*)a.dq, s_out, dq[n], a.scale, row[n], a.dim, a.ovec);
   }
 }
 
@@ -180,8 +180,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   constexpr int LD = lds_ld<DP>(), PS = BQ * LD;
   constexpr int BM = 128 * NK;
   constexpr int QT = BQ / 32, DT = DP / 32;
-  __shared__ __attribute__((aligned(16))) bf16_t s_q[2][kParts<T> * PS];
-  __shared__ __attribute__((aligned(16))) bf16_t s_o[2][kParts<T> * PS];
+  constexpr int TILE = kParts<T> * PS;
+  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE)];
+  auto s_q = [&](int buf) { return (bf16_t*)s_mem + buf * TILE; };
+  auto s_o = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
@@ -250,8 +252,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 
   int buf = 0;
   for (int t0 = 0; t0 < n_rows; t0 += BQ, buf ^= 1) {
-    sq.template store<LD, PS>(s_q[buf]);
-    so.template store<LD, PS>(s_o[buf]);
+    sq.template store<LD, PS>(s_q(buf));
+    so.template store<LD, PS>(s_o(buf));
     if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = n_lse, s_delta[buf][threadIdx.x] = n_delta;
     if (t0 + BQ < n_rows) fetch(t0 + BQ);
     __syncthreads();
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
         const int at = (t * 32 + (lane & 31)) * LD + kk * 16 + h * 8;
-        const frag fq = load_row<T, PS>(&s_q[buf][at]), fo = load_row<T, PS>(&s_o[buf][at]);
+        const frag fq = load_row<T, PS>(s_q(buf) + at), fo = load_row<T, PS>(s_o(buf) + at);
 #pragma unroll
         for (int n = 0; n < NK; ++n) {
           s[n] = mma(fq, fk[n][kk], s[n]);
@@ -293,8 +295,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const frag go = load_tr<T, LD, PS>(s_o[buf], t * 32 + mm * 16, d * 32);
-          const frag gq = load_tr<T, LD, PS>(s_q[buf], t * 32 + mm * 16, d * 32);
+          const frag go = load_tr<T, LD, PS>(s_o(buf), t * 32 + mm * 16, d * 32);
+          const frag gq = load_tr<T, LD, PS>(s_q(buf), t * 32 + mm * 16, d * 32);
 #pragma unroll
           for (int n = 0; n < NK; ++n) {
             dv[n][d] = mma(go, fp[n], dv[n][d]);
@@ -304,23 +306,18 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       }
     }
   }
+  __syncthreads();
+  void* const s_out = s_mem + wave * (32 * (DP + 4) * 4);
 #pragma unroll
   for (int n = 0; n < NK; ++n) {
-    if (key[n] < 0) continue;
-    const int64_t row = key[n] * a.kv_heads + kh;
+    const int64_t row = key[n] < 0 ? -1 : key[n] * a.kv_heads + kh;
     if (a.splits > 1) {
-      const int64_t at = ((int64_t)split * a.nk * a.kv_heads + row) * a.dim;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        store_col<float>(a.part_a + at, d * 32, a.dim, dk[n][d], a.scale, a.dim % 4 == 0);
-        store_col<float>(a.part_b + at, d * 32, a.dim, dv[n][d], 1.f, a.dim % 4 == 0);
-      }
+      const int64_t first = (int64_t)split * a.nk * a.kv_heads * a.dim;
+      store_tile<float, DP>(a.part_a + first, s_out, dk[n], a.scale, row, a.dim, a.dim % 4 == 0);
+      store_tile<float, DP>(a.part_b + first, s_out, dv[n], 1.f, row, a.dim, a.dim % 4 == 0);
     } else {
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        store_col<T>((T*)a.dk + row * a.dim, d * 32, a.dim, dk[n][d], a.scale, a.ovec);
-        store_col<T>((T*)a.dv + row * a.dim, d * 32, a.dim, dv[n][d], 1.f, a.ovec);
-      }
+      store_tile<T, DP>((T*)a.dk, s_out, dk[n], a.scale, row, a.dim, a.ovec);
+      store_tile<T, DP>((T*)a.dv, s_out, dv[n], 1.f, row, a.dim, a.ovec);
     }
   }
 }
@@ -341,34 +338,32 @@ void sum_go(const float* part, int splits, int64_t n, void* out, hipStream_t s) 
   k_attn_sum<T><<<(unsigned)std::min<int64_t>((n + kNT - 1) / kNT, 8192), kNT, 0, s>>>(part, splits, n, (T*)out);
 }
 
-// Tiles of the two kernels: 32 NQ (NK) rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
-#ifndef QN
-#define QN 1
-#define QW (DP <= 64 ? 2 : 1)
-#define KN 1
-#define KW (DP <= 64 ? 2 : 1)
-#define BB 64
-#endif
+// Tiles of the two kernels: 32 NQ (NK) query rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
+// bf16, measured on 60,000 queries x 1,500 keys and 256 channels (dq / dkv, us): heads of 32: dq 209 with three waves,
+// 228 with NQ 2; dkv 286 with NK 2, 346 with NK 1. Heads of 64: dq 175 with NQ 2 on 32-key tiles, 184 on 64, 187 with NQ 1;
+// dkv 231, with NK 2 (one wave) 317, on 32-row tiles 254. Heads of 128: dq 184 with two waves, 242 with one; dkv 290 with
+// one wave, 470 with two (spills).
 template <typename T, int DP>
 struct BwdShape;
 template <int DP>
 struct BwdShape<bf16_t, DP> {
-  static constexpr int NQ = QN, QWPE = QW, NK = KN, KWPE = KW, B = BB;
+  static constexpr int NQ = DP == 64 ? 2 : 1, QWPE = DP <= 32 ? 3 : 2, QB = DP == 64 ? 32 : 64;
+  static constexpr int NK = DP <= 32 ? 2 : 1, KWPE = DP <= 64 ? 2 : 1, KB = 64;
 };
 template <int DP>
 struct BwdShape<float, DP> {
-  static constexpr int NQ = 1, QWPE = DP <= 64 ? 2 : 1, NK = 1, KWPE = DP <= 32 ? 2 : 1, B = 32;
+  static constexpr int NQ = 1, QWPE = DP <= 64 ? 2 : 1, QB = 32, NK = 1, KWPE = DP <= 32 ? 2 : 1, KB = 32;
 };
 struct BwdRows {
   int q, k;
 };
-BwdRows bwd_rows(int dtype, int dim) {
-  if (dtype == IGC_BF16) {
-    constexpr int DP = 64;
-    return {128 * QN, 128 * KN};
-  }
-  return {128, 128};
+template <typename T>
+BwdRows bwd_rows_t(int dim) {
+  if (dim <= 32) return {128 * BwdShape<T, 32>::NQ, 128 * BwdShape<T, 32>::NK};
+  if (dim <= 64) return {128 * BwdShape<T, 64>::NQ, 128 * BwdShape<T, 64>::NK};
+  return {128 * BwdShape<T, 128>::NQ, 128 * BwdShape<T, 128>::NK};
 }
+BwdRows bwd_rows(int dtype, int dim) { return dtype == IGC_BF16 ? bwd_rows_t<bf16_t>(dim) : bwd_rows_t<float>(dim); }
 
 template <typename T, int DP>
 void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
@@ -381,8 +376,8 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     d.splits = a.dq ? p.dq_splits : 1;
     d.part_a = ws;
     const unsigned wgs = (unsigned)((a.nq * a.group / (128 * S::NQ) + a.batch) * a.kv_heads * d.splits);
-    if (vec) k_attn_dq<T, DP, S::NQ, S::B, S::QWPE, true><<<wgs, kNT, 0, s>>>(d);
-    else k_attn_dq<T, DP, S::NQ, S::B, S::QWPE, false><<<wgs, kNT, 0, s>>>(d);
+    if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true><<<wgs, kNT, 0, s>>>(d);
+    else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false><<<wgs, kNT, 0, s>>>(d);
     if (a.dq && d.splits > 1) sum_go<T>(ws, d.splits, a.nq * a.heads * a.dim, a.dq, s);
   }
   if (a.dk && a.nk > 0) {
@@ -391,8 +386,8 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     a.part_a = ws;
     a.part_b = ws + (p.dkv_splits > 1 ? p.dkv_splits * n : 0);
     const unsigned wgs = (unsigned)((a.nk / (128 * S::NK) + a.batch) * a.kv_heads * a.splits);
-    if (vec) k_attn_dkv<T, DP, S::NK, S::B, S::KWPE, true><<<wgs, kNT, 0, s>>>(a);
-    else k_attn_dkv<T, DP, S::NK, S::B, S::KWPE, false><<<wgs, kNT, 0, s>>>(a);
+    if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false><<<wgs, kNT, 0, s>>>(a);
     if (a.splits > 1) {
       sum_go<T>(a.part_a, a.splits, n, a.dk, s);
       sum_go<T>(a.part_b, a.splits, n, a.dv, s);
