@@ -396,7 +396,7 @@ template <typename T, int DP>
 struct FwdShape;  // NQ, BN
 template <int DP>
 struct FwdShape<bf16_t, DP> {
-  static constexpr int NQ = DP <= 64 ? 2 : 1, BN = 64, WPE = 2;
+  static constexpr int NQ = DP <= 64 ? 2 : 1, BN = 64, WPE = DP <= 32 ? 3 : 2;
 };
 template <int DP>
 struct FwdShape<float, DP> {
