@@ -17,59 +17,62 @@ namespace {
 constexpr int kNT = 256;
 
 // GL lanes hold a group of up to 64 channels, V each; unit u = (row, group).
-template <typename T, int V, int GL>
-__global__ __launch_bounds__(kNT) void k_pack(const T* __restrict__ x, int64_t units, int c, int groups,
+template <typename T, int V, int GL, bool TAIL>
+__global__ __launch_bounds__(kNT) void k_pack(const T* __restrict__ x, uint32_t units, int c, int groups,
                                               int8_t* __restrict__ codes, float* __restrict__ scales) {
   constexpr int SL = kNT / GL;
   const int l = threadIdx.x % GL, slot = threadIdx.x / GL;
-  for (int64_t u0 = (int64_t)blockIdx.x * SL; u0 < units; u0 += (int64_t)gridDim.x * SL) {
-    const int64_t u = u0 + slot;
-    const int64_t r = u / groups;
-    const int ch = (int)(u - r * groups) * kQ8Group + l * V;
-    const bool in = u < units && ch < c;
+  for (uint64_t u0 = (uint64_t)blockIdx.x * SL; u0 < units; u0 += (uint64_t)gridDim.x * SL) {
+    const uint32_t u = (uint32_t)u0 + slot;
+    const bool live = u0 + slot < units;
+    const uint32_t r = groups == 1 ? u : u / (uint32_t)groups;
+    const RowPos<V, TAIL> e((int)(u - r * groups) * kQ8Group + l * V, c);
     float v[V];
     float a = 0.f;
-    if (in) load_vec<T, V>(x + r * c + ch, v);
+    if (live && e.in) load_vec<T, V>(x + (int64_t)r * c + e.at, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) a = in ? absmax2(a, v[i]) : 0.f;
+    for (int i = 0; i < V; ++i) a = live && e.in && e.own(i) ? absmax2(a, v[i]) : a;
     a = lanes_absmax<GL>(a);
     float inv, scale;
     q8_scale(a, inv, scale);
-    if (in) {
-      store_codes<V>(codes + r * c + ch, v, inv);
+    if (live && e.in) {
+      store_codes<V>(codes + (int64_t)r * c + e.at, v, inv, e.skip);
       if (l == 0) scales[u] = scale;
     }
   }
 }
 
-// V channels of one group per thread.
-template <typename T, int V>
+// V channels of one row per thread.
+template <typename T, int V, bool TAIL>
 __global__ __launch_bounds__(kNT) void k_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales,
                                                 int64_t items, int per_row, int c, int groups, T* __restrict__ x) {
-  for (int64_t e = (int64_t)blockIdx.x * kNT + threadIdx.x; e < items; e += (int64_t)gridDim.x * kNT) {
-    const int64_t r = e / per_row;
-    const int ch = (int)(e - r * per_row) * V;
+  const bool small = items <= UINT32_MAX;
+  for (int64_t at = (int64_t)blockIdx.x * kNT + threadIdx.x; at < items; at += (int64_t)gridDim.x * kNT) {
+    const int64_t r = small ? (int64_t)((uint32_t)at / (uint32_t)per_row) : at / per_row;
+    const int first = (int)(at - r * per_row) * V;
+    const RowPos<V, TAIL> e(first, c);
     float v[V];
-    load_codes<V>(codes + r * c + ch, v);
-    const float sc = scales[r * groups + ch / kQ8Group];
+    load_codes<V>(codes + r * c + e.at, v);
+    const float sc = scales[r * groups + first / kQ8Group];
+    const float before = TAIL ? scales[r * groups + e.at / kQ8Group] : sc;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= sc;
-    store_vec<T, V>(x + r * c + ch, v);
+    for (int i = 0; i < V; ++i) v[i] *= e.own(i) ? sc : before;
+    store_vec<T, V>(x + r * c + e.at, v);
   }
-}
-
-template <typename T>
-int vec_of(int c, const void* x, const void* codes) {
-  for (int v = 16 / (int)sizeof(T); v >= 4; v /= 2)
-    if (c % v == 0 && (uintptr_t)x % (v * sizeof(T)) == 0 && (uintptr_t)codes % v == 0) return v;
-  return 1;
 }
 
 template <typename T, int V, int GL>
 void pack_go(const T* x, int64_t n, int c, int8_t* codes, float* scales, hipStream_t s) {
   const int groups = (c + kQ8Group - 1) / kQ8Group;
-  const int64_t blocks = (n * groups + kNT / GL - 1) / (kNT / GL);
-  k_pack<T, V, GL><<<(unsigned)std::min<int64_t>(blocks, 8192), kNT, 0, s>>>(x, n * groups, c, groups, codes, scales);
+  // 32-bit units: rows of more groups are packed 2^25 rows at a time.
+  for (int64_t r = 0; r < n; r += (int64_t)1 << 25) {
+    const int64_t rows = std::min<int64_t>(n - r, (int64_t)1 << 25);
+    const uint32_t units = (uint32_t)(rows * groups);
+    const unsigned blocks = (unsigned)std::min<int64_t>(((int64_t)units + kNT / GL - 1) / (kNT / GL), 8192);
+    const T* xr = x + r * c;
+    if (c % V == 0) k_pack<T, V, GL, false><<<blocks, kNT, 0, s>>>(xr, units, c, groups, codes + r * c, scales + r * groups);
+    else k_pack<T, V, GL, true><<<blocks, kNT, 0, s>>>(xr, units, c, groups, codes + r * c, scales + r * groups);
+  }
 }
 
 template <typename T, int V>
@@ -77,42 +80,40 @@ void pack_v(const T* x, int64_t n, int c, int8_t* codes, float* scales, hipStrea
   const int lanes = (std::min(c, kQ8Group) + V - 1) / V;
   if (lanes <= 1) return pack_go<T, V, 1>(x, n, c, codes, scales, s);
   if (lanes <= 2) return pack_go<T, V, 2>(x, n, c, codes, scales, s);
-  if (lanes <= 4) return pack_go<T, V, 4>(x, n, c, codes, scales, s);
-  if (lanes <= 8) return pack_go<T, V, 8>(x, n, c, codes, scales, s);
-  if constexpr (V < 8) {
-    if (lanes <= 16) return pack_go<T, V, 16>(x, n, c, codes, scales, s);
-    if constexpr (V < 4) {
-      if (lanes <= 32) return pack_go<T, V, 32>(x, n, c, codes, scales, s);
-      pack_go<T, V, 64>(x, n, c, codes, scales, s);
-    }
+  if constexpr (V >= 4) {
+    if (lanes <= 4) return pack_go<T, V, 4>(x, n, c, codes, scales, s);
+    if (lanes <= 8) return pack_go<T, V, 8>(x, n, c, codes, scales, s);
+    if constexpr (V == 4) pack_go<T, V, 16>(x, n, c, codes, scales, s);
   }
 }
 
 template <typename T, int V>
 void unpack_v(const int8_t* codes, const float* scales, int64_t n, int c, T* x, hipStream_t s) {
-  const int64_t items = n * (c / V);
-  const int64_t blocks = (items + kNT - 1) / kNT;
-  k_unpack<T, V><<<(unsigned)std::min<int64_t>(blocks, 16384), kNT, 0, s>>>(codes, scales, items, c / V, c,
-                                                                           (c + kQ8Group - 1) / kQ8Group, x);
+  const int per_row = (c + V - 1) / V, groups = (c + kQ8Group - 1) / kQ8Group;
+  const int64_t items = n * per_row;
+  const unsigned blocks = (unsigned)std::min<int64_t>((items + kNT - 1) / kNT, 16384);
+  if (c % V == 0) k_unpack<T, V, false><<<blocks, kNT, 0, s>>>(codes, scales, items, per_row, c, groups, x);
+  else k_unpack<T, V, true><<<blocks, kNT, 0, s>>>(codes, scales, items, per_row, c, groups, x);
 }
 
+// 16 bytes a load, less only for rows of fewer channels than that.
 template <typename T>
 void pack_t(const T* x, int64_t n, int c, int8_t* codes, float* scales, hipStream_t s) {
-  const int v = vec_of<T>(c, x, codes);
   if constexpr (sizeof(T) == 2) {
-    if (v == 8) return pack_v<T, 8>(x, n, c, codes, scales, s);
+    if (c >= 8) return pack_v<T, 8>(x, n, c, codes, scales, s);
   }
-  if (v == 4) return pack_v<T, 4>(x, n, c, codes, scales, s);
+  if (c >= 4) return pack_v<T, 4>(x, n, c, codes, scales, s);
+  if (c >= 2) return pack_v<T, 2>(x, n, c, codes, scales, s);
   pack_v<T, 1>(x, n, c, codes, scales, s);
 }
 
 template <typename T>
 void unpack_t(const int8_t* codes, const float* scales, int64_t n, int c, T* x, hipStream_t s) {
-  const int v = vec_of<T>(c, x, codes);
   if constexpr (sizeof(T) == 2) {
-    if (v == 8) return unpack_v<T, 8>(codes, scales, n, c, x, s);
+    if (c >= 8) return unpack_v<T, 8>(codes, scales, n, c, x, s);
   }
-  if (v == 4) return unpack_v<T, 4>(codes, scales, n, c, x, s);
+  if (c >= 4) return unpack_v<T, 4>(codes, scales, n, c, x, s);
+  if (c >= 2) return unpack_v<T, 2>(codes, scales, n, c, x, s);
   unpack_v<T, 1>(codes, scales, n, c, x, s);
 }
 

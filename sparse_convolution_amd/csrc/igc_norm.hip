@@ -55,7 +55,7 @@ __device__ __forceinline__ float row_sum(float a, float* s) {
   return a;
 }
 
-template <typename T, int V, int LPR, int NV, bool Q8>
+template <typename T, int V, int LPR, int NV, bool TAIL, bool Q8>
 __global__ __launch_bounds__(kNT) void k_norm(const T* __restrict__ x, int64_t n, int c, const void* __restrict__ w,
                                               const void* __restrict__ b, int wf32, float eps, T* __restrict__ y,
                                               float* __restrict__ mean, float* __restrict__ rstd,
@@ -68,13 +68,14 @@ __global__ __launch_bounds__(kNT) void k_norm(const T* __restrict__ x, int64_t n
   const int groups = (c + kQ8Group - 1) / kQ8Group;
   float pw[NV][V], pb[NV][V];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    const RowPos<V, TAIL> e((j * LPR + l) * V, c);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int ch = (j * LPR + l) * V + i;
-      pw[j][i] = w && ch < c ? load_param(w, ch, wf32) : 1.f;
-      pb[j][i] = b && ch < c ? load_param(b, ch, wf32) : 0.f;
+      pw[j][i] = w && e.in ? load_param(w, e.at + i, wf32) : 1.f;
+      pb[j][i] = b && e.in ? load_param(b, e.at + i, wf32) : 0.f;
     }
+  }
   for (int64_t r0 = (int64_t)blockIdx.x * SL; r0 < n; r0 += (int64_t)gridDim.x * SL) {
     const int64_t r = r0 + slot;
     const bool live = r < n;
@@ -82,26 +83,27 @@ __global__ __launch_bounds__(kNT) void k_norm(const T* __restrict__ x, int64_t n
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int ch = (j * LPR + l) * V;
-      if (live && ch < c) {
-        load_vec<T, V>(x + r * c + ch, v[j]);
+      const RowPos<V, TAIL> e((j * LPR + l) * V, c);
+      if (live && e.in) {
+        load_vec<T, V>(x + r * c + e.at, v[j]);
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[j][i] = 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += v[j][i];
+      for (int i = 0; i < V; ++i) sum += e.own(i) ? v[j][i] : 0.f;
     }
     const float mu0 = row_sum<LPR>(sum, s_red) * inv_c;
     float sq = 0.f, rest = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in = (j * LPR + l) * V < c;
+      const RowPos<V, TAIL> e((j * LPR + l) * V, c);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[j][i] = in ? v[j][i] - mu0 : 0.f;
-        rest += v[j][i];
-        sq = fmaf(v[j][i], v[j][i], sq);
+        v[j][i] = e.in ? v[j][i] - mu0 : 0.f;
+        const float d = e.own(i) ? v[j][i] : 0.f;
+        rest += d;
+        sq = fmaf(d, d, sq);
       }
     }
     row_sum2<LPR>(rest, sq, s_red);
@@ -110,23 +112,24 @@ __global__ __launch_bounds__(kNT) void k_norm(const T* __restrict__ x, int64_t n
     const float rs = 1.0f / sqrtf(fmaxf(fmaf(-rest, rest, sq * inv_c), 0.f) + eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int ch = (j * LPR + l) * V;
+      const int first = (j * LPR + l) * V;
+      const RowPos<V, TAIL> e(first, c);
       float o[V];
       float a = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[j][i] = ch < c ? (v[j][i] - rest) * rs : 0.f;
+        v[j][i] = e.in ? (v[j][i] - rest) * rs : 0.f;
         o[i] = fmaf(v[j][i], pw[j][i], pb[j][i]);
-        if (Q8) a = absmax2(a, v[j][i]);
+        if (Q8) a = absmax2(a, e.own(i) ? v[j][i] : 0.f);
       }
-      if (live && ch < c) store_vec<T, V>(y + r * c + ch, o);
+      if (live && e.in) store_vec<T, V>(y + r * c + e.at, o);
       if constexpr (Q8) {
         a = lanes_absmax<GL>(a);
         float inv, scale;
         q8_scale(a, inv, scale);
-        if (live && ch < c) {
-          store_codes<V>(codes + r * c + ch, v[j], inv);
-          if (l % GL == 0) scales[r * groups + ch / kQ8Group] = scale;
+        if (live && e.in) {
+          store_codes<V>(codes + r * c + e.at, v[j], inv, e.skip);
+          if (l % GL == 0) scales[r * groups + first / kQ8Group] = scale;
         }
       }
     }
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(kNT) void k_norm(const T* __restrict__ x, int64_t n
 
 // Q8: xhat comes from codes and scales, otherwise from x, mean and rstd. part (may be null) gets
 // the workgroup's partial dw and db, [gridDim.x][2][c].
-template <typename T, int V, int LPR, int NV, bool Q8>
+template <typename T, int V, int LPR, int NV, bool TAIL, bool Q8>
 __global__ __launch_bounds__(kNT) void k_norm_bwd(const T* __restrict__ dy, const T* __restrict__ x,
                                                   const float* __restrict__ mean, const int8_t* __restrict__ codes,
                                                   const float* __restrict__ scales, const float* __restrict__ rstd,
@@ -153,13 +156,14 @@ __global__ __launch_bounds__(kNT) void k_norm_bwd(const T* __restrict__ dy, cons
   const int groups = (c + kQ8Group - 1) / kQ8Group;
   float pw[NV][V], aw[NV][V], ab[NV][V];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    const RowPos<V, TAIL> e((j * LPR + l) * V, c);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int ch = (j * LPR + l) * V + i;
-      pw[j][i] = ch >= c ? 0.f : w ? load_param(w, ch, wf32) : 1.f;
+      pw[j][i] = !e.in ? 0.f : w ? load_param(w, e.at + i, wf32) : 1.f;
       aw[j][i] = ab[j][i] = 0.f;
     }
+  }
   for (int64_t r0 = (int64_t)blockIdx.x * SL; r0 < n; r0 += (int64_t)gridDim.x * SL) {
     const int64_t r = r0 + slot;
     const bool live = r < n;
@@ -169,44 +173,49 @@ __global__ __launch_bounds__(kNT) void k_norm_bwd(const T* __restrict__ dy, cons
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int ch = (j * LPR + l) * V;
-      const bool in = live && ch < c;
+      const int first = (j * LPR + l) * V;
+      const RowPos<V, TAIL> e(first, c);
 #pragma unroll
       for (int i = 0; i < V; ++i) g[j][i] = h[j][i] = 0.f;
-      if (in) {
-        load_vec<T, V>(dy + r * c + ch, g[j]);
+      if (live && e.in) {
+        load_vec<T, V>(dy + r * c + e.at, g[j]);
         if constexpr (Q8) {
-          load_codes<V>(codes + r * c + ch, h[j]);
-          const float sc = scales[r * groups + ch / kQ8Group];
+          load_codes<V>(codes + r * c + e.at, h[j]);
+          const float sc = scales[r * groups + first / kQ8Group];
+          const float before = TAIL ? scales[r * groups + e.at / kQ8Group] : sc;
 #pragma unroll
-          for (int i = 0; i < V; ++i) h[j][i] *= sc;
+          for (int i = 0; i < V; ++i) h[j][i] *= e.own(i) ? sc : before;
         } else {
-          load_vec<T, V>(x + r * c + ch, h[j]);
+          load_vec<T, V>(x + r * c + e.at, h[j]);
 #pragma unroll
           for (int i = 0; i < V; ++i) h[j][i] = (h[j][i] - mu) * rs;
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const RowPos<V, TAIL> e((j * LPR + l) * V, c);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        aw[j][i] = fmaf(g[j][i], h[j][i], aw[j][i]);
-        ab[j][i] += g[j][i];
+        const float gi = e.own(i) ? g[j][i] : 0.f;
+        aw[j][i] = fmaf(gi, h[j][i], aw[j][i]);
+        ab[j][i] += gi;
         g[j][i] *= pw[j][i];
-        s1 += g[j][i];
-        s2 = fmaf(g[j][i], h[j][i], s2);
+        const float gw = e.own(i) ? g[j][i] : 0.f;
+        s1 += gw;
+        s2 = fmaf(gw, h[j][i], s2);
       }
+    }
     row_sum2<LPR>(s1, s2, s_red);
     s1 *= inv_c;
     s2 *= inv_c;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int ch = (j * LPR + l) * V;
+      const RowPos<V, TAIL> e((j * LPR + l) * V, c);
       float o[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) o[i] = rs * fmaf(-h[j][i], s2, g[j][i] - s1);
-      if (live && ch < c) store_vec<T, V>(dx + r * c + ch, o);
+      if (live && e.in) store_vec<T, V>(dx + r * c + e.at, o);
     }
   }
   if (!part) return;
@@ -224,28 +233,29 @@ __global__ __launch_bounds__(kNT) void k_norm_bwd(const T* __restrict__ dy, cons
     }
   if constexpr (LPR == kNT) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const RowPos<V, TAIL> e((j * LPR + l) * V, c);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int ch = (j * LPR + l) * V + i;
-        if (ch < c) {
-          part[(size_t)blockIdx.x * 2 * c + ch] = aw[j][i];
-          part[(size_t)blockIdx.x * 2 * c + c + ch] = ab[j][i];
+      for (int i = 0; i < V; ++i)
+        if (e.in && e.own(i)) {
+          part[(size_t)blockIdx.x * 2 * c + e.at + i] = aw[j][i];
+          part[(size_t)blockIdx.x * 2 * c + c + e.at + i] = ab[j][i];
         }
-      }
+    }
   } else {
     for (int q = 0; q < kNT / 64; ++q) {
       if ((int)(threadIdx.x >> 6) == q && lane_id() < WL) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+          const RowPos<V, TAIL> e((j * LPR + l) * V, c);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int ch = (j * LPR + l) * V + i;
-            if (ch < c) {
+          for (int i = 0; i < V; ++i)
+            if (e.in && e.own(i)) {
+              const int ch = e.at + i;
               s_part[ch] = q ? s_part[ch] + aw[j][i] : aw[j][i];
               s_part[c + ch] = q ? s_part[c + ch] + ab[j][i] : ab[j][i];
             }
-          }
+        }
       }
       __syncthreads();
     }
@@ -279,59 +289,53 @@ __global__ __launch_bounds__(kNT) void k_norm_reduce(const float* __restrict__ p
 template <int V>
 using IntC = std::integral_constant<int, V>;
 
-// Calls f(V, LPR, NV) as compile-time integers for rows of c channels loaded V at a time.
+// Calls f(V, LPR, NV) as compile-time integers for rows of c channels loaded V at a time (V < 4: only the rows of
+// fewer than 4 channels).
 template <int V, typename F>
 void with_row_shape(int c, F f) {
   const int lanes = (c + V - 1) / V;  // loads of a row
   if (lanes <= 1) return f(IntC<V>{}, IntC<1>{}, IntC<1>{});
   if (lanes <= 2) return f(IntC<V>{}, IntC<2>{}, IntC<1>{});
-  if (lanes <= 4) return f(IntC<V>{}, IntC<4>{}, IntC<1>{});
-  if (lanes <= 8) return f(IntC<V>{}, IntC<8>{}, IntC<1>{});
-  if (lanes <= 16) return f(IntC<V>{}, IntC<16>{}, IntC<1>{});
-  if (lanes <= 32) return f(IntC<V>{}, IntC<32>{}, IntC<1>{});
-  if (lanes <= 64) return f(IntC<V>{}, IntC<64>{}, IntC<1>{});
-  if (lanes <= 128) return f(IntC<V>{}, IntC<64>{}, IntC<2>{});
-  if constexpr (V < 8) {
-    if (lanes <= 256) return f(IntC<V>{}, IntC<64>{}, IntC<4>{});
-    if constexpr (V < 4) {
-      if (lanes <= 512) return f(IntC<V>{}, IntC<64>{}, IntC<8>{});
-      if (lanes <= 1024) return f(IntC<V>{}, IntC<64>{}, IntC<16>{});
-      if (lanes <= 2048) return f(IntC<V>{}, IntC<kNT>{}, IntC<8>{});
-      return f(IntC<V>{}, IntC<kNT>{}, IntC<16>{});
-    } else {
+  if constexpr (V >= 4) {
+    if (lanes <= 4) return f(IntC<V>{}, IntC<4>{}, IntC<1>{});
+    if (lanes <= 8) return f(IntC<V>{}, IntC<8>{}, IntC<1>{});
+    if (lanes <= 16) return f(IntC<V>{}, IntC<16>{}, IntC<1>{});
+    if (lanes <= 32) return f(IntC<V>{}, IntC<32>{}, IntC<1>{});
+    if (lanes <= 64) return f(IntC<V>{}, IntC<64>{}, IntC<1>{});
+    if (lanes <= 128) return f(IntC<V>{}, IntC<64>{}, IntC<2>{});
+    if constexpr (V == 4) {
+      if (lanes <= 256) return f(IntC<V>{}, IntC<64>{}, IntC<4>{});
       if (lanes <= 512) return f(IntC<V>{}, IntC<kNT>{}, IntC<2>{});
       return f(IntC<V>{}, IntC<kNT>{}, IntC<4>{});
+    } else {
+      if (lanes <= 256) return f(IntC<V>{}, IntC<kNT>{}, IntC<1>{});
+      return f(IntC<V>{}, IntC<kNT>{}, IntC<2>{});
     }
-  } else {
-    if (lanes <= 256) return f(IntC<V>{}, IntC<kNT>{}, IntC<1>{});
-    return f(IntC<V>{}, IntC<kNT>{}, IntC<2>{});
   }
 }
 
-// Values per load: the widest that divides the row and that every pointer is aligned for.
-template <typename T>
-int row_vec(int c, const void* a, const void* b, const void* q) {
-  const uintptr_t p = (uintptr_t)a | (uintptr_t)b;
-  for (int v = 16 / (int)sizeof(T); v >= 4; v /= 2)
-    if (c % v == 0 && p % (v * sizeof(T)) == 0 && (uintptr_t)q % v == 0) return v;
-  return 1;
-}
-
+// Calls f(V, LPR, NV, TAIL): 16 bytes a load, less only for rows of fewer channels than that.
 template <typename T, typename F>
-void with_shape(int c, int vec, F f) {
+void with_shape(int c, F f) {
+  auto with = [&](auto V) {
+    with_row_shape<V>(c, [&](auto v, auto lpr, auto nv) {
+      if (c % v == 0) f(v, lpr, nv, std::false_type{});
+      else f(v, lpr, nv, std::true_type{});
+    });
+  };
   if constexpr (sizeof(T) == 2) {
-    if (vec == 8) return with_row_shape<8>(c, f);
+    if (c >= 8) return with(IntC<8>{});
   }
-  if (vec == 4) return with_row_shape<4>(c, f);
-  with_row_shape<1>(c, f);
+  if (c >= 4) return with(IntC<4>{});
+  if (c >= 2) return with(IntC<2>{});
+  with(IntC<1>{});
 }
 
 template <typename T, bool Q8>
 int norm_t(const NormArgs& a, hipStream_t s) {
-  const int vec = row_vec<T>(a.c, a.x, a.y, a.codes);
-  with_shape<T>(a.c, vec, [&](auto V, auto L, auto NV) {
+  with_shape<T>(a.c, [&](auto V, auto L, auto NV, auto TAIL) {
     const int64_t blocks = (a.n + kNT / L - 1) / (kNT / L);
-    k_norm<T, V, L, NV, Q8><<<(unsigned)std::min<int64_t>(blocks, 4096), kNT, 0, s>>>(
+    k_norm<T, V, L, NV, TAIL, Q8><<<(unsigned)std::min<int64_t>(blocks, 4096), kNT, 0, s>>>(
         (const T*)a.x, a.n, a.c, a.w, a.b, a.wf32, a.eps, (T*)a.y, a.mean, a.rstd, a.codes, a.scales);
   });
   IGC_HIP(hipGetLastError(), a.fn);
@@ -340,11 +344,10 @@ int norm_t(const NormArgs& a, hipStream_t s) {
 
 template <typename T, bool Q8>
 int norm_bwd_t(const NormArgs& a, void* ws, hipStream_t s) {
-  const int vec = row_vec<T>(a.c, Q8 ? a.y : a.x, (void*)((uintptr_t)a.dy | (uintptr_t)a.y), a.codes);
   const int parts = norm_bwd_parts(a.n, a.c);
   float* part = a.dw ? (float*)ws : nullptr;
-  with_shape<T>(a.c, vec, [&](auto V, auto L, auto NV) {
-    k_norm_bwd<T, V, L, NV, Q8><<<(unsigned)parts, kNT, 8 * (size_t)a.c, s>>>(
+  with_shape<T>(a.c, [&](auto V, auto L, auto NV, auto TAIL) {
+    k_norm_bwd<T, V, L, NV, TAIL, Q8><<<(unsigned)parts, kNT, 8 * (size_t)a.c, s>>>(
         (const T*)a.dy, (const T*)a.x, a.mean, a.codes, a.scales, a.rstd, a.w, a.wf32, a.n, a.c, (T*)a.y, part);
   });
   IGC_HIP(hipGetLastError(), a.fn);

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace igc {
 
 typedef __bf16 bf16_t;
@@ -12,16 +14,31 @@ typedef __bf16 bf16_t;
 // Channels of a row that share one scale of an 8-bit checkpoint.
 constexpr int kQ8Group = 64;
 
+// Vectors of V values at any address that T allows: global memory takes 16-byte accesses at every alignment, so
+// rows of an odd number of channels are read as wide as others (see RowPos).
 template <typename T, int V>
 struct VecOf {
-  typedef T type __attribute__((ext_vector_type(V)));
+  typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T))));
 };
 template <typename T>
 struct VecOf<T, 1> {
   typedef T type;
 };
 
-// V consecutive values at p (aligned to V * sizeof(T)) as floats.
+// Where a lane's V channels of a row of c >= V channels lie: from `first` on, where its turn comes, or, at the end of a
+// row that V does not divide, the row's last V; the first `skip` of them belong to the lane before, which
+// computes and stores the same values, and stay out of every sum.
+template <int V, bool TAIL>
+struct RowPos {
+  int at, skip;
+  bool in;
+  __device__ __forceinline__ RowPos(int first, int c) : at(first), skip(0), in(first < c) {
+    if (TAIL && in && first + V > c) at = c - V, skip = first - at;
+  }
+  __device__ __forceinline__ bool own(int i) const { return !TAIL || i >= skip; }
+};
+
+// V consecutive values at p as floats.
 template <typename T, int V>
 __device__ __forceinline__ void load_vec(const T* p, float (&v)[V]) {
   const typename VecOf<T, V>::type t = *(const typename VecOf<T, V>::type*)p;
@@ -98,41 +115,36 @@ __device__ __forceinline__ int q8_code(float x, float inv) {
   return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
-// V codes to / from memory (p aligned to V bytes).
+// V codes to memory, without the first `skip` (their group may be another).
 template <int V>
-__device__ __forceinline__ void store_codes(int8_t* p, const float (&x)[V], float inv) {
-  if constexpr (V == 1) {
-    *p = (int8_t)q8_code(x[0], inv);
-  } else {
-    uint32_t w[V / 4];
+__device__ __forceinline__ void store_codes(int8_t* p, const float (&x)[V], float inv, int skip) {
+  typedef int8_t i8x __attribute__((ext_vector_type(V < 2 ? 2 : V), aligned(1)));
+  typedef uint32_t u32u __attribute__((aligned(1)));
+  typedef uint16_t u16u __attribute__((aligned(1)));
+  uint64_t w = 0;
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      w[i] = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)q8_code(x[4 * i + j], inv) & 0xFFu) << (8 * j);
-    }
-    if constexpr (V == 4) *(uint32_t*)p = w[0];
-    else if constexpr (V == 8) *(uint2*)p = make_uint2(w[0], w[1]);
-    else *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < V; ++i) w |= (uint64_t)((uint32_t)q8_code(x[i], inv) & 0xFFu) << (8 * i);
+  if (skip == 0) {
+    if constexpr (V == 1) *p = (int8_t)w;
+    else *(i8x*)p = __builtin_bit_cast(i8x, typename std::conditional<V == 8, uint64_t, typename std::conditional<V == 4, uint32_t, uint16_t>::type>::type(w));
+    return;
   }
+  p += skip;
+  w >>= 8 * skip;
+  const int n = V - skip;
+  if (n & 4) *(u32u*)p = (uint32_t)w, p += 4, w >>= 32;
+  if (n & 2) *(u16u*)p = (uint16_t)w, p += 2, w >>= 16;
+  if (n & 1) *p = (int8_t)w;
 }
 template <int V>
 __device__ __forceinline__ void load_codes(const int8_t* p, float (&v)[V]) {
+  typedef int8_t i8x __attribute__((ext_vector_type(V < 2 ? 2 : V), aligned(1)));
   if constexpr (V == 1) {
     v[0] = (float)*p;
   } else {
-    uint32_t w[V / 4];
-    if constexpr (V == 4) {
-      w[0] = *(const uint32_t*)p;
-    } else if constexpr (V == 8) {
-      const uint2 t = *(const uint2*)p;
-      w[0] = t.x, w[1] = t.y;
-    } else {
-      const uint4 t = *(const uint4*)p;
-      w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
-    }
+    const i8x t = *(const i8x*)p;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = (float)(int8_t)(w[i / 4] >> (8 * (i & 3)));
+    for (int i = 0; i < V; ++i) v[i] = (float)t[i];
   }
 }
 
