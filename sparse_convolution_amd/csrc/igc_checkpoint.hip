@@ -16,6 +16,10 @@ namespace {
 
 constexpr int kNT = 256;
 
+// Two tiles a workgroup once there are more than fill the GPU. Pack and restore of 128 M values, bf16 / fp32, us: 143 / 240; one
+// tile 148 / 254, four 147 / 243, at most 8192 and 16384 workgroups 152 / 270.
+unsigned wgs_for(int64_t tiles) { return (unsigned)std::max<int64_t>(std::min<int64_t>(tiles, 2048), (tiles + 1) / 2); }
+
 // GL lanes hold a group of up to 64 channels, V each; unit u = (row, group).
 template <typename T, int V, int GL, bool TAIL>
 __global__ __launch_bounds__(kNT) void k_pack(const T* __restrict__ x, uint32_t units, int c, int groups,
@@ -68,7 +72,7 @@ void pack_go(const T* x, int64_t n, int c, int8_t* codes, float* scales, hipStre
   for (int64_t r = 0; r < n; r += (int64_t)1 << 25) {
     const int64_t rows = std::min<int64_t>(n - r, (int64_t)1 << 25);
     const uint32_t units = (uint32_t)(rows * groups);
-    const unsigned blocks = (unsigned)std::min<int64_t>(((int64_t)units + kNT / GL - 1) / (kNT / GL), 8192);
+    const unsigned blocks = wgs_for(((int64_t)units + kNT / GL - 1) / (kNT / GL));
     const T* xr = x + r * c;
     if (c % V == 0) k_pack<T, V, GL, false><<<blocks, kNT, 0, s>>>(xr, units, c, groups, codes + r * c, scales + r * groups);
     else k_pack<T, V, GL, true><<<blocks, kNT, 0, s>>>(xr, units, c, groups, codes + r * c, scales + r * groups);
@@ -91,7 +95,7 @@ template <typename T, int V>
 void unpack_v(const int8_t* codes, const float* scales, int64_t n, int c, T* x, hipStream_t s) {
   const int per_row = (c + V - 1) / V, groups = (c + kQ8Group - 1) / kQ8Group;
   const int64_t items = n * per_row;
-  const unsigned blocks = (unsigned)std::min<int64_t>((items + kNT - 1) / kNT, 16384);
+  const unsigned blocks = wgs_for((items + kNT - 1) / kNT);
   if (c % V == 0) k_unpack<T, V, false><<<blocks, kNT, 0, s>>>(codes, scales, items, per_row, c, groups, x);
   else k_unpack<T, V, true><<<blocks, kNT, 0, s>>>(codes, scales, items, per_row, c, groups, x);
 }

@@ -148,9 +148,17 @@ __device__ __forceinline__ void load_codes(const int8_t* p, float (&v)[V]) {
   }
 }
 
-// Channel i of a weight or bias vector held in fp32 or in the features' type.
-__device__ __forceinline__ float load_param(const void* p, int i, bool f32) {
-  return f32 ? ((const float*)p)[i] : (float)((const bf16_t*)p)[i];
+// V channels of a weight or bias vector held in fp32 or in bf16, `none` where there is no vector.
+template <int V>
+__device__ __forceinline__ void load_params(const void* p, int at, bool f32, float none, float (&v)[V]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = none;
+  } else if (f32) {
+    load_vec<float, V>((const float*)p + at, v);
+  } else {
+    load_vec<bf16_t, V>((const bf16_t*)p + at, v);
+  }
 }
 
 }  // namespace igc
