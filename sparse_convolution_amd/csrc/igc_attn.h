@@ -190,6 +190,16 @@ __device__ __forceinline__ Frag<T> to_frag(const f32x16& s, int m) {
   }
 }
 
+// The same as two operands, the rounded values and what the rounding left (fp32 data: all in the first).
+template <typename T>
+__device__ __forceinline__ void to_frag2(const f32x16& s, int m, Frag<T>& hi, Frag<T>& lo) {
+  hi = to_frag<T>(s, m);
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo.p[0][i] = (bf16_t)(s[8 * m + i] - (float)hi.p[0][i]);
+  }
+}
+
 // Largest of a tile's 16 registers. Not as inline assembly, which would save passing the operands through a
 // maximum with themselves first: the compiler places no wait between a matrix instruction and assembly that
 // reads its result.
