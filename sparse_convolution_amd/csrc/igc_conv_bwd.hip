@@ -452,6 +452,14 @@ int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const FeatsIn&
     if (dtype == IGC_BF16) {
       // 128 x 256 blocks on 8 waves (85 FLOP per staged byte instead of 64) measured slower on
       // the large workload (222 ms against 214): staging is not bound by the L2 feed.
+      if (feats.codes && cin % 128 == 0 && cout % 128 == 0) {
+        // From 8 bits, small grids: 27 workgroups per 11 tiles of 256 rows leave the GPU idle, and smaller blocks of the
+        // weight gradient give more of them for the same sums. 128 -> 128, us with 128 x 128 / 64 x 128 / 64 x 64: 1,024
+        // voxels 37 / 28 / 23, 10,000 107 / 80 / 68, 43,264 123 / 111 / 124, 169,744 260 / 311 / 393.
+        const int64_t blocks = (g->n_voxels + 11 * kTileRows - 1) / (11 * kTileRows) * (cin / 128) * (cout / 128);
+        if (blocks <= 8) return launch_wgrad_bf16<64, 64, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
+        if (blocks <= 24) return launch_wgrad_bf16<64, 128, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
+      }
       if (cin % 128 == 0 && cout % 128 == 0)
         return launch_wgrad_bf16<128, 128, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
       if (cin % 64 == 0) return launch_wgrad_bf16<64, 64, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
