@@ -40,6 +40,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kNOff = 27;
 constexpr int kTileRows = 256;  // rows of a plan tile
 constexpr int kStage = 64;      // rows staged at a time
+constexpr int kBatch = 8;       // tiles whose rows are listed in LDS at a time (8-bit input)
 constexpr int kLdT = kStage + 8;  // LDS row stride of the transposed stages (bf16): 144 bytes
 
 // wf[o][co][ci] = w[26 - o][ci][co].
@@ -82,6 +83,10 @@ struct WgradSplit {
 // smaller blocks already run six or eight waves per SIMD. Four waves spill.
 // Q8: the input rows come from an 8-bit checkpoint (codes and per-64-channel scales): half the
 // gathered bytes, restored to the bf16 values the checkpoint stands for on the way into LDS.
+// They are then also walked in batches of kBatch tiles whose row order and source rows are read into LDS
+// at once: each stage's loads then depend on LDS only, and two stages of them are in flight, where the
+// chain of row order, map and data costs a memory round trip per stage. Kernel, us, before and after: 128 -> 128
+// on 43,264 voxels 111 and 88, on 169,744 260 and 215; 64 -> 64 on 43,264 69 and 48. Batches of 12: 86, 236 and 48.
 template <int MB, int NB, int NWV, bool Q8>
 __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) void k_wgrad_bf16(const int32_t* __restrict__ map, int64_t N,
                                                     const int32_t* __restrict__ perm,
@@ -143,7 +148,9 @@ __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) v
     }
   };
   auto load_src = [&](int32_t r, int32_t& src) { src = r >= 0 ? map_o[r] : -1; };
-  uint4 xa[XI], xb[XI], da[DI], db[DI];  // stage data: rows 2 pr (a) and 2 pr + 1 (b)
+  struct StageData {
+    uint4 xa[XI], xb[XI], da[DI], db[DI];  // rows 2 pr (a) and 2 pr + 1 (b)
+  };
   const int qgroups = (cin + kQ8Group - 1) / kQ8Group;
   // Q8: 8 codes and, in .z, their scale; restored when the stage is written to LDS.
   auto load_q8 = [&](int32_t r, int g) -> uint4 {
@@ -157,25 +164,25 @@ __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) v
     for (int i = 0; i < 8; ++i) v[i] = (__bf16)((float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3))) * sc);
     return __builtin_bit_cast(uint4, v);
   };
-  auto load_data = [&](int32_t r0, int32_t r1, int32_t s0, int32_t s1) {
+  auto load_data = [&](StageData& t, int32_t r0, int32_t r1, int32_t s0, int32_t s1) {
 #pragma unroll
     for (int j = 0; j < XI; ++j) {
       const int g = (tid >> 5) + GS * j;
       const bool ok = 32 * XG >= NT || g < XG;
       if constexpr (Q8) {
-        xa[j] = ok && s0 >= 0 ? load_q8(s0, g) : make_uint4(0, 0, 0, 0);
-        xb[j] = ok && s1 >= 0 ? load_q8(s1, g) : make_uint4(0, 0, 0, 0);
+        t.xa[j] = ok && s0 >= 0 ? load_q8(s0, g) : make_uint4(0, 0, 0, 0);
+        t.xb[j] = ok && s1 >= 0 ? load_q8(s1, g) : make_uint4(0, 0, 0, 0);
       } else {
-        xa[j] = ok && s0 >= 0 ? *(const uint4*)(feats + (size_t)s0 * cin + c0 + g * 8) : make_uint4(0, 0, 0, 0);
-        xb[j] = ok && s1 >= 0 ? *(const uint4*)(feats + (size_t)s1 * cin + c0 + g * 8) : make_uint4(0, 0, 0, 0);
+        t.xa[j] = ok && s0 >= 0 ? *(const uint4*)(feats + (size_t)s0 * cin + c0 + g * 8) : make_uint4(0, 0, 0, 0);
+        t.xb[j] = ok && s1 >= 0 ? *(const uint4*)(feats + (size_t)s1 * cin + c0 + g * 8) : make_uint4(0, 0, 0, 0);
       }
     }
 #pragma unroll
     for (int j = 0; j < DI; ++j) {
       const int g = (tid >> 5) + GS * j;
       const bool ok = 32 * DG >= NT || g < DG;
-      da[j] = ok && s0 >= 0 ? *(const uint4*)(dout + (size_t)r0 * cout + n0 + g * 8) : make_uint4(0, 0, 0, 0);
-      db[j] = ok && s1 >= 0 ? *(const uint4*)(dout + (size_t)r1 * cout + n0 + g * 8) : make_uint4(0, 0, 0, 0);
+      t.da[j] = ok && s0 >= 0 ? *(const uint4*)(dout + (size_t)r0 * cout + n0 + g * 8) : make_uint4(0, 0, 0, 0);
+      t.db[j] = ok && s1 >= 0 ? *(const uint4*)(dout + (size_t)r1 * cout + n0 + g * 8) : make_uint4(0, 0, 0, 0);
     }
   };
   // Transposed store: channel c of granule g gets the pair (row 2 pr, row 2 pr + 1) as one word.
@@ -194,47 +201,23 @@ __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) v
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // Prologue: data of the first stage, source rows of the second, row order of the third.
-  int64_t cur = next_stage();
-  int64_t nx1 = next_stage();
-  int64_t nx2 = next_stage();
-  int32_t r0, r1, s0, s1;
-  load_perm(cur, r0, r1);
-  load_src(r0, s0);
-  load_src(r1, s1);
-  load_data(r0, r1, s0, s1);
-  int32_t m_r0, m_r1, m_s0, m_s1;  // stage nx1
-  load_perm(nx1, m_r0, m_r1);
-  load_src(m_r0, m_s0);
-  load_src(m_r1, m_s1);
-  int32_t p_r0, p_r1;  // stage nx2
-  load_perm(nx2, p_r0, p_r1);
-
   const int frow = lane & 15, fk = (lane >> 4) * 8;
-  while (cur >= 0) {
-    __syncthreads();  // the previous stage's LDS reads are done
+  auto store_stage = [&](const StageData& t) {
 #pragma unroll
     for (int j = 0; j < XI; ++j) {
       const int g = (tid >> 5) + GS * j;
       if (32 * XG >= NT || g < XG) {
-        if constexpr (Q8) store_pair(s_xt, g, restore(xa[j]), restore(xb[j]));
-        else store_pair(s_xt, g, xa[j], xb[j]);
+        if constexpr (Q8) store_pair(s_xt, g, restore(t.xa[j]), restore(t.xb[j]));
+        else store_pair(s_xt, g, t.xa[j], t.xb[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < DI; ++j) {
       const int g = (tid >> 5) + GS * j;
-      if (32 * DG >= NT || g < DG) store_pair(s_dt, g, da[j], db[j]);
+      if (32 * DG >= NT || g < DG) store_pair(s_dt, g, t.da[j], t.db[j]);
     }
-    // Loads for the next stages.
-    load_data(m_r0, m_r1, m_s0, m_s1);
-    m_r0 = p_r0;
-    m_r1 = p_r1;
-    load_src(m_r0, m_s0);
-    load_src(m_r1, m_s1);
-    const int64_t nx3 = next_stage();
-    load_perm(nx3, p_r0, p_r1);
-    __syncthreads();
+  };
+  auto multiply = [&]() {
 #pragma unroll
     for (int ks = 0; ks < kStage; ks += 32) {
       bf16x8 a[MI], b[NI];
@@ -250,9 +233,88 @@ __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) v
         for (int ni = 0; ni < NI; ++ni)
           acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[mi], b[ni], acc[mi][ni], 0, 0, 0);
     }
-    cur = nx1;
-    nx1 = nx2;
-    nx2 = nx3;
+  };
+
+  if constexpr (Q8) {
+    __shared__ int2 s_pair[kBatch * kTileRows];  // (row, source row) of the batch in plan order
+    StageData t0d, t1d;
+    auto load_stage = [&](StageData& t, int st) {
+      const int2 a = s_pair[st * kStage + 2 * pr], b = s_pair[st * kStage + 2 * pr + 1];
+      load_data(t, a.x, b.x, a.y, b.y);
+    };
+    for (int64_t tb = t0; tb < t1; tb += kBatch) {
+      const int tiles = (int)(t1 - tb < kBatch ? t1 - tb : kBatch);
+      int32_t r[kBatch * kTileRows / NT];
+      __syncthreads();  // the previous batch's lists have been read
+#pragma unroll
+      for (int i = 0; i < kBatch * kTileRows / NT; ++i)
+        r[i] = i * NT < tiles * kTileRows ? perm[tb * kTileRows + i * NT + tid] : -1;
+#pragma unroll
+      for (int i = 0; i < kBatch * kTileRows / NT; ++i)
+        s_pair[i * NT + tid] = make_int2(r[i], r[i] >= 0 ? map_o[r[i]] : -1);
+      // Stages of the batch that hold a pair, one bit each.
+      const bool some = lane < tiles * 4 && (blk[(tb + (lane >> 2)) * kNOff + o] >> ((lane & 3) * 4) & 0xFu);
+      uint64_t todo = __ballot(some);
+      __syncthreads();
+      auto take = [&]() {
+        const int st = __ffsll((unsigned long long)todo) - 1;
+        todo &= todo - 1;
+        return st;
+      };
+      auto one = [&](StageData& t) {
+        __syncthreads();  // the previous stage's LDS reads are done
+        store_stage(t);
+        if (todo) load_stage(t, take());
+        __syncthreads();
+        multiply();
+      };
+      int left = __popcll(todo);
+      if (left > 0) load_stage(t0d, take());
+      if (left > 1) load_stage(t1d, take());
+      for (; left > 0; left -= 2) {
+        one(t0d);
+        if (left > 1) one(t1d);
+      }
+    }
+  } else {
+    // Prologue: data of the first stage, source rows of the second, row order of the third.
+    int64_t cur = next_stage();
+    int64_t nx1 = next_stage();
+    int64_t nx2 = next_stage();
+    StageData t0d;
+    int32_t r0, r1, s0, s1;
+    load_perm(cur, r0, r1);
+    load_src(r0, s0);
+    load_src(r1, s1);
+    load_data(t0d, r0, r1, s0, s1);
+    int32_t m_r0, m_r1, m_s0, m_s1;  // stage nx1
+    load_perm(nx1, m_r0, m_r1);
+    load_src(m_r0, m_s0);
+    load_src(m_r1, m_s1);
+    int32_t p_r0, p_r1;  // stage nx2
+    load_perm(nx2, p_r0, p_r1);
+    // One stage: t into LDS, the loads of a later stage into t, the products.
+    auto stage = [&](StageData& t) -> int64_t {
+      __syncthreads();  // the previous stage's LDS reads are done
+      store_stage(t);
+      // Loads for the next stages.
+      load_data(t, m_r0, m_r1, m_s0, m_s1);
+      m_r0 = p_r0;
+      m_r1 = p_r1;
+      load_src(m_r0, m_s0);
+      load_src(m_r1, m_s1);
+      const int64_t next = next_stage();
+      load_perm(next, p_r0, p_r1);
+      __syncthreads();
+      multiply();
+      return next;
+    };
+    while (cur >= 0) {
+      const int64_t nx3 = stage(t0d);
+      cur = nx1;
+      nx1 = nx2;
+      nx2 = nx3;
+    }
   }
   // D layout: lane holds column lane%16 of rows 4*(lane/16) + j.
   float* dst = part + ((size_t)chunk * kNOff + o) * (size_t)cin * cout;
@@ -455,7 +517,7 @@ int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const FeatsIn&
       if (feats.codes && cin % 128 == 0 && cout % 128 == 0) {
         // From 8 bits, small grids: 27 workgroups per 11 tiles of 256 rows leave the GPU idle, and smaller blocks of the
         // weight gradient give more of them for the same sums. 128 -> 128, us with 128 x 128 / 64 x 128 / 64 x 64: 1,024
-        // voxels 37 / 28 / 23, 10,000 107 / 80 / 68, 43,264 123 / 111 / 124, 169,744 260 / 311 / 393.
+        // voxels 30 / 21 / 16, 10,000 79 / 57 / 48, 43,264 96 / 88 / 104, 169,744 216 / 265 / 327.
         const int64_t blocks = (g->n_voxels + 11 * kTileRows - 1) / (11 * kTileRows) * (cin / 128) * (cout / 128);
         if (blocks <= 8) return launch_wgrad_bf16<64, 64, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
         if (blocks <= 24) return launch_wgrad_bf16<64, 128, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
