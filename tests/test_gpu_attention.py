@@ -323,3 +323,33 @@ def test_other_stream_repeat_and_graph_are_bit_identical(lq, lk):
         torch.cuda.synchronize()
         for a, b in zip(kept, both()):
             assert torch.equal(a, b), n
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_caches_past_2_to_the_31_elements(rows):
+    # The states of the last sequence lie beyond element 2^31 of k and v (4.4 GB each); the same states in a
+    # small tensor of their own give the same bits.
+    igc = _igc()
+    heads, dim, nk, last = 8, 128, 2150000, 900
+    k = torch.zeros(nk, heads, dim, dtype=BF16, device="cuda")
+    v = torch.zeros(nk, heads, dim, dtype=BF16, device="cuda")
+    assert (nk - last) * heads * dim > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k[-last:] = torch.randn(last, heads, dim, generator=g, device="cuda").to(BF16)
+    v[-last:] = torch.randn(last, heads, dim, generator=g, device="cuda").to(BF16)
+    q = torch.randn(rows, heads, dim, generator=g, device="cuda").to(BF16)
+    do = torch.randn(rows, heads, dim, generator=g, device="cuda").to(BF16)
+    kl, vl = k[-last:].clone(), v[-last:].clone()
+    # Two empty sequences around one, so that the number of parts is decided from the same averages.
+    qo = torch.tensor([0, 0, rows], dtype=torch.int32, device="cuda")
+    ko = torch.tensor([0, nk - last, nk], dtype=torch.int32, device="cuda")
+    out, lse = igc.cross_attention(q, k, v, qo, ko)
+    ref, rlse = igc.cross_attention(q, kl, vl)
+    # Other parts of the key axis, so equal up to their order: fp32 sums and one rounding to bf16.
+    assert float((lse - rlse).abs().max()) < 1e-4
+    assert float((out.float() - ref.float()).abs().max()) <= 2 * U[BF16] * float(ref.float().abs().max())
+    dq, dk, dv = igc.cross_attention_backward(do, q, k, v, out, lse, qo, ko)
+    rq, rk, rv = igc.cross_attention_backward(do, q, kl, vl, out, lse)
+    assert bool((dk[:nk - last] == 0).all()) and bool((dv[:nk - last] == 0).all())
+    for a, b in ((dq, rq), (dk[-last:], rk), (dv[-last:], rv)):
+        assert float((a.float() - b.float()).abs().max()) <= 4 * U[BF16] * float(b.float().abs().max())

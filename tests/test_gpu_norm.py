@@ -213,3 +213,21 @@ def test_captured_in_a_graph():
         rx, rw, rb = igc.layer_norm_backward(dy, x, rm, rr, w)
         for a, e in ((y, ry), (dx, rx), (dw, rw), (db, rb)):
             assert torch.equal(a, e), k
+
+
+def test_arrays_past_2_to_the_31_elements():
+    igc = _igc()
+    n, c = 2100001, 1024
+    assert n * c > 2 ** 31
+    x = torch.zeros(n, c, dtype=BF16, device="cuda")
+    x[-500:] = torch.randn(500, c, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(BF16)
+    y, mean, rstd = igc.layer_norm(x)
+    yl, ml, rl = igc.layer_norm(x[-500:].contiguous())
+    assert torch.equal(y[-500:], yl) and torch.equal(mean[-500:], ml) and torch.equal(rstd[-500:], rl)
+    dx, dw, db = igc.layer_norm_backward(x, x, mean, rstd)
+    dl, wl, bl = igc.layer_norm_backward(x[-500:].contiguous(), x[-500:].contiguous(), ml, rl)
+    assert torch.equal(dx[-500:], dl)
+    # All other rows are zero: the same sums, grouped differently (fp32 in a lane, fp64 across workgroups).
+    assert float((dw - wl).abs().max()) <= 1e-5 * 500 and float((db - bl).abs().max()) <= 1e-5 * 500
+    ck = igc.checkpoint_pack(x)
+    assert torch.equal(igc.checkpoint_unpack(ck)[-500:], igc.checkpoint_unpack(igc.checkpoint_pack(x[-500:].contiguous())))
