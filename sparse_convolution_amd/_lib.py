@@ -103,9 +103,9 @@ def load() -> ctypes.CDLL:
         "igc_layer_norm_q8_backward": [P, P, P, P, i64, i32, i32, P, i32, P, P, P, P, size, P],
         "igc_checkpoint_pack": [P, i64, i32, i32, P, P, P],
         "igc_checkpoint_unpack": [P, P, i64, i32, i32, P, P],
-        "igc_cross_attention_workspace": [ctypes.POINTER(Attention), i32, ctypes.POINTER(size)],
-        "igc_cross_attention": [ctypes.POINTER(Attention), P, P, P, P, P, P, size, P],
-        "igc_cross_attention_backward": [ctypes.POINTER(Attention), P, P, P, P, P, P, P, P, P, P, size, P],
+        "igc_cross_attention_workspace": [P, i32, ctypes.POINTER(size)],
+        "igc_cross_attention": [P, P, P, P, P, P, P, size, P],
+        "igc_cross_attention_backward": [P, P, P, P, P, P, P, P, P, P, P, size, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
