@@ -8,6 +8,10 @@
 // Two kernels, each keeping its output in registers while it walks the other axis: k_attn_dq owns
 // query rows and walks keys, k_attn_dkv owns keys and walks query rows, so nothing is added by atomics
 // and reruns are bit-identical. Scores are computed again in both (seven products instead of five).
+//
+// p is rounded to bf16 for dv; ds is kept in two bf16 parts for dq, and for dk with few keys (see there),
+// since its terms cancel. Bound like the forward pass, by the vector unit beside the matrix cores: bf16,
+// 100,003 queries, 4 heads on 2 key heads of 64, three sequences of ~800 keys: dq 240 us, dk and dv 263, sums 7.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -377,8 +381,8 @@ void sum_go(const float* part0, const float* part1, int splits, int64_t n, int d
 }
 
 // Tiles of the two kernels: 32 NQ (NK) query rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
-// bf16, measured on 60,000 queries x 1,500 keys and 256 channels (dq / dkv, us): heads of 32: dq 209 with three waves,
-// 228 with NQ 2; dkv 286 with NK 2, 346 with NK 1. Heads of 64: dq 175 with NQ 2 on 32-key tiles, 184 on 64, 187 with NQ 1;
+// bf16, measured on 60,000 queries x 1,500 keys and 256 channels (dq / dkv, us; dq with ds rounded once, a quarter less than
+// with two parts): heads of 32: dq 209 with three waves, 228 with NQ 2; dkv 286 with NK 2, 346 with NK 1. Heads of 64: dq 175 with NQ 2 on 32-key tiles, 184 on 64, 187 with NQ 1;
 // dkv 231, with NK 2 (one wave) 317, on 32-row tiles 254. Heads of 128: dq 184 with two waves, 242 with one; dkv 290 with
 // one wave, 470 with two (spills).
 template <typename T, int DP>

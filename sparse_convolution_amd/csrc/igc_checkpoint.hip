@@ -2,7 +2,8 @@
 // the backward pass.
 //
 // Groups of 64 consecutive channels of a row share one fp32 scale (the last group of a row may
-// be shorter); see q8_scale for the formula. Memory bound: each value is read and written once.
+// be shorter); see q8_scale for the formula. Memory bound: each value is read and written once. 4,100,003 fp32 rows of
+// 16: pack 75 us, 4.6 TB/s, restore 54 us, 6.4 TB/s; 2,000,003 bf16 rows of 128: restore 129 us, 6.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -18,7 +19,9 @@ constexpr int kNT = 256;
 
 // Two tiles a workgroup once there are more than fill the GPU. Pack and restore of 128 M values, bf16 / fp32, us: 143 / 240; one
 // tile 148 / 254, four 147 / 243, at most 8192 and 16384 workgroups 152 / 270.
-unsigned wgs_for(int64_t tiles) { return (unsigned)std::max<int64_t>(std::min<int64_t>(tiles, 2048), (tiles + 1) / 2); }
+unsigned wgs_for(int64_t tiles) {
+  return (unsigned)std::min(std::max<int64_t>(std::min<int64_t>(tiles, 2048), (tiles + 1) / 2), kMaxWgs);
+}
 
 // GL lanes hold a group of up to 64 channels, V each; unit u = (row, group).
 template <typename T, int V, int GL, bool TAIL>

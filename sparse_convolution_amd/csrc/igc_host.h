@@ -191,6 +191,10 @@ int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const FeatsIn&
                          const void* d_w, int32_t cout, const void* d_dout, void* d_dfeats, float* d_dw,
                          int32_t dgrad_path, hipStream_t s);
 
+// Workgroups of 256 threads that a kernel striding over its work is launched with at most: a launch takes fewer than
+// 2^32 threads along an axis.
+constexpr int64_t kMaxWgs = (int64_t)1 << 23;
+
 // 8-bit activation checkpoints (igc_checkpoint.hip).
 int launch_pack(const void* x, int32_t dtype, int64_t n, int32_t c, int8_t* codes, float* scales, hipStream_t s);
 int launch_unpack(const int8_t* codes, const float* scales, int64_t n, int32_t c, int32_t dtype, void* x, hipStream_t s);

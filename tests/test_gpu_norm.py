@@ -231,3 +231,20 @@ def test_arrays_past_2_to_the_31_elements():
     assert float((dw - wl).abs().max()) <= 1e-5 * 500 and float((db - bl).abs().max()) <= 1e-5 * 500
     ck = igc.checkpoint_pack(x)
     assert torch.equal(igc.checkpoint_unpack(ck)[-500:], igc.checkpoint_unpack(igc.checkpoint_pack(x[-500:].contiguous())))
+
+
+def test_more_rows_than_one_launch_has_threads_for():
+    # 64 lanes a row and two rows a lane would be more than 2^32 threads, so the workgroups take more rows each (140 GB).
+    igc = _igc()
+    n, c, block = 135000003, 129, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = torch.randn(block, c, generator=g, device="cuda")
+    x = torch.empty(n, c, device="cuda")
+    for at in range(0, n, block):
+        x[at:at + block] = rows[:min(block, n - at)]
+    y, mean, rstd = igc.layer_norm(x)
+    ry, rm, rr = igc.layer_norm(rows)
+    last = (n - 1) // block * block
+    for at in (0, last // 2 // block * block, last - block, last):
+        k = min(block, n - at)
+        assert torch.equal(y[at:at + k], ry[:k]) and torch.equal(mean[at:at + k], rm[:k]) and torch.equal(rstd[at:at + k], rr[:k])
