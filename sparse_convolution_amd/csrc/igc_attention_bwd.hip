@@ -11,7 +11,7 @@
 //
 // p is rounded to bf16 for dv; ds is kept in two bf16 parts for dq, and for dk with few keys (see there),
 // since its terms cancel. Bound like the forward pass, by the vector unit beside the matrix cores: bf16,
-// 100,003 queries, 4 heads on 2 key heads of 64, three sequences of ~800 keys: dq 240 us, dk and dv 263, sums 7.
+// 100,003 queries, 4 heads on 2 key heads of 64, three sequences of ~800 keys: dq 229 us, dk and dv 223, sums 7.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -184,7 +184,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 }
 
 // dk and dv: four waves of 32 NK keys each over tiles of BQ query rows of the sequence. FINE: ds in two parts for the
-// product with q, as for dq; with few keys its terms cancel too.
+// product with q, as for dq; with few keys its terms cancel too. A score costs its exponential, two multiplications and
+// two roundings: the products with dout start from -delta (read into their accumulators from LDS), and what the mask leaves out is
+// cleared in the results instead of per score (100,003 queries, three sequences of ~800 keys, 4 heads of 64: 252 and 223 us).
 template <typename T, int DP, int NK, int BQ, int WPE, bool FINE, bool VEC>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
   typedef Frag<T> frag;
@@ -195,7 +197,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE)];
   auto s_q = [&](int buf) { return (bf16_t*)s_mem + buf * TILE; };
   auto s_o = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
-  __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];  // s_delta: -delta
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
   const int kh = blockIdx.x % a.kv_heads;
@@ -228,7 +230,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         split_row(r0 + t0 + threadIdx.x, a.group, qi, g);
         const int64_t at = (q0 + qi) * a.heads + kh * a.group + g;
         n_lse = lse_base2(a.lse_in[at]);
-        n_delta = a.delta[at];
+        n_delta = -a.delta[at];
       }
     }
   };
@@ -272,7 +274,15 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     for (int t = 0; t < QT; ++t) {
       f32x16 s[NK], dp[NK];
 #pragma unroll
-      for (int n = 0; n < NK; ++n) s[n] = zero16(), dp[n] = zero16();
+      for (int n = 0; n < NK; ++n) {
+        s[n] = zero16();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4v x = *(const f32x4v*)&s_delta[buf][t * 32 + 8 * g + 4 * h];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dp[n][4 * g + i] = x[i];
+        }
+      }
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
         const int at = (t * 32 + (lane & 31)) * LD + kk * 16 + h * 8;
@@ -286,13 +296,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4v lse = *(const f32x4v*)&s_lse[buf][t * 32 + 8 * g + 4 * h];
-        const f32x4v delta = *(const f32x4v*)&s_delta[buf][t * 32 + 8 * g + 4 * h];
 #pragma unroll
         for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = keep[n] ? __builtin_amdgcn_exp2f(fmaf(s[n][4 * g + i], c, -lse[i])) : 0.f;
-            dp[n][4 * g + i] = p * (dp[n][4 * g + i] - delta[i]);
+            // Of a key that the mask leaves out this may be anything: it stays in the key's own results.
+            const float p = __builtin_amdgcn_exp2f(fmaf(s[n][4 * g + i], c, -lse[i]));
+            dp[n][4 * g + i] *= p;
             s[n][4 * g + i] = p;
           }
       }
@@ -324,6 +334,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
   for (int n = 0; n < NK; ++n) {
     const int64_t row = key[n] < 0 ? -1 : key[n] * a.kv_heads + kh;
+    if (!keep[n]) {
+#pragma unroll
+      for (int t = 0; t < DT; ++t) dk[n][t] = zero16(), dv[n][t] = zero16();
+    }
     if (a.splits > 1) {
       const int64_t first = (int64_t)split * a.nk * a.kv_heads * a.dim;
       store_tile<float, DP>(a.part_a + first, s_out, dk[n], a.scale, row, a.dim, a.dim % 4 == 0);
@@ -381,8 +395,9 @@ void sum_go(const float* part0, const float* part1, int splits, int64_t n, int d
 }
 
 // Tiles of the two kernels: 32 NQ (NK) query rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
-// bf16, measured on 60,000 queries x 1,500 keys and 256 channels (dq / dkv, us; dq with ds rounded once, a quarter less than
-// with two parts): heads of 32: dq 209 with three waves, 228 with NQ 2; dkv 286 with NK 2, 346 with NK 1. Heads of 64: dq 175 with NQ 2 on 32-key tiles, 184 on 64, 187 with NQ 1;
+// bf16, measured on 60,000 queries x 1,500 keys and 256 channels (dq / dkv, us; with ds rounded once and delta subtracted
+// per score, where dq of 64 took 175 and now takes 217, dkv 231 and now 212): heads of 32: dq 209 with three waves, 228
+// with NQ 2; dkv 286 with NK 2, 346 with NK 1. Heads of 64: dq 175 with NQ 2 on 32-key tiles, 184 on 64, 187 with NQ 1;
 // dkv 231, with NK 2 (one wave) 317, on 32-row tiles 254. Heads of 128: dq 184 with two waves, 242 with one; dkv 290 with
 // one wave, 470 with two (spills).
 template <typename T, int DP>

@@ -174,6 +174,17 @@ __device__ __forceinline__ Frag<T> load_tr(const bf16_t* s, int row0, int col0) 
   return f;
 }
 
+// x - part[i] in one instruction, a dot product with (-1, 0) or (0, -1); exact where part[i] is x rounded to bf16. An
+// infinite neighbour makes it NaN, so the neighbours have to belong to the same sum. The pair comes from a register: as an
+// inline constant, which the compiler would take for (-1, 0), the instruction reads -1 into the other half.
+__device__ __forceinline__ float minus_part(const bf16x8v& part, int i, float x) {
+  typedef bf16_t bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 pair = {part[i & ~1], part[i | 1]};
+  uint32_t pick = i & 1 ? 0xBF800000u : 0x0000BF80u;
+  asm("" : "+s"(pick));
+  return __builtin_amdgcn_fdot2_f32_bf16(pair, __builtin_bit_cast(bf16x2, pick), x, false);
+}
+
 // Registers 8 m .. 8 m + 7 of a score tile as the second operand (bf16 data: rounded to nearest).
 template <typename T>
 __device__ __forceinline__ Frag<T> to_frag(const f32x16& s, int m) {
@@ -196,7 +207,7 @@ __device__ __forceinline__ void to_frag2(const f32x16& s, int m, Frag<T>& hi, Fr
   hi = to_frag<T>(s, m);
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo.p[0][i] = (bf16_t)(s[8 * m + i] - (float)hi.p[0][i]);
+    for (int i = 0; i < 8; ++i) lo.p[0][i] = (bf16_t)minus_part(hi.p[0], i, s[8 * m + i]);
   }
 }
 
