@@ -8,7 +8,7 @@
 //
 // Long against long, the vector unit bounds it beside the matrix cores: 425 vector instructions (exponentials,
 // sums, maxima, rounding) for the 32 matrix instructions of a wave's 64 x 64 scores with heads of 64, at two waves
-// per SIMD. bf16, 215,003 queries on 5 x ~1024 keys, 4 heads of 64: 293 to 307 us, 720 to 754 TFLOP/s. fp32, 300
+// per SIMD. bf16, 215,003 queries on 5 x ~1024 keys, 4 heads of 64: 283 to 307 us, 720 to 780 TFLOP/s. fp32, 300
 // queries on 43,217 keys, 8 heads of 32: 131 us and 8 to join, 101 TFLOP/s. Single tokens (k_attn_few) read K and
 // V once: 64 on 262,147 keys, 8 heads of 64, about half of the keys in sequences with a query: 40 us and 4 to join, some
 // 6.7 TB/s.
@@ -64,15 +64,12 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   Stage<T, BN, DP, kNT, VEC> sk, sv;
   sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], 0, a.ks[0], 0, 1, a.dim);
   sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], 0, a.vs[0], 0, 1, a.dim);
-  // Keys of the tile from k0 + j on that exist and that the mask keeps.
-  auto key_bits = [&](int j) -> uint64_t {
-    bool ok = lane < BN && j + lane < keys;
-    if (ok && a.mask) ok = a.mask[k0 + j + lane];
-    return __ballot(ok);
-  };
+  // Whether key j + lane exists and the mask keeps it. The ballot of these comes a tile later: at once it would wait for
+  // the tile's loads too.
+  auto key_ok = [&](int j) -> int { return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + j + lane] : 1) : 0; };
   sk.load(keys);
   sv.load(keys);
-  uint64_t next_bits = key_bits(0);
+  int next_ok = key_ok(0);
 
   // This lane's query rows (one per 32-column tile), and their values as second operands.
   int64_t row[NQ];  // row of out and lse, -1: none
@@ -107,7 +104,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 
   int buf = 0;
   for (int j = 0; j < keys; j += BN, buf ^= 1) {
-    const uint64_t bits = next_bits;
+    const uint64_t bits = __ballot(next_ok != 0);
     if (a.mask) {  // what a masked place holds must not meet a zero probability
       sk.template store<LD, PS>(s_k(buf), bits);
       sv.template store<LD, PS>(s_v(buf), bits);
@@ -118,7 +115,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     if (j + BN < keys) {
       sk.load(keys - j - BN);
       sv.load(keys - j - BN);
-      next_bits = key_bits(j + BN);
+      next_ok = key_ok(j + BN);
     }
     // Two buffers: the barrier of the last tile already had every wave past reading this one.
     __syncthreads();

@@ -11,7 +11,7 @@
 //
 // p is rounded to bf16 for dv; ds is kept in two bf16 parts for dq, and for dk with few keys (see there),
 // since its terms cancel. Bound like the forward pass, by the vector unit beside the matrix cores: bf16,
-// 100,003 queries, 4 heads on 2 key heads of 64, three sequences of ~800 keys: dq 229 us, dk and dv 223, sums 7.
+// 100,003 queries, 4 heads on 2 key heads of 64, three sequences of ~800 keys: dq 213 us, dk and dv 211, sums 7.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -61,14 +61,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   Stage<T, BN, DP, kNT, VEC> sk, sv;
   sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], 0, a.ks[0], 0, 1, a.dim);
   sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], 0, a.vs[0], 0, 1, a.dim);
-  auto key_bits = [&](int j) -> uint64_t {
-    bool ok = lane < BN && j + lane < keys;
-    if (ok && a.mask) ok = a.mask[k0 + j + lane];
-    return __ballot(ok);
-  };
+  // As in k_attn_fwd: the ballot comes a tile later, so that it waits for no loads (100,003 queries, masked: 231 and 213 us).
+  auto key_ok = [&](int j) -> int { return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + j + lane] : 1) : 0; };
   sk.load(keys);
   sv.load(keys);
-  uint64_t next_bits = key_bits(0);
+  int next_ok = key_ok(0);
 
   int64_t row[NQ];  // row of out and lse, -1: none
   frag fq[NQ][DP / 16], fo[NQ][DP / 16];
@@ -108,7 +105,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 
   int buf = 0;
   for (int j = 0; j < keys; j += BN, buf ^= 1) {
-    const uint64_t bits = next_bits;
+    const uint64_t bits = __ballot(next_ok != 0);
     if (a.mask) {
       sk.template store<LD, PS>(s_k(buf), bits);
       sv.template store<LD, PS>(s_v(buf), bits);
@@ -119,7 +116,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     if (j + BN < keys) {
       sk.load(keys - j - BN);
       sv.load(keys - j - BN);
-      next_bits = key_bits(j + BN);
+      next_ok = key_ok(j + BN);
     }
     __syncthreads();
 #pragma unroll
@@ -217,20 +214,20 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   // Query rows step through the heads of the group before the next query.
   const int n_rows = (int)(r1 - r0);
   Stage<T, BQ, DP, kNT, VEC> sq, so;
-  float n_lse = 0.f, n_delta = 0.f;
+  float n_lse = 0.f, n_delta = 0.f;  // as loaded: worked on a tile later (223 and 211 us)
   auto fetch = [&](int t0) {
     sq.load(n_rows - t0);
     so.load(n_rows - t0);
     if (threadIdx.x < BQ) {
-      n_lse = INFINITY;
+      n_lse = -INFINITY;
       n_delta = 0.f;
       if (t0 + (int)threadIdx.x < n_rows) {
         int64_t qi;
         int g;
         split_row(r0 + t0 + threadIdx.x, a.group, qi, g);
         const int64_t at = (q0 + qi) * a.heads + kh * a.group + g;
-        n_lse = lse_base2(a.lse_in[at]);
-        n_delta = -a.delta[at];
+        n_lse = a.lse_in[at];
+        n_delta = a.delta[at];
       }
     }
   };
@@ -267,7 +264,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   for (int t0 = 0; t0 < n_rows; t0 += BQ, buf ^= 1) {
     sq.template store<LD, PS>(s_q(buf));
     so.template store<LD, PS>(s_o(buf));
-    if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = n_lse, s_delta[buf][threadIdx.x] = n_delta;
+    if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = lse_base2(n_lse), s_delta[buf][threadIdx.x] = -n_delta;
     if (t0 + BQ < n_rows) fetch(t0 + BQ);
     __syncthreads();
 #pragma unroll
@@ -396,7 +393,7 @@ void sum_go(const float* part0, const float* part1, int splits, int64_t n, int d
 
 // Tiles of the two kernels: 32 NQ (NK) query rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
 // bf16, measured on 60,000 queries x 1,500 keys and 256 channels (dq / dkv, us; with ds rounded once and delta subtracted
-// per score, where dq of 64 took 175 and now takes 217, dkv 231 and now 212): heads of 32: dq 209 with three waves, 228
+// per score, where dq of 64 took 175 and now takes 220, dkv 231 and now 208): heads of 32: dq 209 with three waves, 228
 // with NQ 2; dkv 286 with NK 2, 346 with NK 1. Heads of 64: dq 175 with NQ 2 on 32-key tiles, 184 on 64, 187 with NQ 1;
 // dkv 231, with NK 2 (one wave) 317, on 32-row tiles 254. Heads of 128: dq 184 with two waves, 242 with one; dkv 290 with
 // one wave, 470 with two (spills).
