@@ -1,4 +1,5 @@
-"""MI355X-native IndexGrid build, neighbour map and submanifold sparse convolution.
+"""MI355X-native IndexGrid build, neighbour map and submanifold sparse convolution, and the operators between
+convolutions: layer norm, 8-bit activation checkpoints and cross attention.
 
 Thin Python binding over libigconv (include/igconv.h): it checks tensor shapes, dtypes and
 devices, and passes raw device pointers and the current HIP stream to the C ABI. All device
