@@ -9,7 +9,7 @@
 // Long against long, the vector unit bounds it beside the matrix cores: 425 vector instructions (exponentials,
 // sums, maxima, rounding) for the 32 matrix instructions of a wave's 64 x 64 scores with heads of 64, at two waves
 // per SIMD. bf16, 215,003 queries on 5 x ~1024 keys, 4 heads of 64: 283 to 307 us, 720 to 780 TFLOP/s. fp32, 300
-// queries on 43,217 keys, 8 heads of 32: 131 us and 8 to join, 101 TFLOP/s. Single tokens (k_attn_few) read K and
+// queries on 43,217 keys, 8 heads of 32: 111 us in all, 119 TFLOP/s. Single tokens (k_attn_few) read K and
 // V once: 64 on 262,147 keys, 8 heads of 64, about half of the keys in sequences with a query: 40 us and 4 to join, some
 // 6.7 TB/s.
 #include <hip/hip_runtime.h>
@@ -470,7 +470,10 @@ int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int
   const int bm = fwd_rows(dtype, dim, nq, batch, heads / kv_heads);
   const int64_t per_seq = (nq + batch - 1) / batch * (heads / kv_heads);
   const int64_t wgs = batch * ((per_seq + bm - 1) / bm) * kv_heads;
-  const int64_t fill = bm <= kFewRows ? 2048 : 512;
+  // Workgroups that fill it: two a CU of the matrix kernel, three of its fp32 form for short heads, which is small enough
+  // and waits more. 300 queries on 43,217 keys, 256 channels, us with 512 / 768 / 1024: fp32 heads of 32 121 / 114 / 116, of 64
+  // 102 / 118 / 111, of 128 125 / 145 / 145; bf16 56 / 58 / 68, 44 / 56 / 57 and 49 / 59 / 60.
+  const int64_t fill = bm <= kFewRows ? 2048 : dtype == IGC_F32 && dim <= 32 ? 768 : 512;
   const int64_t want = wgs >= fill ? 1 : fill / std::max<int64_t>(1, wgs);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxParts), nk / batch / 256));
 }
