@@ -353,3 +353,21 @@ def test_caches_past_2_to_the_31_elements(rows):
     assert bool((dk[:nk - last] == 0).all()) and bool((dv[:nk - last] == 0).all())
     for a, b in ((dq, rq), (dk[-last:], rk), (dv[-last:], rv)):
         assert float((a.float() - b.float()).abs().max()) <= 4 * U[BF16] * float(b.float().abs().max())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_masked_keys_get_zeros_whatever_the_output_gradient_holds(dtype):
+    igc = _igc()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q, do = (torch.randn(150, 2, 64, generator=g, device="cuda").to(dtype) for _ in range(2))
+    k, v = (torch.randn(300, 2, 64, generator=g, device="cuda").to(dtype) for _ in range(2))
+    mask = torch.rand(300, generator=g, device="cuda") > 0.3
+    do[7, 0, 5], do[11, 1, 3] = float("nan"), float("inf")
+    out, lse = igc.cross_attention(q, k, v, key_mask=mask)
+    _, dk, dv = igc.cross_attention_backward(do, q, k, v, out, lse, key_mask=mask)
+    assert bool((dk[~mask] == 0).all()) and bool((dv[~mask] == 0).all())
+    # The gradients of the kept keys carry the NaN of each head's one channel, and dv nothing else.
+    assert bool(dk[mask].isnan().any()) and bool(dv[mask][:, 0, 5].isnan().all())
+    rest = dv[mask][:, 0].clone()
+    rest[:, 5] = 0
+    assert bool(rest.isfinite().all())
