@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "igc_host.h"
+#include "igc_ragged.h"
 #include "igc_row.h"
 #include "igc_wave.h"
 
@@ -28,42 +29,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
-
-// Rows [begin, end) of sequence b; whatever the offsets hold, within [0, n].
-__device__ __forceinline__ void seq_rows(const int32_t* off, int b, int64_t n, int64_t& begin, int64_t& end) {
-  if (!off) {
-    begin = 0, end = n;
-    return;
-  }
-  begin = clamp64(off[b], 0, n);
-  end = clamp64(off[b + 1], begin, n);
-}
-
-// Tiles of `bm` rows over ragged sequences without a plan: sequence b of rows [begin, end) (times mul)
-// owns the slots from begin * mul / bm + b on, which are at least as many as its tiles, so that
-// n * mul / bm + batch slots cover everything and a slot finds its sequence by a binary search.
-// Returns the tile in sequence b (it may lie past the sequence's end).
-__device__ __forceinline__ int64_t find_tile(const int32_t* off, int batch, int64_t n, int mul, int bm, int64_t slot,
-                                             int& b) {
-  b = 0;
-  if (!off) return slot;
-  int hi = batch;  // slots of hi and beyond start after `slot`
-  while (hi - b > 1) {
-    const int mid = (b + hi) >> 1;
-    if (clamp64(off[mid], 0, n) * mul / bm + mid <= slot) b = mid;
-    else hi = mid;
-  }
-  return slot - (clamp64(off[b], 0, n) * mul / bm + b);
-}
-
-// Query and head of the group of row r of a sequence (rows of all sequences together stay below 2^31).
-__device__ __forceinline__ void split_row(int64_t r, int group, int64_t& query, int& g) {
-  const uint32_t x = (uint32_t)r, q = group == 1 ? x : x / (uint32_t)group;
-  query = q;
-  g = (int)(x - q * (uint32_t)group);
-}
 
 // Operands of the matrix instructions are bf16. An fp32 value is split into three parts of 8 significant
 // bits each, x = x0 + x1 + x2 exactly, and a product takes the six part products down to 2^-16 of it, which

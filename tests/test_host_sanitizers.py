@@ -58,3 +58,15 @@ def test_tuning_parser_under_asan_ubsan(tmp_path):
     _run([CLANG, *SAN_FLAGS, *objs, "-o", exe, "-lpthread"])
     r = _run([exe], env=_env(tmp_path))
     assert "tuning driver: ok" in r.stdout
+
+
+@pytest.mark.skipif(not (os.path.exists(HIPCC) and os.path.exists(CLANG)), reason="hipcc / clang++ not available")
+def test_ragged_rows_under_asan_ubsan(tmp_path):
+    """tests/sanitize/ragged_driver.cpp: tiles and rows that the attention kernels form from sequence offsets."""
+    obj, exe = str(tmp_path / "ragged.o"), str(tmp_path / "ragged_driver")
+    host_san = [x for f in SAN_FLAGS for x in (["-Xarch_host", f] if f.startswith(("-fsanitize", "-fno-sanitize")) else [f])]
+    _run([HIPCC, "-x", "hip", "--cuda-host-only", "-std=c++17", *host_san, "-I", os.path.join(ROOT, "sparse_convolution_amd", "csrc"),
+          "-c", os.path.join(SAN, "ragged_driver.cpp"), "-o", obj])
+    _run([CLANG, *SAN_FLAGS, obj, "-o", exe, "-lpthread"])
+    r = _run([exe], env=_env(tmp_path))
+    assert "ragged driver: ok" in r.stdout
