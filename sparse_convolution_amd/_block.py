@@ -269,7 +269,8 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets
     any row and head strides), sequence by sequence: rows q_offsets[b] .. q_offsets[b+1] of q attend to rows
     kv_offsets[b] .. kv_offsets[b+1] of k and v (int32 [batch + 1] on the device; None: one sequence).
     key_mask (bool or uint8 [nk]): false rows are left out. scale defaults to dim ** -0.5. Returns (out
-    [nq, heads, dim], lse [nq, heads] float32); a row without keys gets zeros and -inf (igc_cross_attention)."""
+    [nq, heads, dim], lse [nq, heads] float32); a row without keys gets zeros and -inf, a row of no sequence is left
+    unwritten, in the gradients too (igc_cross_attention)."""
     p, sizes = _problem(q, k, v, q_offsets, kv_offsets, key_mask, scale)
     dev = q.device
     out = torch.empty(q.shape, dtype=q.dtype, device=dev)

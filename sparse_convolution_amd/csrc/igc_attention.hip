@@ -353,13 +353,16 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
 
 constexpr int kMaxParts = 128;
 
-// Joins the parts of a split key axis, one workgroup per row: a lane per part weighs it, then the waves
+// Joins the parts of a split key axis, one workgroup per row of a sequence: a lane per part weighs it, then the waves
 // share the parts and the lanes the channels.
 template <typename T>
 __global__ __launch_bounds__(kNT) void k_attn_join(AttnArgs a) {
   __shared__ float s_w[kMaxParts], s_o[4][kAttnMaxDim];
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int64_t rows = a.nq * a.heads, row = blockIdx.x;
+  int64_t q0, q1;
+  covered_rows(a.qo, a.batch, a.nq, q0, q1);
+  if (row < q0 * a.heads || row >= q1 * a.heads) return;
   float m[2], l[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

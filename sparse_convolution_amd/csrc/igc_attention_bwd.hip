@@ -346,22 +346,27 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   }
 }
 
-// out[e] = sum over splits of part[split][e] in a fixed order: eight groups of threads take every eighth part, and
+// out[e] = sum over splits of part[split][e] in a fixed order, over the rows (of `width` values) that the sequences of
+// `off` cover: eight groups of threads take every eighth part, and
 // their sums are added in order. Two results of n values each (blockIdx.y). With one thread for all parts of an
 // element, 128 parts of 77 keys x 256 channels took 31 us.
 template <typename T, int V>
 __global__ __launch_bounds__(kNT) void k_attn_sum(const float* __restrict__ part0, const float* __restrict__ part1,
-                                                  int splits, int64_t n, T* __restrict__ out0, T* __restrict__ out1) {
+                                                  int splits, const int32_t* __restrict__ off, int batch, int64_t rows,
+                                                  int64_t width, T* __restrict__ out0, T* __restrict__ out1) {
   constexpr int G = 8, EL = kNT / G;
   __shared__ float s_sum[G][EL][V];
   const float* part = blockIdx.y ? part1 : part0;
   T* out = blockIdx.y ? out1 : out0;
   const int el = threadIdx.x % EL, g = threadIdx.x / EL;
-  const int64_t e = ((int64_t)blockIdx.x * EL + el) * V;
+  const int64_t e = ((int64_t)blockIdx.x * EL + el) * V, n = rows * width;  // V divides width
+  int64_t first, last;
+  covered_rows(off, batch, rows, first, last);
+  const bool mine = e >= first * width && e < last * width;
   float t[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) t[i] = 0.f;
-  if (e < n) {
+  if (mine) {
 #pragma unroll 4
     for (int s = g; s < splits; s += G) {
       float v[V];
@@ -373,7 +378,7 @@ __global__ __launch_bounds__(kNT) void k_attn_sum(const float* __restrict__ part
 #pragma unroll
   for (int i = 0; i < V; ++i) s_sum[g][el][i] = t[i];
   __syncthreads();
-  if (g == 0 && e < n) {
+  if (g == 0 && mine) {
 #pragma unroll
     for (int k = 1; k < G; ++k)
 #pragma unroll
@@ -383,12 +388,15 @@ __global__ __launch_bounds__(kNT) void k_attn_sum(const float* __restrict__ part
 }
 
 template <typename T>
-void sum_go(const float* part0, const float* part1, int splits, int64_t n, int dim, bool vec, void* out0, void* out1,
-            hipStream_t s) {
+void sum_go(const float* part0, const float* part1, int splits, const int32_t* off, int batch, int64_t rows, int heads,
+            int dim, bool vec, void* out0, void* out1, hipStream_t s) {
+  const int64_t width = (int64_t)heads * dim, n = rows * width;
   const int per = vec && dim % 4 == 0 ? 128 : 32;  // values of a workgroup
   const dim3 grid((unsigned)((n + per - 1) / per), out1 ? 2 : 1);
-  if (per == 128) k_attn_sum<T, 4><<<grid, kNT, 0, s>>>(part0, part1, splits, n, (T*)out0, (T*)out1);
-  else k_attn_sum<T, 1><<<grid, kNT, 0, s>>>(part0, part1, splits, n, (T*)out0, (T*)out1);
+  if (per == 128)
+    k_attn_sum<T, 4><<<grid, kNT, 0, s>>>(part0, part1, splits, off, batch, rows, width, (T*)out0, (T*)out1);
+  else
+    k_attn_sum<T, 1><<<grid, kNT, 0, s>>>(part0, part1, splits, off, batch, rows, width, (T*)out0, (T*)out1);
 }
 
 // Tiles of the two kernels: 32 NQ (NK) query rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
@@ -433,7 +441,7 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true><<<wgs, kNT, 0, s>>>(d);
     else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false><<<wgs, kNT, 0, s>>>(d);
     if (a.dq && d.splits > 1)
-      sum_go<T>(ws, nullptr, d.splits, a.nq * a.heads * a.dim, a.dim, a.ovec, a.dq, nullptr, s);
+      sum_go<T>(ws, nullptr, d.splits, a.qo, a.batch, a.nq, a.heads, a.dim, a.ovec, a.dq, nullptr, s);
   }
   if (a.dk && a.nk > 0) {
     const int64_t n = a.nk * a.kv_heads * a.dim;
@@ -449,7 +457,8 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     // 100 keys 1.5 / 1.1, 400 keys 1.45 / 1.05); with so few the kernel waits for memory, not for its products.
     if (sizeof(T) == 2 && a.nk <= (int64_t)256 * a.batch) go(std::integral_constant<bool, sizeof(T) == 2>{});
     else go(std::false_type{});
-    if (a.splits > 1) sum_go<T>(a.part_a, a.part_b, a.splits, n, a.dim, a.ovec, a.dk, a.dv, s);
+    if (a.splits > 1)
+      sum_go<T>(a.part_a, a.part_b, a.splits, a.ko, a.batch, a.nk, a.kv_heads, a.dim, a.ovec, a.dk, a.dv, s);
   }
 }
 

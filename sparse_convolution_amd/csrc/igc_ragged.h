@@ -20,6 +20,13 @@ __host__ __device__ __forceinline__ void seq_rows(const int32_t* off, int b, int
   end = clamp64(off[b + 1], begin, n);
 }
 
+// Rows [begin, end) that the sequences cover together (ascending offsets); the rest is left unwritten.
+__host__ __device__ __forceinline__ void covered_rows(const int32_t* off, int batch, int64_t n, int64_t& begin,
+                                                      int64_t& end) {
+  begin = off ? clamp64(off[0], 0, n) : 0;
+  end = off ? clamp64(off[batch], begin, n) : n;
+}
+
 // Tiles of `bm` rows over ragged sequences without a plan: sequence b of rows [begin, end) (times mul)
 // owns the slots from (begin - first) * mul / bm + b on, with `first` the first sequence's first row, which are at
 // least as many as its tiles, so that n * mul / bm + batch slots cover everything and a slot finds its sequence by a

@@ -1,8 +1,10 @@
 """Cross attention over offsets that leave rows out: before the first sequence, after the last one, or both.
 
-Rows that no sequence covers take no part; the rest equals the attention of the
+Rows that no sequence covers take no part and their results are left unwritten; the rest equals the attention of the
 covered slices alone, to the bounds of tests/test_gpu_attention.py.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -54,3 +56,45 @@ def test_a_first_sequence_that_starts_late(qo, nq, ko, nk, dtype):
     for name, t in (("out", out[qs]), ("dq", dq[qs]), ("dk", dk[ks]), ("dv", dv[ks])):
         err = (t.double().cpu() - r[name]).abs()
         assert bool((err <= b[name]).all()), (name, float((err / b[name]).max()))
+
+
+def _address(t):
+    return ctypes.c_void_p(t.data_ptr())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("heads,dim", [(4, 32), (2, 33)])
+@pytest.mark.parametrize("qo,nq,ko,nk", FIRST_ROWS + [([0, 1], 4, [0, 2000], 2500), ([0, 60, 100], 150, [0, 900, 3000], 3300),
+                                                      ([0, 3000], 3500, [0, 20], 50), ([0, 100], 160, [0, 90], 200), ([5, 5], 9, [3, 3], 7)])
+def test_rows_of_no_sequence_are_left_unwritten(qo, nq, ko, nk, heads, dim, dtype):
+    # Outputs filled with 7 and the workspace with NaN before the calls: what no sequence covers still holds 7, and
+    # nothing else takes up the workspace's content.
+    from sparse_convolution_amd import _lib
+    lib = _lib.load()
+    say(f"attention rows of no sequence, {qo} of {nq}, {ko} of {nk}, {heads} heads of {dim}, {dtype}")
+    (q, k, v, do), _, _ = _case([nq], [nk], heads, 2, dim, dtype)
+    qo, ko = _offsets(*qo), _offsets(*ko)
+    pair = ctypes.c_int64 * 2
+    p = _lib.Attention(dtype=int(dtype == BF16), batch=qo.numel() - 1, heads=heads, kv_heads=2, dim=dim, scale=dim ** -0.5, n_q=nq, n_k=nk,
+                       q_stride=pair(heads * dim, dim), k_stride=pair(2 * dim, dim), v_stride=pair(2 * dim, dim),
+                       d_q_offsets=qo.data_ptr(), d_kv_offsets=ko.data_ptr(), d_key_mask=None)
+
+    def workspace(backward):
+        size = ctypes.c_size_t(0)
+        assert lib.igc_cross_attention_workspace(ctypes.byref(p), backward, ctypes.byref(size)) == 0
+        return torch.full((size.value // 4 + 1,), float("nan"), device="cuda"), size.value
+
+    out, lse = torch.full_like(q, 7), torch.full((nq, heads), 7.0, device="cuda")
+    dq, dk, dv = torch.full_like(q, 7), torch.full_like(k, 7), torch.full_like(v, 7)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    ws, size = workspace(0)
+    assert lib.igc_cross_attention(ctypes.byref(p), _address(q), _address(k), _address(v), _address(out), _address(lse), _address(ws), size,
+                                   stream) == 0
+    ws, size = workspace(1)
+    assert lib.igc_cross_attention_backward(ctypes.byref(p), _address(q), _address(k), _address(v), _address(out), _address(lse),
+                                            _address(do), _address(dq), _address(dk), _address(dv), _address(ws), size, stream) == 0
+    torch.cuda.synchronize()
+    for name, t, off in (("out", out, qo), ("lse", lse, qo), ("dq", dq, qo), ("dk", dk, ko), ("dv", dv, ko)):
+        lo, hi = int(off[0]), int(off[-1])
+        assert bool((t[:lo] == 7).all()) and bool((t[hi:] == 7).all()), name
+        assert not bool(t[lo:hi].isnan().any()), name
