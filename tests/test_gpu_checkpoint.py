@@ -176,3 +176,28 @@ def test_conv_weight_gradient_from_codes_at_an_odd_address():
     odd = igc.Checkpoint8(moved, ck.scales, BF16)
     assert torch.equal(igc.sparse_conv_backward(g, odd, w, dy, m)[1], igc.sparse_conv_backward(g, ck, w, dy, m)[1])
     assert torch.equal(igc.checkpoint_unpack(odd), igc.checkpoint_unpack(ck))
+
+
+@pytest.mark.parametrize("cin,cout,side,blocks", [(128, 128, 46, (9, 24)), (128, 128, 63, (25, 99)), (256, 256, 32, (9, 24)),
+                                                  (256, 256, 41, (25, 99)), (256, 128, 44, (9, 24)), (128, 256, 55, (25, 99))])
+def test_conv_weight_gradient_from_a_checkpoint_on_larger_grids(cin, cout, side, blocks):
+    # The block of the weight gradient that a workgroup computes grows with the grid: up to 8 blocks of 128 x 128 for each 11 tiles
+    # of 256 rows it is 64 x 64, up to 24 it is 64 x 128, beyond 128 x 128. The row order and the chunks are those of the
+    # features' gradient at these sizes, so the sums are the same to the bit.
+    igc = _igc()
+    rng = np.random.default_rng(side)
+    cube = np.stack(np.meshgrid(*[np.arange(side)] * 3, indexing="ij"), -1).reshape(-1, 3)
+    g = igc.grid_build(to_dev(cube[rng.random(cube.shape[0]) < 0.3].astype(np.int32)))
+    m, n = igc.kernel_map(g), g.n_voxels
+    say(f"conv backward from a checkpoint {cin}->{cout}, {n} voxels")
+    count = -(-n // (11 * 256)) * (cin // 128) * (cout // 128)
+    assert blocks[0] <= count <= blocks[1], count
+    f = torch.from_numpy(workloads.make_features(n, cin, 5200)).to("cuda", BF16)
+    dy = torch.from_numpy(workloads.make_features(n, cout, 7200)).to("cuda", BF16)
+    w = torch.zeros(27, cin, cout, dtype=BF16, device="cuda")
+    ck = igc.checkpoint_pack(f)
+    v = igc.checkpoint_unpack(ck)
+    dw = igc.sparse_conv_backward(g, ck, w, dy, m, need_dfeats=False)[1]
+    assert torch.equal(dw, igc.sparse_conv_backward(g, v, w, dy, m, need_dfeats=False)[1])
+    ref = oracle.conv_wgrad(m.cpu().numpy(), v.float().cpu().numpy(), dy.float().cpu().numpy())
+    assert normwise_error(dw.cpu().numpy(), ref) <= 1e-5
