@@ -114,8 +114,10 @@ __global__ __launch_bounds__(kNT) void k_norm(const T* __restrict__ x, int64_t n
     }
     row_sum2<LPR>(rest, sq, s_red);
     rest *= inv_c;
-    const float mu = mu0 + rest;
-    const float rs = 1.0f / sqrtf(fmaxf(fmaf(-rest, rest, sq * inv_c), 0.f) + eps);
+    // An infinite mean leaves NaN differences: it stays as it is, and the variance is NaN (a maximum with 0 would drop that).
+    const float mu = rest - rest == 0.f ? mu0 + rest : mu0;
+    const float var = fmaf(-rest, rest, sq * inv_c);
+    const float rs = 1.0f / sqrtf((var < 0.f ? 0.f : var) + eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int first = (j * LPR + l) * V;

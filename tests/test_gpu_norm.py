@@ -248,3 +248,26 @@ def test_more_rows_than_one_launch_has_threads_for():
     for at in (0, last // 2 // block * block, last - block, last):
         k = min(block, n - at)
         assert torch.equal(y[at:at + k], ry[:k]) and torch.equal(mean[at:at + k], rm[:k]) and torch.equal(rstd[at:at + k], rr[:k])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("c", [1, 3, 8, 64, 130, 1040, 4096])
+def test_statistics_of_a_row_with_infinity_or_nan(c, dtype):
+    # By the definition: a NaN makes mean and rstd NaN; an infinity the mean infinite (of its sign) and rstd NaN, both signs
+    # all NaN. The other rows keep theirs.
+    igc = _igc()
+    x, _, w, b = _inputs(40, c, dtype, dtype, 13)
+    clean = igc.layer_norm(x, w, b)
+    nan, inf = float("nan"), float("inf")
+    x[3, c // 2], x[5, 0], x[8, c - 1] = nan, inf, -inf
+    both = c > 1
+    if both:
+        x[9, 0], x[9, c - 1] = inf, -inf
+    y, mean, rstd = igc.layer_norm(x, w, b)
+    y8, ck, rstd8 = igc.layer_norm_checkpoint(x, w, b)
+    bad = [3, 5, 8] + [9] * both
+    assert bool(mean[3].isnan()) and float(mean[5]) == inf and float(mean[8]) == -inf and (not both or bool(mean[9].isnan()))
+    for t in (rstd, rstd8, y, y8, igc.checkpoint_unpack(ck)):
+        assert bool(t[bad].isnan().all())
+    rest = [r for r in range(40) if r not in bad]
+    assert torch.equal(mean[rest], clean[1][rest]) and torch.equal(rstd[rest], clean[2][rest]) and torch.equal(rstd8[rest], clean[2][rest])
