@@ -342,6 +342,7 @@ int igc_layer_norm_q8_backward(const void* d_dy, const int8_t* d_codes, const fl
 
 /* A cross-attention problem: queries (voxels or object queries) of `batch` sequences attending to
  * another set of rows (an encoder's states, or voxels) of the same sequences.
+ *  - n_k, and n_q times the query heads per key head, are at most 2^31 - 1024 (IGC_ERR_RANGE beyond).
  *  - q is [n_q, heads, dim], k and v [n_k, kv_heads, dim] of type `dtype`, dim contiguous, with any row
  *    and head strides (elements): slices of one projection need no copy. Query head h reads key head
  *    h / (heads / kv_heads). dim is 1 to 128.

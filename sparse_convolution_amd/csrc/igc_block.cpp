@@ -82,8 +82,8 @@ int attention_args(const char* fn, const igc_attention_t* p, AttnArgs& a) {
   if (!(p->scale > 0.f) || std::isinf(p->scale))
     return set_error(IGC_ERR_INVALID_ARG, f + ": scale must be positive and finite");
   const int64_t group = p->heads / p->kv_heads;
-  if (p->n_k > INT32_MAX || p->n_q > INT32_MAX / group)
-    return set_error(IGC_ERR_RANGE, f + ": n_q times heads per key head, and n_k, must stay below 2^31");
+  if (p->n_k > kAttnMaxRows || p->n_q > kAttnMaxRows / group)
+    return set_error(IGC_ERR_RANGE, f + ": n_q times heads per key head, and n_k, can be at most 2^31 - 1024");
   // Workgroups: at most 128 parts of each tile (of 128 rows, or of a few where sequences have only those).
   if ((std::min(p->n_q * group / 128, INT64_C(1) << 31) + (int64_t)p->batch * 9) * p->kv_heads > INT32_MAX / 128 ||
       (p->n_k / 128 + p->batch) * (int64_t)p->kv_heads > INT32_MAX / 128)

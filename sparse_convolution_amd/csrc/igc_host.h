@@ -236,6 +236,9 @@ struct AttnArgs {
   float scale = 1.f;
 };
 constexpr int32_t kAttnMaxDim = 128;
+// Keys, and query rows (queries times the heads that share a key head), of a problem at most: the kernels count those of a
+// sequence in 32 bits and step up to 256 past its end.
+constexpr int64_t kAttnMaxRows = INT32_MAX - 1023;
 // Parts the key axis is split into; the forward workspace holds splits * nq * heads * (dim + 2) floats
 // where there is more than one.
 int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim);

@@ -93,6 +93,19 @@ def test_attention_problems(lib, change, status, word):
     _refused(lib, status, lib.igc_cross_attention_backward(p, P, P, P, P, P, P, Q, Q, Q, Q, 1 << 40, None), word)
 
 
+@pytest.mark.parametrize("change", [{"n_k": (1 << 31) - 1}, {"n_k": (1 << 31) - 129}, {"n_k": (1 << 31) - 1023}, {"n_q": (1 << 31) - 1023},
+                                    {"n_q": (1 << 30) - 511, "heads": 2}])
+def test_attention_row_counts_within_a_tile_of_2_to_the_31(lib, change):
+    # The kernels step up to 256 past a sequence's end in 32 bits. 2^31 - 1024 is the largest count taken.
+    problem = dict({"n_q": 3, "n_k": 3, "heads": 1, "kv_heads": 1}, **change)
+    p, size = ctypes.byref(_problem(**problem)), ctypes.c_size_t(0)
+    _refused(lib, RANGE, lib.igc_cross_attention_workspace(p, 0, ctypes.byref(size)), b"2^31 - 1024")
+    _refused(lib, RANGE, lib.igc_cross_attention(p, P, P, P, Q, Q, Q, 1 << 40, None), b"2^31 - 1024")
+    _refused(lib, RANGE, lib.igc_cross_attention_backward(p, P, P, P, P, P, P, Q, Q, Q, Q, 1 << 40, None), b"2^31 - 1024")
+    largest = _problem(n_q=3, n_k=(1 << 31) - 1024, heads=1, kv_heads=1)
+    assert lib.igc_cross_attention_workspace(ctypes.byref(largest), 0, ctypes.byref(size)) == 0, lib.igc_last_error()
+
+
 def test_attention_operands(lib):
     p = ctypes.byref(_problem())
     _refused(lib, INVALID, lib.igc_cross_attention(None, P, P, P, Q, Q, None, 0, None), b"problem")
