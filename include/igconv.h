@@ -372,7 +372,7 @@ int igc_cross_attention_workspace(const igc_attention_t* problem, int32_t backwa
  * gives d_out = 0 and d_lse = -infinity. Statistics and sums are fp32; with bf16 data the probabilities are
  * rounded to bf16 for the product with v (not for a few queries a sequence). fp32 products run as six bf16 products of
  * three-part operands, to 2^-24 of each: an infinite operand gives NaN. d_ws: at least igc_cross_attention_workspace bytes
- * (IGC_ERR_CAPACITY otherwise). d_out must not alias an input. Reruns are bit-identical. */
+ * (IGC_ERR_CAPACITY otherwise), aligned to 16 bytes (IGC_ERR_INVALID_ARG). d_out must not alias an input. Reruns are bit-identical. */
 int igc_cross_attention(const igc_attention_t* problem, const void* d_q, const void* d_k, const void* d_v, void* d_out,
                         float* d_lse, void* d_ws, size_t ws_bytes, igc_stream stream);
 
@@ -384,7 +384,7 @@ int igc_cross_attention(const igc_attention_t* problem, const void* d_q, const v
  * d_dq [n_q, heads, dim], d_dk and d_dv [n_k, kv_heads, dim], dense, of type `dtype`; NULL d_dq, or NULL d_dk
  * and d_dv together, skip them. Masked keys get zeros. With bf16 data p is rounded to bf16
  * for dv; ds enters dq in two bf16 parts (16 bits), and dk too with up to 256 keys a sequence on average, else
- * rounded to bf16. Sums are fp32 in a fixed order (reruns are bit-identical). */
+ * rounded to bf16. Sums are fp32 in a fixed order (reruns are bit-identical). d_ws as above, aligned to 16 bytes. */
 int igc_cross_attention_backward(const igc_attention_t* problem, const void* d_q, const void* d_k, const void* d_v,
                                  const void* d_out, const float* d_lse, const void* d_dout, void* d_dq, void* d_dk,
                                  void* d_dv, void* d_ws, size_t ws_bytes, igc_stream stream);

@@ -110,13 +110,20 @@ void attention_alignment(const igc_attention_t* p, AttnArgs& a, const void* dens
   a.ovec = d && aligned16(dense) && (int64_t)a.heads * a.dim < (1 << 22);
 }
 
+// Floats before the statistics in the forward workspace: the partial results, up to the next 16 bytes.
+size_t forward_results(const AttnArgs& a) { return ((size_t)a.splits * a.nq * a.heads * a.dim + 3) / 4 * 4; }
 size_t forward_bytes(const AttnArgs& a) {
-  return a.splits > 1 ? (size_t)a.splits * a.nq * a.heads * (a.dim + 2) * sizeof(float) : 0;
+  return a.splits > 1 ? (forward_results(a) + (size_t)a.splits * a.nq * a.heads * 2) * sizeof(float) : 0;
 }
 
-int workspace_error(const char* fn, size_t need) {
-  return set_error(IGC_ERR_CAPACITY, std::string(fn) + ": needs " + std::to_string(need) +
-                                         " bytes of workspace (igc_cross_attention_workspace)");
+// Checks a workspace of which `need` bytes are used.
+int check_workspace(const char* fn, const void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return IGC_OK;
+  if (!ws || ws_bytes < need)
+    return set_error(IGC_ERR_CAPACITY, std::string(fn) + ": needs " + std::to_string(need) +
+                                           " bytes of workspace (igc_cross_attention_workspace)");
+  if (!aligned16(ws)) return set_error(IGC_ERR_INVALID_ARG, std::string(fn) + ": d_ws must be aligned to 16 bytes");
+  return IGC_OK;
 }
 
 }  // namespace
@@ -151,10 +158,9 @@ int igc_cross_attention(const igc_attention_t* p, const void* d_q, const void* d
   a.q = d_q, a.k = d_k, a.v = d_v, a.out = d_out, a.lse = d_lse;
   attention_alignment(p, a, d_out);
   a.splits = attn_fwd_splits(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
-  const size_t need = forward_bytes(a);
-  if (need > 0 && (!d_ws || ws_bytes < need)) return workspace_error(fn, need);
+  if (const int bad = check_workspace(fn, d_ws, ws_bytes, forward_bytes(a))) return bad;
   a.part_a = (float*)d_ws;
-  a.part_b = a.part_a + (size_t)a.splits * a.nq * a.heads * a.dim;
+  a.part_b = a.part_a + forward_results(a);
   return launch_attn_fwd(a, p->dtype, (hipStream_t)stream);
 }
 
@@ -180,8 +186,7 @@ int igc_cross_attention_backward(const igc_attention_t* p, const void* d_q, cons
   attention_alignment(p, a, (const void*)((uintptr_t)d_out | (uintptr_t)d_dout | (uintptr_t)d_dq | (uintptr_t)d_dk |
                                           (uintptr_t)d_dv));
   const AttnBwdPlan plan = attn_bwd_plan(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
-  const size_t need = plan.floats * sizeof(float);
-  if (need > 0 && (!d_ws || ws_bytes < need)) return workspace_error(fn, need);
+  if (const int bad = check_workspace(fn, d_ws, ws_bytes, plan.floats * sizeof(float))) return bad;
   return launch_attn_bwd(a, p->dtype, plan, d_ws, (hipStream_t)stream);
 }
 

@@ -239,8 +239,8 @@ constexpr int32_t kAttnMaxDim = 128;
 // Keys, and query rows (queries times the heads that share a key head), of a problem at most: the kernels count those of a
 // sequence in 32 bits and step up to 256 past its end.
 constexpr int64_t kAttnMaxRows = INT32_MAX - 1023;
-// Parts the key axis is split into; the forward workspace holds splits * nq * heads * (dim + 2) floats
-// where there is more than one.
+// Parts the key axis is split into; where there is more than one, the forward workspace holds dim partial results and two
+// statistics for each part, query and head.
 int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim);
 int launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s);
 struct AttnBwdPlan {

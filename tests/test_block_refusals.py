@@ -106,6 +106,20 @@ def test_attention_row_counts_within_a_tile_of_2_to_the_31(lib, change):
     assert lib.igc_cross_attention_workspace(ctypes.byref(largest), 0, ctypes.byref(size)) == 0, lib.igc_last_error()
 
 
+def test_attention_workspaces_are_aligned(lib):
+    # 1 query, 1 head of 33 channels, 1000 keys in 3 parts: 99 partial results, then 3 pairs of statistics that are read as
+    # pairs, from the next multiple of 16 bytes on.
+    size = ctypes.c_size_t(0)
+    odd = ctypes.byref(_problem(dtype=0, n_q=1, n_k=1000, heads=1, kv_heads=1, dim=33))
+    assert lib.igc_cross_attention_workspace(odd, 0, ctypes.byref(size)) == 0
+    assert size.value == 4 * (100 + 3 * 2)
+    off = ctypes.c_void_p(8192 + 4)
+    _refused(lib, INVALID, lib.igc_cross_attention(odd, P, P, P, Q, Q, off, 1 << 30, None), b"d_ws must be aligned to 16 bytes")
+    p = ctypes.byref(_problem())
+    _refused(lib, INVALID, lib.igc_cross_attention_backward(p, P, P, P, P, P, P, Q, Q, Q, off, 1 << 30, None),
+             b"d_ws must be aligned to 16 bytes")
+
+
 def test_attention_operands(lib):
     p = ctypes.byref(_problem())
     _refused(lib, INVALID, lib.igc_cross_attention(None, P, P, P, Q, Q, None, 0, None), b"problem")

@@ -371,3 +371,10 @@ def test_masked_keys_get_zeros_whatever_the_output_gradient_holds(dtype):
     rest = dv[mask][:, 0].clone()
     rest[:, 5] = 0
     assert bool(rest.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lq,heads,dim", [([1], 1, 33), ([1], 1, 1), ([3], 3, 45), ([41], 1, 99)])
+def test_a_split_key_axis_with_odd_sizes(lq, heads, dim, dtype):
+    # 3 parts: an odd number of partial results before the statistics.
+    check(lq, [1000], heads, heads, dim, dtype)
