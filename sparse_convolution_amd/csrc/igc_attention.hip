@@ -91,7 +91,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     }
   }
 
-  const float c = a.scale * kLog2e, slack = kSlack / c;
+  // Finite, so that the first reference (-infinity) is passed whatever the scale.
+  const float c = a.scale * kLog2e, slack = fminf(kSlack / c, 3.4e38f);
   f32x16 o[NQ][DT];
   float m[NQ], l[NQ];  // references (in the scores' units) and this lane's part of the sums
 #pragma unroll

@@ -378,3 +378,19 @@ def test_masked_keys_get_zeros_whatever_the_output_gradient_holds(dtype):
 def test_a_split_key_axis_with_odd_sizes(lq, heads, dim, dtype):
     # 3 parts: an odd number of partial results before the statistics.
     check(lq, [1000], heads, heads, dim, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,keys", [(1, 90), (40, 90), (300, 90), (40, 3000)])
+def test_a_scale_near_zero(rows, keys, dtype):
+    # With a scale below the smallest normal number all scores are 0 to 2^-100: out is the mean of v and lse log(keys).
+    igc = _igc()
+    (q, k, v, do), _, _ = _case([rows], [keys], 2, 2, 32, dtype)
+    out, lse = igc.cross_attention(q, k, v, scale=1e-38)
+    mean = v.double().mean(0).cpu()
+    assert bool(((lse.double().cpu() - np.log(keys)).abs() <= F * (1 + np.log(keys))).all())
+    # Probabilities are 1 or 1 / keys: exact or one rounding; sums and the result's rounding as in the bounds above.
+    assert bool(((out.double().cpu() - mean).abs() <= (U[dtype] + F) * v.double().abs().mean(0).cpu() + U[dtype] * mean.abs()).all())
+    _, _, dv = igc.cross_attention_backward(do, q, k, v, out, lse, scale=1e-38)
+    ref, mag = do.double().sum(0).cpu() / keys, do.double().abs().sum(0).cpu() / keys
+    assert bool(((dv.double().cpu() - ref).abs() <= (U[dtype] + F) * mag + U[dtype] * ref.abs()).all())
