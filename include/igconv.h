@@ -351,7 +351,7 @@ int igc_layer_norm_q8_backward(const void* d_dy, const int8_t* d_codes, const fl
  *    with batch 1). Sequences may be empty on either side. Offsets are clamped to the arrays, so wrong ones
  *    cannot reach outside; rows that no sequence covers are left unwritten.
  *  - d_key_mask (uint8 [n_k], may be NULL): rows with 0 are left out. Their k and v may hold anything.
- *  - scale multiplies q . k; positive and finite. */
+ *  - scale multiplies q . k; positive, and finite times log2(e). */
 typedef struct {
   int32_t dtype, batch, heads, kv_heads, dim;
   float scale;

@@ -79,8 +79,9 @@ int attention_args(const char* fn, const igc_attention_t* p, AttnArgs& a) {
     return set_error(IGC_ERR_UNSUPPORTED, f + ": at most " + std::to_string(kAttnMaxDim) + " channels a head");
   if (p->batch > 1 && (!p->d_q_offsets || !p->d_kv_offsets))
     return set_error(IGC_ERR_INVALID_ARG, f + ": several sequences need d_q_offsets and d_kv_offsets");
-  if (!(p->scale > 0.f) || std::isinf(p->scale))
-    return set_error(IGC_ERR_INVALID_ARG, f + ": scale must be positive and finite");
+  // The kernels exponentiate in base 2, with scale * log2(e).
+  if (!(p->scale > 0.f) || std::isinf(p->scale * 1.4426950408889634f))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": scale must be positive, and finite times log2(e)");
   const int64_t group = p->heads / p->kv_heads;
   if (p->n_k > kAttnMaxRows || p->n_q > kAttnMaxRows / group)
     return set_error(IGC_ERR_RANGE, f + ": n_q times heads per key head, and n_k, can be at most 2^31 - 1024");

@@ -106,6 +106,13 @@ def test_attention_row_counts_within_a_tile_of_2_to_the_31(lib, change):
     assert lib.igc_cross_attention_workspace(ctypes.byref(largest), 0, ctypes.byref(size)) == 0, lib.igc_last_error()
 
 
+def test_attention_scales_that_overflow_in_base_2(lib):
+    # Finite, but not times log2(e), which the kernels exponentiate with: every result would be NaN.
+    p, size = ctypes.byref(_problem(scale=3e38)), ctypes.c_size_t(0)
+    _refused(lib, INVALID, lib.igc_cross_attention_workspace(p, 0, ctypes.byref(size)), b"scale must be positive, and finite times")
+    assert lib.igc_cross_attention_workspace(ctypes.byref(_problem(scale=2e38)), 0, ctypes.byref(size)) == 0
+
+
 def test_attention_workspaces_are_aligned(lib):
     # 1 query, 1 head of 33 channels, 1000 keys in 3 parts: 99 partial results, then 3 pairs of statistics that are read as
     # pairs, from the next multiple of 16 bytes on.
