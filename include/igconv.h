@@ -383,8 +383,7 @@ int igc_cross_attention(const igc_attention_t* problem, const void* d_q, const v
  *     j's sequence and the heads h that share hk.
  * d_dq [n_q, heads, dim], d_dk and d_dv [n_k, kv_heads, dim], dense, of type `dtype`; NULL d_dq, or NULL d_dk
  * and d_dv together, skip them. Masked keys get zeros. With bf16 data p is rounded to bf16
- * for dv; ds enters dq in two bf16 parts (16 bits), and dk too with up to 256 keys a sequence on average, else
- * rounded to bf16. Sums are fp32 in a fixed order (reruns are bit-identical). d_ws as above, aligned to 16 bytes. */
+ * for dv; ds enters dq and dk in two bf16 parts (16 bits). Sums are fp32 in a fixed order (reruns are bit-identical). d_ws as above, aligned to 16 bytes. */
 int igc_cross_attention_backward(const igc_attention_t* problem, const void* d_q, const void* d_k, const void* d_v,
                                  const void* d_out, const float* d_lse, const void* d_dout, void* d_dq, void* d_dk,
                                  void* d_dv, void* d_ws, size_t ws_bytes, igc_stream stream);

@@ -9,13 +9,12 @@
 // query rows and walks keys, k_attn_dkv owns keys and walks query rows, so nothing is added by atomics
 // and reruns are bit-identical. Scores are computed again in both (seven products instead of five).
 //
-// p is rounded to bf16 for dv; ds is kept in two bf16 parts for dq, and for dk with few keys (see there),
-// since its terms cancel. Bound like the forward pass, by the vector unit beside the matrix cores: bf16,
+// With bf16 data p is rounded to bf16 for dv, whose terms it weighs one by one; ds is kept in two bf16 parts for dq and
+// dk, since its terms cancel (see k_attn_dkv for both sides). Bound like the forward pass, by the vector unit beside the matrix cores: bf16,
 // 100,003 queries, 4 heads on 2 key heads of 64, three sequences of ~800 keys: dq 213 us, dk and dv 211, sums 7.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "igc_attn.h"
 #include "igc_host.h"
@@ -151,7 +150,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
       for (int mm = 0; mm < 2; ++mm) {
         // ds in two parts: rounded once, dq would be off by more than one and a half times what its own rounding to
-        // bf16 costs, since the terms of a row cancel (their ds add up to 0).
+        // bf16 costs, since the terms of a row cancel (their ds add up to 0). In two parts by 1.00.
         frag hi[NQ], lo[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) to_frag2<T>(s[n], mm, hi[n], lo[n]);
@@ -180,11 +179,14 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   }
 }
 
-// dk and dv: four waves of 32 NK keys each over tiles of BQ query rows of the sequence. FINE: ds in two parts for the
-// product with q, as for dq; with few keys its terms cancel too. A score costs its exponential, two multiplications and
-// two roundings: the products with dout start from -delta (read into their accumulators from LDS), and what the mask leaves out is
+// dk and dv: four waves of 32 NK keys each over tiles of BQ query rows of the sequence. bf16 data: ds in two parts for the
+// product with q, as for dq, its terms cancel too: rounded once, dk is off by 1.40 to 1.46 times what its own rounding to
+// bf16 costs (30 to 1,500 keys a sequence, 256 queries, heads of 64, rms against 64 bits), in two parts by 1.00. The second
+// product costs 4 to 12% of the backward pass over 300 to 1,500 keys (60,000 queries, heads of 128 to 32: 433 and 453 us, 466 and
+// 521), for all lengths alike, so that a sequence's gradients are as exact whatever its neighbours are. A score costs its exponential, two multiplications,
+// three roundings and a remainder: the products with dout start from -delta (read into their accumulators from LDS), and what the mask leaves out is
 // cleared in the results instead of per score (100,003 queries, three sequences of ~800 keys, 4 heads of 64: 252 and 223 us).
-template <typename T, int DP, int NK, int BQ, int WPE, bool FINE, bool VEC>
+template <typename T, int DP, int NK, int BQ, int WPE, bool VEC>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int LD = lds_ld<DP>(), PS = BQ * LD;
@@ -309,8 +311,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
         for (int n = 0; n < NK; ++n) {
           fp[n] = to_frag<T>(s[n], mm);
-          if constexpr (FINE) to_frag2<T>(dp[n], mm, fs[n], lo[n]);
-          else fs[n] = to_frag<T>(dp[n], mm);
+          to_frag2<T>(dp[n], mm, fs[n], lo[n]);
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
           for (int n = 0; n < NK; ++n) {
             dv[n][d] = mma(go, fp[n], dv[n][d]);
-            if constexpr (FINE) dk[n][d] = mma(gq, lo[n], dk[n][d]);
+            if constexpr (sizeof(T) == 2) dk[n][d] = mma(gq, lo[n], dk[n][d]);
             dk[n][d] = mma(gq, fs[n], dk[n][d]);
           }
         }
@@ -449,14 +450,8 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     a.part_a = ws;
     a.part_b = ws + (p.dkv_splits > 1 ? p.dkv_splits * n : 0);
     const unsigned wgs = (unsigned)((a.nk / (128 * S::NK) + a.batch) * a.kv_heads * a.splits);
-    const auto go = [&](auto fine) {
-      if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, fine, true><<<wgs, kNT, 0, s>>>(a);
-      else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, fine, false><<<wgs, kNT, 0, s>>>(a);
-    };
-    // Up to 256 keys a sequence (simulated against 64 bits, relative to rounding alone, one part / two: 30 keys 1.7 / 1.35,
-    // 100 keys 1.5 / 1.1, 400 keys 1.45 / 1.05); with so few the kernel waits for memory, not for its products.
-    if (sizeof(T) == 2 && a.nk <= (int64_t)256 * a.batch) go(std::integral_constant<bool, sizeof(T) == 2>{});
-    else go(std::false_type{});
+    if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false><<<wgs, kNT, 0, s>>>(a);
     if (a.splits > 1)
       sum_go<T>(a.part_a, a.part_b, a.splits, a.ko, a.batch, a.nk, a.kv_heads, a.dim, a.ovec, a.dk, a.dv, s);
   }

@@ -394,3 +394,40 @@ def test_a_scale_near_zero(rows, keys, dtype):
     _, _, dv = igc.cross_attention_backward(do, q, k, v, out, lse, scale=1e-38)
     ref, mag = do.double().sum(0).cpu() / keys, do.double().abs().sum(0).cpu() / keys
     assert bool(((dv.double().cpu() - ref).abs() <= (U[dtype] + F) * mag + U[dtype] * ref.abs()).all())
+
+
+def _off_by(lk, seqs, rows=256):
+    """rms errors of dq, and of dk sequence by sequence, against float64, as multiples of the error that rounding the exact
+    results to bf16 makes. The reference's delta comes from the rounded `out`, as the kernel's does."""
+    igc = _igc()
+    lq, lk = [rows] * seqs, lk if isinstance(lk, list) else [lk] * seqs
+    dev, (qo, ko), _ = _case(lq, lk, 2, 2, 64, BF16)
+    q, k, v, do = dev
+    out, lse = igc.cross_attention(q, k, v, qo, ko)
+    dq, dk, _ = igc.cross_attention_backward(do, q, k, v, out, lse, qo, ko)
+    q, k, v, do, out, dq, dk = [t.double().cpu() for t in (q, k, v, do, out, dq, dk)]
+    rq, rk = torch.zeros_like(q), torch.zeros_like(k)
+    a = b = 0
+    for nq, nk in zip(lq, lk):
+        for h in range(2):
+            qq, kk, vv, dd, oo = q[a:a + nq, h], k[b:b + nk, h], v[b:b + nk, h], do[a:a + nq, h], out[a:a + nq, h]
+            p = torch.softmax(qq @ kk.T / 8, 1)
+            ds = p * (dd @ vv.T - (dd * oo).sum(1, keepdim=True))
+            rq[a:a + nq, h], rk[b:b + nk, h] = ds @ kk / 8, ds.T @ qq / 8
+        a, b = a + nq, b + nk
+    res, b = [], 0
+    for nk in lk:
+        s = slice(b, b + nk)
+        res.append(float((dk[s] - rk[s]).norm() / (rk[s].bfloat16().double() - rk[s]).norm()))
+        b += nk
+    return float((dq - rq).norm() / (rq.bfloat16().double() - rq).norm()), res
+
+
+@pytest.mark.parametrize("lk", [30, 100, 256, 400, 1500, [30, 900], [900, 30]])
+def test_bf16_score_gradients_are_not_rounded_once(lk):
+    # ds in two bf16 parts carries 16 bits: what is left is the result's own rounding, with the fp32 chain and the order of
+    # sums far below it. Rounded once, each term is off by as much of itself as the result's rounding is of the result, and the
+    # terms cancel: both errors are independent and at least as large, sqrt(2) in all. Halfway between 1 and 1.5.
+    dq, dk = _off_by(lk, 2)
+    say(f"lk={lk}: dq {dq:.3f}, dk {dk}")
+    assert dq < 1.25 and max(dk) < 1.25
