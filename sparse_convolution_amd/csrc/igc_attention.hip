@@ -414,13 +414,31 @@ struct FwdShape<float, DP> {
 constexpr int kFewRows = 4;
 
 // Query rows of a tile: a few (k_attn_few) or those of the matrix kernel. Decided from the average number of rows
-// that share a key head in a sequence; either kernel takes any number of rows. Measured, bf16, few / matrix: 64 x 4096
-// keys, 8 key heads of 64, 1, 2, 4 and 8 rows 115 / 192, 117 / 188, 125 / 186 and 184 / 101 us; 100,000 keys, 8 heads of
-// 128, 1 row 99 / 93, 4 rows 103 / 91; 32 x 2048 keys, 2 heads of 128, 4 rows 36 / 23.
+// that share a key head in a sequence; either kernel takes any number of rows. The whole batch takes one form: a sequence of
+// many rows among empty ones runs through tiles of a few, its keys read again for each. us a call, few / matrix, with 1, 2
+// and 4 rows:
+//                                bf16                                    fp32
+//   64 x 4096 keys, 8 heads
+//     of 32                      88 / 123   93 / 123   104 / 124         118 / 209   121 / 210   128 / 211
+//     of 64                      117 / 151  120 / 151  129 / 152         195 / 336   199 / 339   204 / 344
+//     of 128                     199 / 193  202 / 193  217 / 193         382 / 728   386 / 729   393 / 730
+//   100,000 keys, 8 heads
+//     of 32                      49 / 59    54 / 59    60 / 60           59 / 83     61 / 83     69 / 84
+//     of 64                      60 / 71    63 / 72    70 / 72           88 / 136    91 / 137    95 / 138
+//     of 128                     102 / 93   100 / 94   106 / 94          164 / 303   164 / 302   165 / 301
+//   32 x 2048 keys, 2 heads
+//     of 32                      20 / 19    24 / 19    30 / 19           21 / 24     23 / 24     30 / 24
+//     of 64                      20 / 21    24 / 21    32 / 21           23 / 31     26 / 31     33 / 31
+//     of 128                     25 / 24    29 / 24    37 / 24           33 / 64     35 / 64     42 / 65
+// So a few rows take k_attn_few, but for bf16 heads over 64, where the matrix kernel is ahead throughout. What the rule
+// gives away is up to 11 us a call on small problems, bf16 in the main, whose parts of 256 keys leave the GPU half empty.
+// 8 rows of bf16, 64 x 4096 keys, 8 heads of 64: 184 / 101.
 int fwd_rows(int dtype, int dim, int64_t nq, int batch, int group) {
   const int64_t rows = (nq + batch - 1) / batch * group;
-  for (int r = 1; r <= (dim <= 64 ? kFewRows : 2); r *= 2)
-    if (rows <= r) return r;
+  if (dtype == IGC_F32 || dim <= 64) {
+    for (int r = 1; r <= kFewRows; r *= 2)
+      if (rows <= r) return r;
+  }
   return dtype == IGC_BF16 && dim <= 64 ? 256 : 128;
 }
 
@@ -455,8 +473,7 @@ void fwd_t(const AttnArgs& a, int dtype, hipStream_t s) {
   if (rows <= kFewRows) {
     if (a.dim <= 32) few_r<T, 4>(a, rows, wgs, s);
     else if (a.dim <= 64) few_r<T, 8>(a, rows, wgs, s);
-    else if (rows == 1) few_go<T, 16, 1>(a, wgs, s);
-    else few_go<T, 16, 2>(a, wgs, s);
+    else if constexpr (sizeof(T) == 4) few_r<T, 16>(a, rows, wgs, s);
   } else {
     if (a.dim <= 32) fwd_go<T, 32>(a, wgs, s);
     else if (a.dim <= 64) fwd_go<T, 64>(a, wgs, s);
@@ -475,8 +492,10 @@ int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int
   const int64_t per_seq = (nq + batch - 1) / batch * (heads / kv_heads);
   const int64_t wgs = batch * ((per_seq + bm - 1) / bm) * kv_heads;
   // Workgroups that fill it: two a CU of the matrix kernel, three of its fp32 form for short heads, which is small enough
-  // and waits more. 300 queries on 43,217 keys, 256 channels, us with 512 / 768 / 1024: fp32 heads of 32 121 / 114 / 116, of 64
-  // 102 / 118 / 111, of 128 125 / 145 / 145; bf16 56 / 58 / 68, 44 / 56 / 57 and 49 / 59 / 60.
+  // and waits more. 300 queries on 43,217 keys, 256 channels, us with 512 / 768 / 1024: fp32 heads of 32 119 / 112 / 114, of 64
+  // 102 / 118 / 111, of 128 125 / 145 / 145; bf16 56 / 58 / 68, 44 / 56 / 57 and 49 / 59 / 60. fp32 heads of 32 at other sizes: 900
+  // queries on 8,000 keys, 8 heads, 68 / 65 / 67; 500 on 20,000, 4 heads, 47 / 47 / 48; 100 on 40,000, 8 heads, 48 / 50 / 52;
+  // heads of 16, the first three of these sizes: 117 / 104 / 106, 68 / 62 / 63 and 46 / 45 / 45.
   const int64_t fill = bm <= kFewRows ? 2048 : dtype == IGC_F32 && dim <= 32 ? 768 : 512;
   const int64_t want = wgs >= fill ? 1 : fill / std::max<int64_t>(1, wgs);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxParts), nk / batch / 256));

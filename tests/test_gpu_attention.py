@@ -431,3 +431,11 @@ def test_bf16_score_gradients_are_not_rounded_once(lk):
     dq, dk = _off_by(lk, 2)
     say(f"lk={lk}: dq {dq:.3f}, dk {dk}")
     assert dq < 1.25 and max(dk) < 1.25
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(2, 2, 96), (4, 2, 128), (8, 2, 100), (3, 1, 72), (4, 1, 65)])
+def test_a_few_rows_of_wide_heads(heads, kv_heads, dim, dtype):
+    # 1 to 4 rows that share a key head: one part and several parts of the key axis, a sequence without keys.
+    check([1, 1, 1], [90, 0, 1300], heads, kv_heads, dim, dtype)
+    check([1], [3001], heads, kv_heads, dim, dtype, masked=0.3)
