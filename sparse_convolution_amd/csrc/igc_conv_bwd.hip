@@ -369,8 +369,8 @@ int launch_wgrad_reduce(const float* part, int64_t chunks, int64_t E, float* dw,
 
 namespace {
 
-// feats.codes != nullptr: the input rows come from an 8-bit checkpoint.
-template <int MB, int NB, int NWV>
+// feats.codes != nullptr: the input rows come from an 8-bit checkpoint (ONLY_Q8: always).
+template <int MB, int NB, int NWV, bool ONLY_Q8 = false>
 int launch_wgrad_bf16(const igc_grid* g, const int32_t* d_map, const FeatsIn& feats, int32_t cin,
                       const void* d_dout, int32_t cout, float* d_dw, hipStream_t s) {
   const int64_t N = g->n_voxels;
@@ -411,7 +411,7 @@ int launch_wgrad_bf16(const igc_grid* g, const int32_t* d_map, const FeatsIn& fe
     if (feats.codes)
       k_wgrad_bf16<MB, NB, NWV, true><<<wgs, 64 * NWV, 0, s>>>(d_map, N, perm, blk, nullptr, feats.codes, feats.scales,
                                                              (const uint16_t*)d_dout, cin, cout, n_tiles, tpc, sp, part);
-    else
+    else if constexpr (!ONLY_Q8)
       k_wgrad_bf16<MB, NB, NWV, false><<<wgs, 64 * NWV, 0, s>>>(d_map, N, perm, blk, (const uint16_t*)feats.x, nullptr,
                                                               nullptr, (const uint16_t*)d_dout, cin, cout, n_tiles, tpc,
                                                               sp, part);
@@ -520,7 +520,7 @@ int launch_conv_backward(const igc_grid* g, const int32_t* d_map, const FeatsIn&
         // voxels 30 / 21 / 16, 10,000 79 / 57 / 48, 43,264 96 / 88 / 104, 169,744 216 / 265 / 327.
         const int64_t blocks = (g->n_voxels + 11 * kTileRows - 1) / (11 * kTileRows) * (cin / 128) * (cout / 128);
         if (blocks <= 8) return launch_wgrad_bf16<64, 64, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
-        if (blocks <= 24) return launch_wgrad_bf16<64, 128, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
+        if (blocks <= 24) return launch_wgrad_bf16<64, 128, 4, true>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
       }
       if (cin % 128 == 0 && cout % 128 == 0)
         return launch_wgrad_bf16<128, 128, 4>(g, d_map, feats, cin, d_dout, cout, d_dw, s);
