@@ -174,6 +174,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int mm = 0; mm < 2; ++mm) {
+        // bf16 data: p rounded once, since the matrix cores take bf16. out is then off by 1.26 to 1.39 times what its own
+        // rounding costs (30 to 1,500 keys, heads of 64, rms against 64 bits). In two parts it is off by 1.00, but a second
+        // product and the remainders cost 30 to 33% (215,003 x 5 x ~1024, 4 heads of 64: 291 and 382 us; 60,000 x 1,500, 256
+        // channels, heads of 32, 64 and 128: 167 and 222, 125 and 165, 118 and 154).
         frag p[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) p[n] = to_frag<T>(s[n][t], mm);

@@ -310,6 +310,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         frag fp[NK], fs[NK], lo[NK];
 #pragma unroll
         for (int n = 0; n < NK; ++n) {
+          // bf16 data: rounded once, as in the forward pass. dv is off by 1.38 to 1.45 times its own rounding; in two parts by
+          // 1.00, for 5 to 10% of the backward pass (60,000 x 1,500, heads of 32, 64 and 128: 543 and 599 us, 450 and 490, 471
+          // and 496). p is positive, so the error is at most 2^-8 of the sum of p |dout| (in out 2^-8 of the sum of p |v|);
+          // that of ds can be far more than its sum.
           fp[n] = to_frag<T>(s[n], mm);
           to_frag2<T>(dp[n], mm, fs[n], lo[n]);
         }
