@@ -347,9 +347,9 @@ int igc_layer_norm_q8_backward(const void* d_dy, const int8_t* d_codes, const fl
  *    and head strides (elements): slices of one projection need no copy. Query head h reads key head
  *    h / (heads / kv_heads). dim is 1 to 128.
  *  - Sequence b holds query rows d_q_offsets[b] .. d_q_offsets[b+1] and key rows d_kv_offsets[b] ..
- *    d_kv_offsets[b+1] (int32 device arrays [batch + 1], ascending from 0 to n_q and n_k; they may both be NULL
- *    with batch 1). Sequences may be empty on either side. Offsets are clamped to the arrays, so wrong ones
- *    cannot reach outside; rows that no sequence covers are left unwritten.
+ *    d_kv_offsets[b+1] (int32 device arrays [batch + 1], ascending; they may both be NULL with batch 1: one sequence of
+ *    all rows). Sequences may be empty on either side. Rows before the first sequence and after the last take no
+ *    part, and their results are left unwritten. Offsets are clamped to the arrays, so wrong ones cannot reach outside.
  *  - d_key_mask (uint8 [n_k], may be NULL): rows with 0 are left out. Their k and v may hold anything.
  *  - scale multiplies q . k; positive, and finite times log2(e). */
 typedef struct {

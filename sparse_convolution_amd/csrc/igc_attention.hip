@@ -8,10 +8,11 @@
 //
 // Long against long, the vector unit bounds it beside the matrix cores: 425 vector instructions (exponentials,
 // sums, maxima, rounding) for the 32 matrix instructions of a wave's 64 x 64 scores with heads of 64, at two waves
-// per SIMD. bf16, 215,003 queries on 5 x ~1024 keys, 4 heads of 64: 283 to 307 us, 720 to 780 TFLOP/s. fp32, 300
-// queries on 43,217 keys, 8 heads of 32: 111 us in all, 119 TFLOP/s. Single tokens (k_attn_few) read K and
-// V once: 64 on 262,147 keys, 8 heads of 64, about half of the keys in sequences with a query: 40 us and 4 to join, some
-// 6.7 TB/s.
+// per SIMD. bf16, 215,003 queries on 5 x ~1024 keys, 4 heads of 64: 278 to 309 us by the GPU's clock, 715 to 795 TFLOP/s.
+// fp32, 300 queries on 43,217 keys, 8 heads of 32: 110 to 123 us in all, 108 to 121 TFLOP/s. Single tokens (k_attn_few) read
+// K and V once: 64 sequences of one query and 4,096 keys, 8 heads of 64, bf16 117 us, 4.6 TB/s, fp32 194 us, 5.5 TB/s. 64
+// queries on 262,147 keys where half of the sequences have no query and one has 33: 39 us and 5 to join; the 81,157 keys
+// in use are 166 MB, 4.3 TB/s, and that one sequence's keys are read 33 times, once for each row (see fwd_rows).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -7,11 +7,13 @@
 //
 // Two kernels, each keeping its output in registers while it walks the other axis: k_attn_dq owns
 // query rows and walks keys, k_attn_dkv owns keys and walks query rows, so nothing is added by atomics
-// and reruns are bit-identical. Scores are computed again in both (seven products instead of five).
+// and reruns are bit-identical. Scores are computed again in both (seven products instead of five; nine with bf16 data, where
+// those with ds are done in two parts).
 //
-// With bf16 data p is rounded to bf16 for dv, whose terms it weighs one by one; ds is kept in two bf16 parts for dq and
-// dk, since its terms cancel (see k_attn_dkv for both sides). Bound like the forward pass, by the vector unit beside the matrix cores: bf16,
-// 100,003 queries, 4 heads on 2 key heads of 64, three sequences of ~800 keys: dq 213 us, dk and dv 211, sums 7.
+// With bf16 data p is rounded to bf16 for dv; ds is kept in two bf16 parts for dq and dk, since its terms cancel (see
+// k_attn_dkv for both sides). Bound like the forward pass, by the vector unit beside the matrix cores: bf16, 100,003 queries,
+// 4 heads on 2 key heads of 64, three sequences of ~800 keys: 443 us in all (400 with ds rounded once for dk, on the same GPU);
+// under the profiler, whose clock is lower, dq 227 us, dk and dv 290, sums 7.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -180,12 +182,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 }
 
 // dk and dv: four waves of 32 NK keys each over tiles of BQ query rows of the sequence. bf16 data: ds in two parts for the
-// product with q, as for dq, its terms cancel too: rounded once, dk is off by 1.40 to 1.46 times what its own rounding to
-// bf16 costs (30 to 1,500 keys a sequence, 256 queries, heads of 64, rms against 64 bits), in two parts by 1.00. The second
-// product costs 4 to 12% of the backward pass over 300 to 1,500 keys (60,000 queries, heads of 128 to 32: 433 and 453 us, 466 and
-// 521), for all lengths alike, so that a sequence's gradients are as exact whatever its neighbours are. A score costs its exponential, two multiplications,
-// three roundings and a remainder: the products with dout start from -delta (read into their accumulators from LDS), and what the mask leaves out is
-// cleared in the results instead of per score (100,003 queries, three sequences of ~800 keys, 4 heads of 64: 252 and 223 us).
+// product with q, as for dq, since its terms cancel too: rounded once, dk is off by 1.40 to 1.46 times what its own rounding
+// to bf16 costs (30 to 1,500 keys a sequence, 256 queries, heads of 64, rms against 64 bits), in two parts by 1.00. The
+// second product costs 4 to 12% of the backward pass over 300 to 1,500 keys (60,000 queries on 1,500 keys, heads of 128 and of
+// 32: 433 and 453 us, 466 and 521). It is done at every length, so that a sequence's gradients are as exact whatever its
+// neighbours are. A score costs its exponential, two multiplications, three roundings and a remainder: the products with dout
+// start from -delta (read into their accumulators from LDS), and what the mask leaves out is cleared in the results
+// instead of per score (100,003 queries, three sequences of ~800 keys, 4 heads of 64, ds rounded once: 252 and 223 us).
 template <typename T, int DP, int NK, int BQ, int WPE, bool VEC>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
   typedef Frag<T> frag;
@@ -216,7 +219,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   // Query rows step through the heads of the group before the next query.
   const int n_rows = (int)(r1 - r0);
   Stage<T, BQ, DP, kNT, VEC> sq, so;
-  float n_lse = 0.f, n_delta = 0.f;  // as loaded: worked on a tile later (223 and 211 us)
+  float n_lse = 0.f, n_delta = 0.f;  // as loaded: worked on a tile later (with ds rounded once 223 and 211 us)
   auto fetch = [&](int t0) {
     sq.load(n_rows - t0);
     so.load(n_rows - t0);
@@ -406,10 +409,10 @@ void sum_go(const float* part0, const float* part1, int splits, const int32_t* o
 
 // Tiles of the two kernels: 32 NQ (NK) query rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
 // bf16, measured on 60,000 queries x 1,500 keys and 256 channels (dq / dkv, us; with ds rounded once and delta subtracted
-// per score, where dq of 64 took 175 and now takes 220, dkv 231 and now 208): heads of 32: dq 209 with three waves, 228
-// with NQ 2; dkv 286 with NK 2, 346 with NK 1. Heads of 64: dq 175 with NQ 2 on 32-key tiles, 184 on 64, 187 with NQ 1;
-// dkv 231, with NK 2 (one wave) 317, on 32-row tiles 254. Heads of 128: dq 184 with two waves, 242 with one; dkv 290 with
-// one wave, 470 with two (spills).
+// per score. Since then, with heads of 64: ds in two parts took dq from 175 to 220; delta as the products' start took dkv from 231
+// to 208, and ds in two parts adds 41): heads of 32: dq 209 with three waves, 228 with NQ 2; dkv 286 with NK 2, 346 with
+// NK 1. Heads of 64: dq 175 with NQ 2 on 32-key tiles, 184 on 64, 187 with NQ 1; dkv 231, with NK 2 (one wave) 317, on
+// 32-row tiles 254. Heads of 128: dq 184 with two waves, 242 with one; dkv 290 with one wave, 470 with two (spills).
 template <typename T, int DP>
 struct BwdShape;
 template <int DP>

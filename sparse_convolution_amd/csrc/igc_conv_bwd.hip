@@ -87,6 +87,7 @@ struct WgradSplit {
 // at once: each stage's loads then depend on LDS only, and two stages of them are in flight, where the
 // chain of row order, map and data costs a memory round trip per stage. Kernel, us, before and after: 128 -> 128
 // on 43,264 voxels 111 and 88, on 169,744 260 and 215; 64 -> 64 on 43,264 69 and 48. Batches of 12: 86, 236 and 48.
+// Features keep the walk stage by stage that they had; the batched one has not been measured with them.
 template <int MB, int NB, int NWV, bool Q8>
 __global__ __launch_bounds__(64 * NWV) __attribute__((amdgpu_waves_per_eu(3))) void k_wgrad_bf16(const int32_t* __restrict__ map, int64_t N,
                                                     const int32_t* __restrict__ perm,
