@@ -1,11 +1,12 @@
 """Host code under AddressSanitizer and UndefinedBehaviorSanitizer (CPU only).
 
-Two small drivers are built in a temporary directory and run as child processes:
+Small drivers are built in a temporary directory and run as child processes:
   - tests/sanitize/oracle_driver.cpp: every C entry point of the CPU oracle (g++);
   - tests/sanitize/tuning_driver.cpp: the library's tuning-file parser, igc_tuning.cpp, compiled
-    for the host only by hipcc with the sanitizers on the host side (clang's runtimes).
-Any sanitizer finding aborts the driver (-fno-sanitize-recover=all), so the test passes only when
-both exit 0 and print their "ok" line.
+    for the host only by hipcc with the sanitizers on the host side (clang's runtimes);
+  - tests/sanitize/ragged_driver.cpp: the index arithmetic of ragged sequences, igc_ragged.h, built likewise.
+Any sanitizer finding aborts the driver (-fno-sanitize-recover=all), so the tests pass only when
+they exit 0 and print their "ok" line.
 """
 import os
 import shutil
