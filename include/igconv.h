@@ -388,6 +388,54 @@ int igc_cross_attention_backward(const igc_attention_t* problem, const void* d_q
                                  const void* d_out, const float* d_lse, const void* d_dout, void* d_dq, void* d_dk,
                                  void* d_dv, void* d_ws, size_t ws_bytes, igc_stream stream);
 
+/* Queries and keys of one attention over n rows, before they meet: a norm over each head's channels and the rotation
+ * of channel pairs by the row's positions. All arrays are device memory.
+ *  - q is [n, heads, dim], k [n, kv_heads, dim] of type `dtype`, dim contiguous, with any row and head strides
+ *    (elements); kv_heads 0: no keys. dim is 1 to 128, heads + kv_heads at most 65535.
+ *  - d_positions int32 [n, axes], d_frequencies float [axes, pairs]; axes is 0 (no rotation) to 3 (voxel
+ *    coordinates), 2 * axes * pairs at most dim. Pair t = a * pairs + i turns by the angle d_positions[row, a] *
+ *    d_frequencies[a, i]. layout 0 (halves): channels t and axes * pairs + t; 1 (interleaved): 2 t and 2 t + 1. Channels from
+ *    2 * axes * pairs on do not turn.
+ *  - norm != 0: z = x / sqrt(mean(x^2) + eps) * w over the head's channels, else z = x. */
+typedef struct {
+  int32_t dtype, heads, kv_heads, dim, axes, pairs, layout, norm;
+  float eps, amplitude;
+  int64_t n;
+  int64_t q_stride[2], k_stride[2]; /* between rows, between heads */
+  const int32_t* d_positions;
+  const float* d_frequencies;
+} igc_qk_t;
+
+/* d_yq [n, heads, dim] and d_yk [n, kv_heads, dim] (dense, type `dtype`): for the pair (z1, z2) of angle t
+ *     y1 = amplitude * (z1 cos t - z2 sin t), y2 = amplitude * (z2 cos t + z1 sin t),
+ * and y = z elsewhere. d_qw and d_kw [dim] of type `wdtype` (IGC_F32 or `dtype`; NULL: ones). Sums and products are fp32, the
+ * angle is reduced in 64 bits (far positions keep fp32 accuracy), the result is rounded once. Outputs must not alias inputs. */
+int igc_qk_norm_rotary(const igc_qk_t* problem, const void* d_q, const void* d_k, const void* d_qw, const void* d_kw,
+                       int32_t wdtype, void* d_yq, void* d_yk, igc_stream stream);
+
+/* Bytes of d_ws that the backward pass needs where weight gradients are given (host only). */
+int igc_qk_norm_rotary_workspace(const igc_qk_t* problem, size_t* bytes);
+
+/* Gradients for d_dyq and d_dyk (dense, type `dtype`): with g the transposed rotation of dy, h = g * w, r = 1 / sqrt(mean(x^2)
+ * + eps) and xhat = x * r,
+ *     d_dq, d_dk = r * (h - xhat * mean(h * xhat))    (dense, type `dtype`)
+ *     d_dqw, d_dkw = sum over rows and heads of g * xhat    (float [dim]; NULL d_dqw skips both, d_dkw is not read without keys)
+ * Without the norm d_dq = g, and d_q, d_k and the weights are not read. Sums over rows are fp32 within a workgroup and fp64
+ * across workgroups in a fixed order (reruns are bit-identical). d_ws as above (IGC_ERR_CAPACITY otherwise). */
+int igc_qk_norm_rotary_backward(const igc_qk_t* problem, const void* d_dyq, const void* d_dyk, const void* d_q, const void* d_k,
+                                const void* d_qw, const void* d_kw, int32_t wdtype, void* d_dq, void* d_dk, float* d_dqw,
+                                float* d_dkw, void* d_ws, size_t ws_bytes, igc_stream stream);
+
+/* Dropout of `count` elements of type `dtype`, e = 0, 1, ... in memory order:
+ *     d_y[e] = d_residual[e] + (bits(e) >= drop ? d_x[e] * 65536 / (65536 - drop) : 0), drop = rint(65536 p)
+ * rounded once (d_residual NULL: no sum; p = 1 drops everything). bits(e) is the (e % 8)-th 16 bits, low half of a word first, of
+ * Philox 4x32 with ten rounds, key words (seed low, seed high), counter words (e / 8 low, e / 8 high, offset low, offset
+ * high), the offset being `offset` plus *d_offset (device memory, may be NULL: a captured graph can count its steps there). Nothing else
+ * enters, so the call on dL/dY with the same p, seed and offset is the backward pass. 0 <= p <= 1. d_y may be d_x or d_residual;
+ * arrays must not overlap otherwise. */
+int igc_dropout(const void* d_x, const void* d_residual, int64_t count, int32_t dtype, double p, uint64_t seed,
+                uint64_t offset, const uint64_t* d_offset, void* d_y, igc_stream stream);
+
 /* Output grid of a 3x3x3 convolution with per-axis stride h_stride[0..2] (host, each 1, 2 or 3)
  * over `in` (the grid-to-grid ops ConvGrid and ConvTransposeGrid in the op table of the "ONNX
  * Runtime support for fVDB operations" proposal; the pages name the ops without a formula, so

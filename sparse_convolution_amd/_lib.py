@@ -15,6 +15,7 @@ EXPORTS = (
     "igc_last_error", "igc_sparse_conv_backward_q8", "igc_layer_norm", "igc_layer_norm_q8", "igc_layer_norm_workspace",
     "igc_layer_norm_backward", "igc_layer_norm_q8_backward", "igc_checkpoint_pack", "igc_checkpoint_unpack",
     "igc_cross_attention", "igc_cross_attention_backward", "igc_cross_attention_workspace",
+    "igc_qk_norm_rotary", "igc_qk_norm_rotary_backward", "igc_qk_norm_rotary_workspace", "igc_dropout",
 )
 
 STATUS = {
@@ -56,6 +57,15 @@ class Attention(ctypes.Structure):  # igc_attention_t
     ]
 
 
+class Qk(ctypes.Structure):  # igc_qk_t
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+        ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32), ("layout", ctypes.c_int32), ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("amplitude", ctypes.c_float), ("n", ctypes.c_int64), ("q_stride", ctypes.c_int64 * 2),
+        ("k_stride", ctypes.c_int64 * 2), ("d_positions", ctypes.c_void_p), ("d_frequencies", ctypes.c_void_p),
+    ]
+
+
 class IgcError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -75,7 +85,7 @@ def load() -> ctypes.CDLL:
             "(hipcc, gfx950). There is no non-HIP fallback.")
     lib = ctypes.CDLL(LIB_PATH)
     P, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
-    f32, size = ctypes.c_float, ctypes.c_size_t
+    f32, size, u64 = ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64
     sig = {
         "igc_grid_build": [P, i64, ctypes.POINTER(Allocator), P, ctypes.POINTER(P)],
         "igc_grid_destroy": [P],
@@ -106,6 +116,10 @@ def load() -> ctypes.CDLL:
         "igc_cross_attention_workspace": [P, i32, ctypes.POINTER(size)],
         "igc_cross_attention": [P, P, P, P, P, P, P, size, P],
         "igc_cross_attention_backward": [P, P, P, P, P, P, P, P, P, P, P, size, P],
+        "igc_qk_norm_rotary_workspace": [P, ctypes.POINTER(size)],
+        "igc_qk_norm_rotary": [P, P, P, P, P, i32, P, P, P],
+        "igc_qk_norm_rotary_backward": [P, P, P, P, P, P, P, i32, P, P, P, P, P, size, P],
+        "igc_dropout": [P, P, i64, i32, ctypes.c_double, u64, u64, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)

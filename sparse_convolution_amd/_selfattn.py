@@ -1,0 +1,202 @@
+"""Operators of self-attention among voxels in grid order: the norm of queries and keys with the rotation by their
+positions, and dropout that stores no mask."""
+from __future__ import annotations
+
+import ctypes
+import functools
+import math
+import struct
+
+import torch
+
+from . import _lib
+from ._args import _dtype_code
+from ._block import _call, _heads, _ptr, _same
+
+LAYOUTS = {"half": 0, "interleaved": 1}
+_QK = struct.Struct("@iiiiiiiiffqqqqqPP")  # igc_qk_t
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, axes: int = 1, scaling: str | None = None, factor: float = 1.0,
+                       original: int | None = None, low: float = 1.0, high: float = 32.0) -> torch.Tensor:
+    """Frequencies float32 [axes, pairs] (on the host) for rotating `dim` channels of a head, pairs = dim // 2 // axes
+    on each of 1 to 3 position axes: base ** (-i / pairs). For positions up to `factor` times those trained on:
+    scaling="linear" divides all by factor; "base" raises the base so that the slowest frequency is divided by factor and the
+    fastest stays; "parts" divides those that make fewer than `low` turns over the `original` length, keeps
+    those that make more than `high`, and blends in between."""
+    if not 1 <= axes <= 3 or dim < 2 * axes:
+        raise ValueError("axes must be 1 to 3, and dim at least 2 a axis")
+    if not base > 0 or not factor > 0 or not math.isfinite(base) or not math.isfinite(factor):
+        raise ValueError("base and factor must be positive and finite")
+    pairs = dim // 2 // axes
+    i = torch.arange(pairs, dtype=torch.float64)
+    if scaling == "base" and pairs > 1:
+        base = base * factor ** (pairs / (pairs - 1))
+    f = base ** (-i / pairs)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if original is None or original < 1 or not 0 <= low < high:
+            raise ValueError("scaling in parts needs the original length and 0 <= low < high")
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'parts'")
+    return f.float().expand(axes, -1).contiguous()
+
+
+def _turn(positions, frequencies, n: int, layout: str, index: int) -> tuple[int, int, int]:
+    """Checks positions and frequencies and returns (axes, pairs, layout code)."""
+    if layout not in LAYOUTS:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    if (positions is None) != (frequencies is None):
+        raise ValueError("positions and frequencies come together")
+    if positions is None:
+        return 0, 0, LAYOUTS[layout]
+    if not isinstance(frequencies, torch.Tensor) or frequencies.dim() not in (1, 2):
+        raise ValueError("frequencies must have shape [pairs] or [axes, pairs]")
+    axes, pairs = (1, frequencies.shape[0]) if frequencies.dim() == 1 else frequencies.shape
+    _same(frequencies, "frequencies", torch.float32, frequencies.shape, index)
+    flat = axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1
+    _same(positions, "positions", torch.int32, (n,) if flat else (n, axes), index)
+    return axes, pairs, LAYOUTS[layout]
+
+
+def _weights(q_weight, k_weight, dim: int, dtype: torch.dtype, index: int) -> int:
+    """Checks the weights and returns the type code they share."""
+    first = q_weight if q_weight is not None else k_weight
+    if first is None:
+        return _dtype_code(dtype)
+    dt = first.dtype if isinstance(first, torch.Tensor) else None
+    if dt != torch.float32 and dt != dtype:
+        raise TypeError(f"weights must be float32 or {dtype}, got {dt}")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _same(t, name, dt, (dim,), index)
+    return _dtype_code(dt)
+
+
+def _problem(q, k, positions, frequencies, eps, layout, amplitude, norm) -> tuple[bytes, tuple]:
+    """The problem as an igc_qk_t, and the sizes its workspace depends on."""
+    dt = q.dtype
+    code, index = _dtype_code(dt), q.get_device()
+    _heads(q, "q", dt, index)
+    n, heads, dim = q.shape
+    kv_heads, ks = 0, (0, 0, 0)
+    if k is not None:
+        _heads(k, "k", dt, index)
+        if k.shape[0] != n or k.shape[2] != dim or k.shape[1] < 1:
+            raise ValueError(f"k must have shape [{n}, kv_heads, {dim}], got {tuple(k.shape)}")
+        kv_heads, ks = k.shape[1], k.stride()
+    axes, pairs, how = _turn(positions, frequencies, n, layout, index)
+    sizes = (code, heads, kv_heads, dim, axes, pairs, how, int(norm))
+    qs = q.stride()
+    p = _QK.pack(*sizes, eps, amplitude, n, qs[0], qs[1], ks[0], ks[1], _ptr(positions) or 0, _ptr(frequencies) or 0)
+    return p, sizes + (n,)
+
+
+def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None = None,
+                   frequencies: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                   k_weight: torch.Tensor | None = None, eps: float = 1e-6, layout: str = "half", amplitude: float = 1.0):
+    """Root-mean-square norm of each head of q [n, heads, dim] and k [n, kv_heads, dim] (None: queries alone) with weights [dim]
+    (float32 or q's type; None: ones), and the rotation of its channel pairs by positions (int32 [n] or [n, axes], up to three
+    axes: voxel coordinates) times frequencies (float32 [pairs] or [axes, pairs], see rotary_frequencies; both None: the norm
+    alone). layout "half": pair t is channels t and axes * pairs + t; "interleaved": 2 t and 2 t + 1; channels behind the pairs do not
+    turn. amplitude scales the pairs. dim is up to 128, row and head strides are free. Returns new (q, k), rounded once
+    (igc_qk_norm_rotary)."""
+    p, sizes = _problem(q, k, positions, frequencies, eps, layout, amplitude, True)
+    dt, dev = q.dtype, q.device
+    wd = _weights(q_weight, k_weight, q.shape[2], dt, dev.index)
+    yq = torch.empty(q.shape, dtype=dt, device=dev)
+    yk = torch.empty(k.shape, dtype=dt, device=dev) if k is not None else None
+    _call("igc_qk_norm_rotary", dev.index, p, q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), wd, yq.data_ptr(), _ptr(yk))
+    return yq, yk
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_workspace(*sizes: int) -> int:
+    n = ctypes.c_size_t(0)
+    # eps and the addresses do not matter to the size.
+    _lib.check(_lib.load().igc_qk_norm_rotary_workspace(_QK.pack(*sizes[:-1], 0.0, 1.0, sizes[-1], 0, 0, 0, 0, 0, 0), ctypes.byref(n)))
+    return n.value
+
+
+def qk_norm_rotary_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
+                            positions: torch.Tensor | None = None, frequencies: torch.Tensor | None = None,
+                            q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                            layout: str = "half", amplitude: float = 1.0, need_dweight: bool = True):
+    """Gradients of qk_norm_rotary for its outputs' gradients dq and dk (contiguous), from its inputs: (dq, dk of q's
+    type, dq_weight, dk_weight [dim] float32; the last two None without need_dweight, those of keys None without keys)
+    (igc_qk_norm_rotary_backward)."""
+    p, sizes = _problem(q, k, positions, frequencies, eps, layout, amplitude, True)
+    dt, dev = q.dtype, q.device
+    wd = _weights(q_weight, k_weight, q.shape[2], dt, dev.index)
+    _same(dq, "dq", dt, q.shape, dev.index)
+    if k is not None:
+        _same(dk, "dk", dt, k.shape, dev.index)
+    gq = torch.empty(q.shape, dtype=dt, device=dev)
+    gk = torch.empty(k.shape, dtype=dt, device=dev) if k is not None else None
+    dqw = dkw = ws = None
+    nbytes = 0
+    if need_dweight:
+        nbytes = _qk_workspace(*sizes)
+        dqw = torch.empty(q.shape[2], dtype=torch.float32, device=dev)
+        dkw = torch.empty(q.shape[2], dtype=torch.float32, device=dev) if k is not None else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _call("igc_qk_norm_rotary_backward", dev.index, p, dq.data_ptr(), _ptr(dk) if k is not None else None, q.data_ptr(), _ptr(k),
+          _ptr(q_weight), _ptr(k_weight), wd, gq.data_ptr(), _ptr(gk), _ptr(dqw), _ptr(dkw), _ptr(ws), nbytes)
+    return gq, gk, dqw, dkw
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, layout: str = "half", amplitude: float = 1.0):
+    """The rotation of qk_norm_rotary alone: x [n, heads, dim] turned by its positions (igc_qk_norm_rotary without the norm)."""
+    if positions is None or frequencies is None:
+        raise ValueError("the rotation needs positions and frequencies")
+    p, _ = _problem(x, None, positions, frequencies, 0.0, layout, amplitude, False)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _call("igc_qk_norm_rotary", x.get_device(), p, x.data_ptr(), None, None, None, _dtype_code(x.dtype), y.data_ptr(), None)
+    return y
+
+
+def rotary_backward(dy: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, layout: str = "half",
+                    amplitude: float = 1.0):
+    """Gradient of rotary for the output gradient dy (contiguous): the rotation back, times amplitude."""
+    if positions is None or frequencies is None:
+        raise ValueError("the rotation needs positions and frequencies")
+    p, _ = _problem(dy, None, positions, frequencies, 0.0, layout, amplitude, False)
+    _same(dy, "dy", dy.dtype, dy.shape, dy.get_device())
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    _call("igc_qk_norm_rotary_backward", dy.get_device(), p, dy.data_ptr(), None, None, None, None, None, _dtype_code(dy.dtype),
+          dx.data_ptr(), None, None, None, None, 0)
+    return dx
+
+
+def _dropout(x, p: float, seed: int, offset, residual):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    code, index = _dtype_code(x.dtype), x.get_device()
+    _same(x, "x", x.dtype, x.shape, index)
+    if residual is not None:
+        _same(residual, "residual", x.dtype, x.shape, index)
+    d_offset = None
+    if isinstance(offset, torch.Tensor):
+        _same(offset, "offset", torch.int64, (1,), index)
+        d_offset, offset = offset.data_ptr(), 0
+    if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
+        raise ValueError("seed and offset must be 0 to 2^64 - 1")
+    y = torch.empty_like(x)
+    _call("igc_dropout", index, x.data_ptr(), _ptr(residual), x.numel(), code, p, seed, offset, d_offset, y.data_ptr())
+    return y
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int | torch.Tensor = 0, residual: torch.Tensor | None = None):
+    """x (any shape, contiguous) with each element dropped with probability p (a multiple of 2^-16 is taken) and the others scaled so that
+    the expected value stays, plus residual. What is dropped depends on (p, seed, offset) and the element's index alone: no
+    mask is kept, and dropout_backward computes it again. Give every call of a step an offset of its own; offset may be an int64
+    tensor of one element on the device, so that a captured graph can count its steps (igc_dropout)."""
+    return _dropout(x, p, seed, offset, residual)
+
+
+def dropout_backward(dy: torch.Tensor, p: float, seed: int, offset: int | torch.Tensor = 0):
+    """Gradient of dropout with the same p, seed and offset for the output gradient dy; residual's is dy itself."""
+    return _dropout(dy, p, seed, offset, None)

@@ -1,5 +1,5 @@
 // extern "C" entry points of the operators between convolutions: layer norm, 8-bit activation
-// checkpoints and cross attention. Every check runs on the host before any launch.
+// checkpoints, cross attention, norm and rotation of queries and keys, dropout. Every check runs on the host before any launch.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -127,9 +127,122 @@ int check_workspace(const char* fn, const void* ws, size_t ws_bytes, size_t need
   return IGC_OK;
 }
 
+// Checks the problem's description and fills the device arguments (fn names the call).
+int qk_args(const char* fn, const igc_qk_t* p, QkArgs& a) {
+  clear_error();
+  const std::string f(fn);
+  if (!p) return set_error(IGC_ERR_INVALID_ARG, f + ": the problem is null");
+  if (p->dtype != IGC_F32 && p->dtype != IGC_BF16) return set_error(IGC_ERR_INVALID_ARG, f + ": bad dtype");
+  if (p->n < 0) return set_error(IGC_ERR_INVALID_ARG, f + ": n is negative");
+  if (p->heads < 1 || p->kv_heads < 0 || p->dim < 1)
+    return set_error(IGC_ERR_INVALID_ARG, f + ": heads and dim must be positive, kv_heads not negative");
+  if (p->dim > kAttnMaxDim)
+    return set_error(IGC_ERR_UNSUPPORTED, f + ": at most " + std::to_string(kAttnMaxDim) + " channels a head");
+  if (p->n > INT32_MAX) return set_error(IGC_ERR_RANGE, f + ": n exceeds 2^31-1");
+  if ((int64_t)p->heads + p->kv_heads > 65535) return set_error(IGC_ERR_RANGE, f + ": at most 65535 heads in all");
+  if (p->axes < 0 || p->axes > 3) return set_error(IGC_ERR_INVALID_ARG, f + ": axes must be 0 to 3");
+  if (p->axes > 0 && (p->pairs < 1 || 2 * (int64_t)p->axes * p->pairs > p->dim))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": the pairs of all axes must fit the head");
+  if (p->layout != 0 && p->layout != 1) return set_error(IGC_ERR_INVALID_ARG, f + ": layout must be 0 (halves) or 1 (interleaved)");
+  if (p->norm && (!(p->eps >= 0.f) || std::isinf(p->eps)))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": eps must be finite and >= 0");
+  if (!std::isfinite(p->amplitude)) return set_error(IGC_ERR_INVALID_ARG, f + ": amplitude must be finite");
+  a.fn = fn, a.dtype = p->dtype, a.n = p->n, a.dim = p->dim, a.heads[0] = p->heads, a.heads[1] = p->kv_heads;
+  for (int i = 0; i < 2; ++i) a.xs[0][i] = p->q_stride[i], a.xs[1][i] = p->k_stride[i];
+  a.axes = p->axes, a.pairs = p->axes ? p->pairs : 0, a.interleaved = p->layout, a.norm = p->norm != 0;
+  a.eps = p->eps, a.amplitude = p->amplitude, a.positions = p->d_positions, a.frequencies = p->d_frequencies;
+  return IGC_OK;
+}
+
+// The rest of a call's checks: arrays for n rows, and the weights' type.
+int qk_arrays(QkArgs& a, int32_t wdtype, bool inputs) {
+  const std::string f(a.fn);
+  if (wdtype != IGC_F32 && wdtype != a.dtype)
+    return set_error(IGC_ERR_INVALID_ARG, f + ": weights must be fp32 or of the data's type");
+  a.wf32 = wdtype == IGC_F32;
+  for (int t = 0; t < 2; ++t)
+    if (a.heads[t] > 0 && ((inputs && !a.x[t]) || !a.y[t]))
+      return set_error(IGC_ERR_INVALID_ARG, f + ": an array of queries or keys is null");
+  if (a.axes > 0 && (!a.positions || !a.frequencies))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": d_positions or d_frequencies is null");
+  const void* in[] = {inputs ? a.x[0] : nullptr, inputs && a.heads[1] ? a.x[1] : nullptr, a.dy[0], a.heads[1] ? a.dy[1] : nullptr};
+  for (int t = 0; t < 2; ++t)
+    for (const void* x : in)
+      if (a.heads[t] > 0 && x && x == a.y[t]) return set_error(IGC_ERR_INVALID_ARG, f + ": an output aliases an input");
+  if (a.heads[1] > 0 && a.y[0] == a.y[1]) return set_error(IGC_ERR_INVALID_ARG, f + ": the outputs alias each other");
+  return IGC_OK;
+}
+
+size_t qk_bytes(const QkArgs& a) {
+  return a.n > 0 && a.norm ? (size_t)qk_parts(a.dtype, a.n, a.heads[0] + a.heads[1], a.dim) * 2 * a.dim * sizeof(float) : 0;
+}
+
 }  // namespace
 
 extern "C" {
+
+int igc_qk_norm_rotary_workspace(const igc_qk_t* p, size_t* bytes) {
+  const char* fn = "igc_qk_norm_rotary_workspace";
+  QkArgs a;
+  const int rc = qk_args(fn, p, a);
+  if (rc) return rc;
+  if (!bytes) return set_error(IGC_ERR_INVALID_ARG, "igc_qk_norm_rotary_workspace: bytes is null");
+  *bytes = qk_bytes(a);
+  return IGC_OK;
+}
+
+int igc_qk_norm_rotary(const igc_qk_t* p, const void* d_q, const void* d_k, const void* d_qw, const void* d_kw,
+                       int32_t wdtype, void* d_yq, void* d_yk, igc_stream stream) {
+  QkArgs a;
+  int rc = qk_args("igc_qk_norm_rotary", p, a);
+  if (rc || a.n == 0) return rc;
+  a.x[0] = d_q, a.x[1] = d_k, a.w[0] = d_qw, a.w[1] = d_kw, a.y[0] = d_yq, a.y[1] = d_yk;
+  rc = qk_arrays(a, wdtype, true);
+  return rc ? rc : launch_qk(a, false, (hipStream_t)stream);
+}
+
+int igc_qk_norm_rotary_backward(const igc_qk_t* p, const void* d_dyq, const void* d_dyk, const void* d_q, const void* d_k,
+                                const void* d_qw, const void* d_kw, int32_t wdtype, void* d_dq, void* d_dk, float* d_dqw,
+                                float* d_dkw, void* d_ws, size_t ws_bytes, igc_stream stream) {
+  const std::string f = "igc_qk_norm_rotary_backward";
+  QkArgs a;
+  int rc = qk_args("igc_qk_norm_rotary_backward", p, a);
+  if (rc) return rc;
+  if (d_dqw && !a.norm) return set_error(IGC_ERR_INVALID_ARG, f + ": without the norm there are no weight gradients");
+  if (d_dqw && a.heads[1] > 0 && !d_dkw) return set_error(IGC_ERR_INVALID_ARG, f + ": d_dqw and d_dkw come together");
+  if (a.n == 0 && !d_dqw) return IGC_OK;
+  a.x[0] = d_q, a.x[1] = d_k, a.w[0] = d_qw, a.w[1] = d_kw, a.dy[0] = d_dyq, a.dy[1] = d_dyk, a.y[0] = d_dq, a.y[1] = d_dk;
+  if (a.n > 0) {
+    if (!d_dyq || (a.heads[1] > 0 && !d_dyk)) return set_error(IGC_ERR_INVALID_ARG, f + ": d_dyq or d_dyk is null");
+    rc = qk_arrays(a, wdtype, a.norm);
+    if (rc) return rc;
+  }
+  if (d_dqw) {
+    a.dw[0] = d_dqw, a.dw[1] = a.heads[1] > 0 ? d_dkw : nullptr;
+    const size_t need = qk_bytes(a);
+    if (need > 0 && (!d_ws || ws_bytes < need))
+      return set_error(IGC_ERR_CAPACITY, f + ": needs " + std::to_string(need) + " bytes of workspace (igc_qk_norm_rotary_workspace)");
+    a.part = (float*)d_ws;
+    if (a.n == 0) return launch_pair_sum(a.fn, nullptr, 0, a.dim, a.dw[0], a.dw[1], (hipStream_t)stream);
+  }
+  return launch_qk(a, true, (hipStream_t)stream);
+}
+
+int igc_dropout(const void* d_x, const void* d_residual, int64_t count, int32_t dtype, double p, uint64_t seed,
+                uint64_t offset, const uint64_t* d_offset, void* d_y, igc_stream stream) {
+  clear_error();
+  if (dtype != IGC_F32 && dtype != IGC_BF16) return set_error(IGC_ERR_INVALID_ARG, "igc_dropout: bad dtype");
+  if (count < 0) return set_error(IGC_ERR_INVALID_ARG, "igc_dropout: count is negative");
+  if (!(p >= 0.0 && p <= 1.0)) return set_error(IGC_ERR_INVALID_ARG, "igc_dropout: p must be 0 to 1");
+  if (count == 0) return IGC_OK;
+  if (!d_x || !d_y) return set_error(IGC_ERR_INVALID_ARG, "igc_dropout: d_x or d_y is null");
+  DropoutArgs a;
+  a.dtype = dtype, a.x = d_x, a.residual = d_residual, a.y = d_y, a.count = count;
+  a.drop = (uint32_t)std::rint(65536.0 * p);
+  a.scale = a.drop < 65536 ? 65536.f / (float)(65536 - a.drop) : 0.f;
+  a.seed = seed, a.offset = offset, a.d_offset = d_offset;
+  return launch_dropout(a, (hipStream_t)stream);
+}
 
 int igc_cross_attention_workspace(const igc_attention_t* p, int32_t backward, size_t* bytes) {
   const char* fn = "igc_cross_attention_workspace";

@@ -217,6 +217,41 @@ int launch_norm(const NormArgs& a, hipStream_t s);
 // Workgroups of the backward pass; ws holds 2 c floats for each where dw is wanted.
 int norm_bwd_parts(int64_t n, int32_t c);
 int launch_norm_bwd(const NormArgs& a, void* ws, hipStream_t s);
+// first[e] and second[e] (null: skipped), e < c: the sums of part[chunk][e] and part[chunk][c + e] in fp64, in a fixed order.
+int launch_pair_sum(const char* fn, const float* part, int chunks, int c, float* first, float* second, hipStream_t s);
+
+// Dropout with a counter-based generator (igc_dropout.hip).
+struct DropoutArgs {
+  int32_t dtype = 0;
+  const void *x = nullptr, *residual = nullptr;
+  void* y = nullptr;
+  int64_t count = 0;
+  uint32_t drop = 0;  // elements with fewer than this in 16 bits are dropped
+  float scale = 1.f;
+  uint64_t seed = 0, offset = 0;
+  const uint64_t* d_offset = nullptr;  // added to offset
+};
+int launch_dropout(const DropoutArgs& a, hipStream_t s);
+
+// Norm and rotation of queries (0) and keys (1) for each head (igc_qk.hip); strides in elements.
+struct QkArgs {
+  const char* fn = "";
+  int32_t dtype = 0;
+  int64_t n = 0;
+  int dim = 0, heads[2] = {0, 0}, heads_each = 0;
+  const void *x[2] = {nullptr, nullptr}, *dy[2] = {nullptr, nullptr}, *w[2] = {nullptr, nullptr};
+  int64_t xs[2][2] = {{0, 0}, {0, 0}};  // row and head strides of x; y and dy are dense
+  void* y[2] = {nullptr, nullptr};      // y, or dx
+  int wf32 = 0;                         // w is fp32 (else the data's type)
+  const int32_t* positions = nullptr;   // [n, axes]
+  const float* frequencies = nullptr;   // [axes, pairs]
+  int axes = 0, pairs = 0, interleaved = 0, norm = 0;
+  float eps = 0.f, amplitude = 1.f;
+  float *part = nullptr, *dw[2] = {nullptr, nullptr};
+};
+// Partial weight gradients of the backward pass, 2 dim floats each.
+int qk_parts(int32_t dtype, int64_t n, int32_t heads, int32_t dim);
+int launch_qk(const QkArgs& a, bool backward, hipStream_t s);
 
 // One attention problem on the device; strides in elements.
 struct AttnArgs {

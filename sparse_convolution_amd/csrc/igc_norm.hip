@@ -269,7 +269,7 @@ __global__ __launch_bounds__(kNT) void k_norm_bwd(const T* __restrict__ dy, cons
   }
 }
 
-// dw[e] (e < c) and db[e - c] = sum over chunks of part[chunk][e] in fp64, in a fixed order.
+// dw[e] (e < c) and db[e - c] (null: skipped) = sum over chunks of part[chunk][e] in fp64, in a fixed order.
 __global__ __launch_bounds__(kNT) void k_norm_reduce(const float* __restrict__ part, int chunks, int c,
                                                      float* __restrict__ dw, float* __restrict__ db) {
   constexpr int EL = 16, NG = kNT / EL;
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(kNT) void k_norm_reduce(const float* __restrict__ p
 #pragma unroll
     for (int k = 0; k < NG; ++k) t += s_sum[k][el];
     if (e < c) dw[e] = (float)t;
-    else db[e - c] = (float)t;
+    else if (db) db[e - c] = (float)t;
   }
 }
 
@@ -364,10 +364,7 @@ int norm_bwd_t(const NormArgs& a, void* ws, hipStream_t s) {
         (const T*)a.dy, (const T*)a.x, a.mean, a.codes, a.scales, a.rstd, a.w, a.wf32, a.n, a.c, (T*)a.y, part);
   });
   IGC_HIP(hipGetLastError(), a.fn);
-  if (part) {
-    k_norm_reduce<<<(unsigned)((2 * a.c + 15) / 16), kNT, 0, s>>>(part, parts, a.c, a.dw, a.db);
-    IGC_HIP(hipGetLastError(), a.fn);
-  }
+  if (part) return launch_pair_sum(a.fn, part, parts, a.c, a.dw, a.db, s);
   return IGC_OK;
 }
 
@@ -378,6 +375,12 @@ int norm_bwd_parts(int64_t n, int32_t c) {
   // 768 workgroups, 154 with 512, 158 with 1024, 179 with 2048; from a checkpoint 126, 143, 133 and 154.
   const int64_t rows = 64;
   return (int)std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 768));
+}
+
+int launch_pair_sum(const char* fn, const float* part, int chunks, int c, float* first, float* second, hipStream_t s) {
+  k_norm_reduce<<<(unsigned)((2 * c + 15) / 16), kNT, 0, s>>>(part, chunks, c, first, second);
+  IGC_HIP(hipGetLastError(), fn);
+  return IGC_OK;
 }
 
 int launch_norm(const NormArgs& a, hipStream_t s) {

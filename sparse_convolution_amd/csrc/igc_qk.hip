@@ -1,0 +1,368 @@
+// Norm of queries and keys for each head and the rotation by their positions, in one pass over both, and its gradients.
+//
+//   rstd = 1 / sqrt(mean(x^2) + eps), z = x rstd w
+//   pair (z1, z2) of axis a and frequency f turns by positions[row, a] * f:
+//   y1 = amplitude (z1 cos - z2 sin), y2 = amplitude (z2 cos + z1 sin); channels behind the pairs: y = z
+//   backward: g = the transposed rotation of dy, h = g w, dx = rstd (h - xhat mean(h xhat)), dw = sum of g xhat, xhat = x rstd
+//
+// A row's cosines and sines are computed once for all of its heads: the workgroup's rows first make a table in LDS, then
+// the LPR lanes of a row keep what their channels need of it and walk the heads, V channels a load.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "igc_host.h"
+#include "igc_row.h"
+#include "igc_wave.h"
+
+namespace igc {
+namespace {
+
+constexpr int kNT = 256;
+
+// Cosine and sine of position * frequency. The product and its share of a turn are formed in 64 bits with the rounding
+// errors carried along, so that positions up to 2^31 keep an angle exact to fp32; the rest of an eighth of a turn to either
+// side goes through the Taylor series, whose first missing terms are below 2^-29.
+__device__ __forceinline__ float2 cos_sin(int32_t position, float frequency) {
+  constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591534e-18;  // 1 / (2 pi) in two parts
+  const double a = position, f = frequency;
+  const double p = a * f, p_low = fma(a, f, -p);
+  const double t = p * kTurn, t_low = fma(p_low, kTurn, fma(p, kTurnLow, fma(p, kTurn, -t)));
+  const double quarter = rint(4.0 * t);
+  const float x = (float)((fma(quarter, -0.25, t) + t_low) * 6.283185307179586);
+  const int q = (int)(quarter - 4.0 * floor(0.25 * quarter));
+  const float x2 = x * x;
+  const float s = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  const float c = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float u = q & 1 ? s : c, v = q & 1 ? c : s;
+  return make_float2(q == 1 || q == 2 ? -u : u, q >= 2 ? -v : v);
+}
+
+// What a lane holds of a head: NV times V channels.
+template <typename T, int V, int LPR, int NV>
+struct Head {
+  static constexpr int SL = kNT / LPR;       // rows of a workgroup
+  static constexpr int DP = LPR * NV * V;    // channels that the lanes could hold
+  // Rows of the table: cosines and sines of a row's pairs.
+  static constexpr int kTable = SL * (DP / 2 > 0 ? DP / 2 : 1);
+
+  static __device__ __forceinline__ int channel(int j, int i) { return (j * LPR + (int)threadIdx.x % LPR) * V + i; }
+
+  // Table of the workgroup's rows from r0 on.
+  static __device__ __forceinline__ void fill(const QkArgs& a, int64_t r0, float2* s_table) {
+    const int pairs = a.axes * a.pairs;
+    for (int e = threadIdx.x; e < SL * pairs; e += kNT) {
+      const int slot = e / pairs, p = e % pairs;
+      const int64_t r = r0 + slot;
+      if (r >= a.n) break;
+      float2 t = cos_sin(a.positions[r * a.axes + p / a.pairs], a.frequencies[p]);
+      s_table[e] = make_float2(t.x * a.amplitude, t.y * a.amplitude);
+    }
+  }
+  // This lane's factors: y[c] = z[c] co[c] + z[partner of c] si[c].
+  static __device__ __forceinline__ void factors(const QkArgs& a, const float2* s_table, float (&co)[NV][V], float (&si)[NV][V]) {
+    const int pairs = a.axes * a.pairs, slot = threadIdx.x / LPR;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int ch = channel(j, i);
+        co[j][i] = 1.f, si[j][i] = 0.f;
+        if (ch < 2 * pairs) {
+          const bool second = a.interleaved ? ch & 1 : ch >= pairs;
+          const float2 t = s_table[slot * pairs + (a.interleaved ? ch >> 1 : second ? ch - pairs : ch)];
+          co[j][i] = t.x;
+          si[j][i] = second ? t.y : -t.y;
+        }
+      }
+  }
+  // The partners' values of v; 0 for channels behind the pairs, whose own may be infinite. Channel c of a slot lies at (c % V) * 64 + its lane in the wave's part of LDS, so that neither
+  // the writes nor the reads, whose channels lie a fixed distance apart, meet in a bank.
+  static __device__ __forceinline__ void partners(const QkArgs& a, float* s_x, const float (&v)[NV][V], float (&o)[NV][V]) {
+    const int pairs = a.axes * a.pairs;
+    if (V % 2 == 0 && a.interleaved) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[j][i] = channel(j, i) < 2 * pairs ? v[j][i ^ 1] : 0.f;
+      return;
+    }
+    const int lane = lane_id(), first = lane / LPR * LPR;
+    wave_sync();  // the last values have been read
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_x[(j * V + i) * 64 + lane] = v[j][i];
+    wave_sync();
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int ch = channel(j, i);
+        const bool turns = ch < 2 * pairs;
+        const int to = !turns ? ch : a.interleaved ? ch ^ 1 : ch < pairs ? ch + pairs : ch - pairs;
+        const int group = to / V;
+        const float x = s_x[(group / LPR * V + to % V) * 64 + first + group % LPR];
+        o[j][i] = turns ? x : 0.f;
+      }
+  }
+  static __device__ __forceinline__ void load(const T* p, int dim, bool live, float (&v)[NV][V]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int ch = channel(j, 0);
+      if (live && ch < dim) {
+        load_vec<T, V>(p + ch, *(float(*)[V])&v[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] = 0.f;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int dim, bool live, const float (&v)[NV][V]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int ch = channel(j, 0);
+      if (live && ch < dim) store_vec<T, V>(p + ch, v[j]);
+    }
+  }
+  static __device__ __forceinline__ void weights(const void* w, int f32, int dim, float (&v)[NV][V]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int ch = channel(j, 0);
+      if (ch < dim) {
+        load_params<V>(w, ch, f32, 1.f, v[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] = 0.f;
+      }
+    }
+  }
+};
+
+// blockIdx.x: the rows, blockIdx.y: a share of the heads.
+template <typename T, int V, int LPR, int NV>
+__global__ __launch_bounds__(kNT) void k_qk(QkArgs a) {
+  typedef Head<T, V, LPR, NV> H;
+  __shared__ float2 s_table[H::kTable];
+  __shared__ float s_x[kNT / 64][NV * V * 64];
+  float* const s_mine = s_x[threadIdx.x >> 6];
+  const float inv_d = 1.0f / (float)a.dim;
+  const int h0 = blockIdx.y * a.heads_each, h1 = min(h0 + a.heads_each, a.heads[0] + a.heads[1]);
+  for (int64_t r0 = (int64_t)blockIdx.x * H::SL; r0 < a.n; r0 += (int64_t)gridDim.x * H::SL) {
+    const int64_t r = r0 + threadIdx.x / LPR;
+    const bool live = r < a.n;
+    float co[NV][V], si[NV][V];
+    __syncthreads();
+    H::fill(a, r0, s_table);
+    __syncthreads();
+    H::factors(a, s_table, co, si);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int first = max(h0 - (t ? a.heads[0] : 0), 0), last = min(h1 - (t ? a.heads[0] : 0), a.heads[t]);
+      if (first >= last) continue;
+      float w[NV][V];
+      H::weights(a.w[t], a.wf32, a.dim, w);
+      for (int h = first; h < last; ++h) {
+        float x[NV][V], o[NV][V];
+        H::load((const T*)a.x[t] + r * a.xs[t][0] + h * a.xs[t][1], a.dim, live, x);
+        float rstd = 1.f;
+        if (a.norm) {
+          float ss = 0.f;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) ss = fmaf(x[j][i], x[j][i], ss);
+          rstd = rsqrtf(fmaf(lanes_sum<LPR>(ss), inv_d, a.eps));
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[j][i] *= rstd * w[j][i];
+        H::partners(a, s_mine, x, o);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[j][i] = fmaf(x[j][i], co[j][i], o[j][i] * si[j][i]);
+        H::store((T*)a.y[t] + (r * a.heads[t] + h) * a.dim, a.dim, live, x);
+      }
+    }
+  }
+}
+
+template <typename T, int V, int LPR, int NV>
+__global__ __launch_bounds__(kNT) void k_qk_bwd(QkArgs a) {
+  typedef Head<T, V, LPR, NV> H;
+  __shared__ float2 s_table[H::kTable];
+  __shared__ float s_x[kNT / 64][NV * V * 64];
+  float* const s_mine = s_x[threadIdx.x >> 6];
+  const float inv_d = 1.0f / (float)a.dim;
+  const int h0 = blockIdx.y * a.heads_each, h1 = min(h0 + a.heads_each, a.heads[0] + a.heads[1]);
+  float aw[2][NV][V];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) aw[t][j][i] = 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * H::SL; r0 < a.n; r0 += (int64_t)gridDim.x * H::SL) {
+    const int64_t r = r0 + threadIdx.x / LPR;
+    const bool live = r < a.n;
+    float co[NV][V], si[NV][V];
+    __syncthreads();
+    H::fill(a, r0, s_table);
+    __syncthreads();
+    H::factors(a, s_table, co, si);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int first = max(h0 - (t ? a.heads[0] : 0), 0), last = min(h1 - (t ? a.heads[0] : 0), a.heads[t]);
+      if (first >= last) continue;
+      float w[NV][V];
+      H::weights(a.w[t], a.wf32, a.dim, w);
+      for (int h = first; h < last; ++h) {
+        float g[NV][V], x[NV][V], o[NV][V];
+        H::load((const T*)a.dy[t] + (r * a.heads[t] + h) * a.dim, a.dim, live, g);
+        if (a.norm) H::load((const T*)a.x[t] + r * a.xs[t][0] + h * a.xs[t][1], a.dim, live, x);
+        H::partners(a, s_mine, g, o);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[j][i] = fmaf(g[j][i], co[j][i], -o[j][i] * si[j][i]);
+        if (a.norm) {
+          float ss = 0.f, dot = 0.f;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              ss = fmaf(x[j][i], x[j][i], ss);
+              dot = fmaf(g[j][i] * w[j][i], x[j][i], dot);
+            }
+          // A row behind the last adds nothing to dw, not even NaN where eps is 0.
+          const float rstd = live ? rsqrtf(fmaf(lanes_sum<LPR>(ss), inv_d, a.eps)) : 0.f;
+          const float mean = lanes_sum<LPR>(dot) * inv_d * rstd;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float xhat = x[j][i] * rstd;
+              aw[t][j][i] = fmaf(g[j][i], xhat, aw[t][j][i]);
+              g[j][i] = rstd * fmaf(-xhat, mean, g[j][i] * w[j][i]);
+            }
+        }
+        H::store((T*)a.y[t] + (r * a.heads[t] + h) * a.dim, a.dim, live, g);
+      }
+    }
+  }
+  if (!a.part) return;
+  // The row slots of a wave by lane exchange, then the waves in order.
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int m = LPR; m < 64; m <<= 1) aw[t][j][i] += __shfl_xor(aw[t][j][i], m, 64);
+  __shared__ float s_sum[kNT / 64][2][H::DP];
+  if (lane_id() < LPR)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) s_sum[threadIdx.x >> 6][t][H::channel(j, i)] = aw[t][j][i];
+  __syncthreads();
+  float* const part = a.part + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.dim;
+  for (int e = threadIdx.x; e < 2 * a.dim; e += kNT) {
+    const int t = e / a.dim, ch = e % a.dim;
+    part[e] = (s_sum[0][t][ch] + s_sum[1][t][ch]) + (s_sum[2][t][ch] + s_sum[3][t][ch]);
+  }
+}
+
+template <int V>
+using IntC = std::integral_constant<int, V>;
+
+// Calls f(V, LPR, NV) for heads of `dim` channels: 16 bytes a load where that divides the head, so that pairs of
+// neighbouring channels stay in a lane; less for other sizes.
+template <typename T, typename F>
+void with_head(int dim, F f) {
+  auto lanes = [&](auto V) {
+    const int l = dim / V;
+    if (l <= 1) return f(V, IntC<1>{}, IntC<1>{});
+    if (l <= 2) return f(V, IntC<2>{}, IntC<1>{});
+    if (l <= 4) return f(V, IntC<4>{}, IntC<1>{});
+    if (l <= 8) return f(V, IntC<8>{}, IntC<1>{});
+    if (l <= 16) return f(V, IntC<16>{}, IntC<1>{});
+    if constexpr (V <= 4) {
+      if (l <= 32) return f(V, IntC<32>{}, IntC<1>{});
+    }
+    if constexpr (V <= 2) {
+      if (l <= 64) return f(V, IntC<64>{}, IntC<1>{});
+    }
+    if constexpr (V == 1) return f(V, IntC<64>{}, IntC<2>{});
+  };
+  if constexpr (sizeof(T) == 2) {
+    if (dim % 8 == 0) return lanes(IntC<8>{});
+  }
+  if (dim % 4 == 0) return lanes(IntC<4>{});
+  if (dim % 2 == 0) return lanes(IntC<2>{});
+  lanes(IntC<1>{});
+}
+
+// Heads of a workgroup: all of them, so that a row's table is made once, unless that leaves the GPU empty.
+int heads_each(int64_t wgs, int heads) {
+  const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(heads, 1024 / std::max<int64_t>(1, wgs)));
+  return (int)((heads + shares - 1) / shares);
+}
+
+template <typename T>
+int rows_each(int dim) {
+  int rows = 1;
+  with_head<T>(dim, [&](auto V, auto L, auto NV) { rows = kNT / L; });
+  return rows;
+}
+
+struct QkGrid {
+  int64_t x;
+  int heads_each, y;
+};
+QkGrid qk_grid(int dtype, int64_t n, int heads, int dim, int64_t most) {
+  const int rows = dtype == IGC_BF16 ? rows_each<bf16_t>(dim) : rows_each<float>(dim);
+  QkGrid g;
+  const int64_t wgs = (n + rows - 1) / rows;
+  g.heads_each = heads_each(wgs, heads);
+  g.y = (heads + g.heads_each - 1) / g.heads_each;
+  g.x = std::max<int64_t>(1, std::min<int64_t>(wgs, most));
+  return g;
+}
+
+constexpr int64_t kBwdWgs = 2048;
+
+template <typename T>
+void qk_t(QkArgs a, bool backward, hipStream_t s) {
+  const QkGrid g = qk_grid(a.dtype, a.n, a.heads[0] + a.heads[1], a.dim, backward ? kBwdWgs : kMaxWgs);
+  a.heads_each = g.heads_each;
+  const dim3 grid((unsigned)g.x, (unsigned)g.y);
+  with_head<T>(a.dim, [&](auto V, auto L, auto NV) {
+    if (backward) k_qk_bwd<T, V, L, NV><<<grid, kNT, 0, s>>>(a);
+    else k_qk<T, V, L, NV><<<grid, kNT, 0, s>>>(a);
+  });
+}
+
+}  // namespace
+
+int qk_parts(int32_t dtype, int64_t n, int32_t heads, int32_t dim) {
+  const QkGrid g = qk_grid(dtype, n, heads, dim, kBwdWgs);
+  return (int)g.x * g.y;
+}
+
+int launch_qk(const QkArgs& a, bool backward, hipStream_t s) {
+  if (a.dtype == IGC_BF16) qk_t<bf16_t>(a, backward, s);
+  else qk_t<float>(a, backward, s);
+  IGC_HIP(hipGetLastError(), a.fn);
+  if (backward && a.part)
+    return launch_pair_sum(a.fn, a.part, qk_parts(a.dtype, a.n, a.heads[0] + a.heads[1], a.dim), a.dim, a.dw[0], a.dw[1], s);
+  return IGC_OK;
+}
+
+}  // namespace igc
