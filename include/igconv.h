@@ -388,6 +388,24 @@ int igc_cross_attention_backward(const igc_attention_t* problem, const void* d_q
                                  const void* d_out, const float* d_lse, const void* d_dout, void* d_dq, void* d_dk,
                                  void* d_dv, void* d_ws, size_t ws_bytes, igc_stream stream);
 
+/* Attention among the rows of one set in order (voxels in the grid's order, tokens): igc_cross_attention where a query sees a
+ * window of keys and a few first ones. Query i (0-based) of a sequence of lq queries and lk keys stands at p = i + lk - lq (its
+ * last queries are its last keys; one query: the newest of a cache), and sees key j if
+ *     j <= p + right and (j >= p - left or j < sinks)
+ * and the mask keeps it. left, right -1: no limit to that side (left 0, right 0: itself). All else is as for
+ * igc_cross_attention: problem, results (no visible key: 0 and -infinity), precision, workspaces. k and v of keys that the mask keeps must be
+ * finite, or rows beyond their windows may become NaN too. */
+int igc_window_attention_workspace(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks,
+                                   int32_t backward, size_t* bytes);
+int igc_window_attention(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks, const void* d_q,
+                         const void* d_k, const void* d_v, void* d_out, float* d_lse, void* d_ws, size_t ws_bytes,
+                         igc_stream stream);
+/* Its gradients, as igc_cross_attention_backward. */
+int igc_window_attention_backward(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks,
+                                  const void* d_q, const void* d_k, const void* d_v, const void* d_out, const float* d_lse,
+                                  const void* d_dout, void* d_dq, void* d_dk, void* d_dv, void* d_ws, size_t ws_bytes,
+                                  igc_stream stream);
+
 /* Queries and keys of one attention over n rows, before they meet: a norm over each head's channels and the rotation
  * of channel pairs by the row's positions. All arrays are device memory.
  *  - q is [n, heads, dim], k [n, kv_heads, dim] of type `dtype`, dim contiguous, with any row and head strides

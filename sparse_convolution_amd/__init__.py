@@ -18,14 +18,14 @@ from ._block import (Checkpoint8, checkpoint_pack, checkpoint_unpack, cross_atte
                      layer_norm, layer_norm_backward, layer_norm_checkpoint, layer_norm_checkpoint_backward)
 from ._lib import IgcError
 from ._selfattn import (dropout, dropout_backward, qk_norm_rotary, qk_norm_rotary_backward, rotary, rotary_backward,
-                        rotary_frequencies)
+                        rotary_frequencies, window_attention, window_attention_backward)
 
 __all__ = [
     "Grid", "grid_build", "kernel_map", "sparse_conv", "sparse_conv_backward", "conv_grid", "conv_grid_chain", "conv_map",
     "sparse_conv_between", "standard_offsets", "release_memory", "tuning_load", "IgcError",
     "Checkpoint8", "checkpoint_pack", "checkpoint_unpack", "layer_norm", "layer_norm_backward", "layer_norm_checkpoint",
     "layer_norm_checkpoint_backward", "cross_attention", "cross_attention_backward",
-    "qk_norm_rotary", "qk_norm_rotary_backward", "rotary", "rotary_backward", "rotary_frequencies", "dropout", "dropout_backward",
+    "window_attention", "window_attention_backward", "qk_norm_rotary", "qk_norm_rotary_backward", "rotary", "rotary_backward", "rotary_frequencies", "dropout", "dropout_backward",
     "PATH_AUTO", "PATH_LEAF", "PATH_GGS", "PATH_GATHER",
 ]
 

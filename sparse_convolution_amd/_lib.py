@@ -15,6 +15,7 @@ EXPORTS = (
     "igc_last_error", "igc_sparse_conv_backward_q8", "igc_layer_norm", "igc_layer_norm_q8", "igc_layer_norm_workspace",
     "igc_layer_norm_backward", "igc_layer_norm_q8_backward", "igc_checkpoint_pack", "igc_checkpoint_unpack",
     "igc_cross_attention", "igc_cross_attention_backward", "igc_cross_attention_workspace",
+    "igc_window_attention", "igc_window_attention_backward", "igc_window_attention_workspace",
     "igc_qk_norm_rotary", "igc_qk_norm_rotary_backward", "igc_qk_norm_rotary_workspace", "igc_dropout",
 )
 
@@ -116,6 +117,9 @@ def load() -> ctypes.CDLL:
         "igc_cross_attention_workspace": [P, i32, ctypes.POINTER(size)],
         "igc_cross_attention": [P, P, P, P, P, P, P, size, P],
         "igc_cross_attention_backward": [P, P, P, P, P, P, P, P, P, P, P, size, P],
+        "igc_window_attention_workspace": [P, i32, i32, i32, i32, ctypes.POINTER(size)],
+        "igc_window_attention": [P, i32, i32, i32, P, P, P, P, P, P, size, P],
+        "igc_window_attention_backward": [P, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, size, P],
         "igc_qk_norm_rotary_workspace": [P, ctypes.POINTER(size)],
         "igc_qk_norm_rotary": [P, P, P, P, P, i32, P, P, P],
         "igc_qk_norm_rotary_backward": [P, P, P, P, P, P, P, i32, P, P, P, P, P, size, P],

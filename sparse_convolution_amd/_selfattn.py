@@ -1,5 +1,5 @@
-"""Operators of self-attention among voxels in grid order: the norm of queries and keys with the rotation by their
-positions, and dropout that stores no mask."""
+"""Operators of self-attention among voxels in grid order: attention in a sliding window, the norm of queries and keys with
+the rotation by their positions, and dropout that stores no mask."""
 from __future__ import annotations
 
 import ctypes
@@ -11,10 +11,71 @@ import torch
 
 from . import _lib
 from ._args import _dtype_code
-from ._block import _call, _heads, _ptr, _same
+from ._block import _ATTENTION, _call, _heads, _ptr, _same
+from ._block import _problem as _attention_problem
 
 LAYOUTS = {"half": 0, "interleaved": 1}
 _QK = struct.Struct("@iiiiiiiiffqqqqqPP")  # igc_qk_t
+
+
+def _window(left, right, sinks) -> tuple[int, int, int]:
+    """The window's sides (None: no limit) and sinks as the library takes them."""
+    for value, name in ((left, "left"), (right, "right"), (sinks, "sinks")):
+        if value is not None and not 0 <= value < 1 << 31:
+            raise ValueError(f"{name} must be 0 to 2^31 - 1{'' if name == 'sinks' else ', or None'}")
+    return -1 if left is None else left, -1 if right is None else right, sinks
+
+
+@functools.lru_cache(maxsize=256)
+def _window_workspace(backward: int, window: tuple, code: int, batch: int, heads: int, kv_heads: int, dim: int, nq: int,
+                      nk: int) -> int:
+    # The offsets' addresses only have to be there: the size depends on the counts alone.
+    p = _ATTENTION.pack(code, batch, heads, kv_heads, dim, 1.0, nq, nk, 0, 0, 0, 0, 0, 0, 16, 16, 0)
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().igc_window_attention_workspace(p, *window, backward, ctypes.byref(n)))
+    return n.value
+
+
+def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int | None = None, right: int | None = None,
+                     sinks: int = 0, q_offsets: torch.Tensor | None = None, kv_offsets: torch.Tensor | None = None,
+                     key_mask: torch.Tensor | None = None, scale: float | None = None):
+    """cross_attention among rows in order, where a query sees a window of keys and a few first ones: query i of a
+    sequence of lq queries and lk keys stands at p = i + lk - lq and sees key j if j <= p + right and (j >= p - left or j < sinks) and
+    key_mask keeps it. None: no limit to that side; right 0 is causal. With as many queries as keys this is attention within
+    a sequence, with fewer that of its last rows to a cache (single tokens). k and v must be finite where key_mask keeps them. Returns (out, lse) as
+    cross_attention (igc_window_attention)."""
+    window = _window(left, right, sinks)
+    p, sizes = _attention_problem(q, k, v, q_offsets, kv_offsets, key_mask, scale)
+    dev = q.device
+    out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    n = _window_workspace(0, window, *sizes)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _call("igc_window_attention", dev.index, p, *window, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          _ptr(ws), n)
+    return out, lse
+
+
+def window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                              lse: torch.Tensor, left: int | None = None, right: int | None = None, sinks: int = 0,
+                              q_offsets: torch.Tensor | None = None, kv_offsets: torch.Tensor | None = None,
+                              key_mask: torch.Tensor | None = None, scale: float | None = None, need_dq: bool = True,
+                              need_dkv: bool = True):
+    """Gradients (dq, dk, dv) of window_attention for the output gradient dout, from its inputs and results; None for those
+    not needed (igc_window_attention_backward)."""
+    window = _window(left, right, sinks)
+    p, sizes = _attention_problem(q, k, v, q_offsets, kv_offsets, key_mask, scale)
+    dt, dev = q.dtype, q.device
+    _same(dout, "dout", dt, q.shape, dev.index), _same(out, "out", dt, q.shape, dev.index)
+    _same(lse, "lse", torch.float32, q.shape[:2], dev.index)
+    dq = torch.empty(q.shape, dtype=dt, device=dev) if need_dq else None
+    dk = torch.empty(k.shape, dtype=dt, device=dev) if need_dkv else None
+    dv = torch.empty(k.shape, dtype=dt, device=dev) if need_dkv else None
+    n = _window_workspace(1, window, *sizes)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _call("igc_window_attention_backward", dev.index, p, *window, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), dout.data_ptr(), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n)
+    return dq, dk, dv
 
 
 def rotary_frequencies(dim: int, base: float = 10000.0, axes: int = 1, scaling: str | None = None, factor: float = 1.0,

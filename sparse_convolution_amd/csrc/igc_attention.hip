@@ -33,7 +33,9 @@ constexpr float kSlack = 8.f;
 // Four waves of 32 NQ query rows each over tiles of BN keys. A row is a (query, head of the group
 // that shares the key head) pair, so few queries with shared key heads still fill a tile.
 // splits > 1: each workgroup takes one part of the sequence's keys and leaves an unnormalised result.
-template <typename T, int DP, int NQ, int BN, int WPE, bool VEC>
+// WIN: a query sees the keys of a window and a few first ones (see igc_ragged.h). The tile's workgroup walks the keys that any of its
+// queries sees, a wave passes over tiles that none of its own sees, and only tiles on an edge are masked.
+template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, bool WIN>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_fwd(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int LD = lds_ld<DP>(), PS = BN * LD;
@@ -55,26 +57,48 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   seq_rows(a.ko, b, a.nk, k0, k1);
   const int64_t rows = (q1 - q0) * a.group;
   if (tile * BM >= rows) return;
-  if (a.splits > 1) {
+  // WIN: the tile's keys as one axis, of which this workgroup takes places x0 .. x0 + keys.
+  WindowAxis axis = {};
+  const int64_t lq = q1 - q0, lk = k1 - k0;
+  int64_t x0 = 0, x1 = 0;
+  if constexpr (WIN) {
+    axis = window_axis(a.win, tile * BM / a.group, ((tile + 1) * BM < rows ? (tile + 1) * BM - 1 : rows - 1) / a.group, lq, lk);
+    split_axis(axis.keys, a.splits, split, BN, x0, x1);
+  } else if (a.splits > 1) {
     const int64_t part = ((k1 - k0 + a.splits - 1) / a.splits + BN - 1) / BN * BN;
     k0 = k0 + split * part < k1 ? k0 + split * part : k1;
     k1 = k0 + part < k1 ? k0 + part : k1;
   }
-  int keys = (int)(k1 - k0);
+  int keys = WIN ? (int)(x1 - x0) : (int)(k1 - k0);
 
   Stage<T, BN, DP, kNT, VEC> sk, sv;
   sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], 0, a.ks[0], 0, 1, a.dim);
   sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], 0, a.vs[0], 0, 1, a.dim);
   // Whether key j + lane exists and the mask keeps it. The ballot of these comes a tile later: at once it would wait for
   // the tile's loads too.
-  auto key_ok = [&](int j) -> int { return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + j + lane] : 1) : 0; };
-  sk.load(keys);
-  sv.load(keys);
-  int next_ok = key_ok(0);
+  auto key_ok = [&](int j) -> int {
+    if constexpr (WIN) return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + axis.key(x0 + j + lane)] : 1) : 0;
+    return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + j + lane] : 1) : 0;
+  };
+  auto fetch = [&](int j) {
+    if constexpr (WIN) {
+      const int64_t x = x0 + j, cut = axis.sinks - x;
+      const int64_t r = cut > 0 ? x : x + axis.jump;
+      const int until = cut > 0 && cut < BN ? (int)cut : BN;
+      sk.load_at((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], r, keys - j, until, axis.jump * sk.row_stride);
+      sv.load_at((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], r, keys - j, until, axis.jump * sv.row_stride);
+    } else {
+      sk.load(keys - j);
+      sv.load(keys - j);
+    }
+    return key_ok(j);
+  };
+  int next_ok = fetch(0);
 
   // This lane's query rows (one per 32-column tile), and their values as second operands.
   int64_t row[NQ];  // row of out and lse, -1: none
   frag fq[NQ][DP / 16];
+  WindowRow see[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
@@ -90,7 +114,15 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       const int d = kk * 16 + h * 8;
       fq[n][kk] = to_parts(load8<T>(p + d, r < rows ? a.dim - d : 0, VEC));
     }
+    if constexpr (WIN) {  // rows behind the last one see what it sees
+      int64_t i;
+      split_row(r < rows ? r : rows - 1, a.group, i, head);
+      see[n] = window_row(a.win, axis, i, lq, lk);
+      see[n].first -= (int)x0, see[n].low -= (int)x0, see[n].high -= (int)x0;
+    }
   }
+  WindowWave wave_sees;
+  if constexpr (WIN) wave_sees.start(see[0], see[NQ - 1]);
 
   // Finite, so that the first reference (-infinity) is passed whatever the scale.
   const float c = a.scale * kLog2e, slack = fminf(kSlack / c, 3.4e38f);
@@ -114,13 +146,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       sk.template store<LD, PS>(s_k(buf));
       sv.template store<LD, PS>(s_v(buf));
     }
-    if (j + BN < keys) {
-      sk.load(keys - j - BN);
-      sv.load(keys - j - BN);
-      next_ok = key_ok(j + BN);
-    }
+    if (j + BN < keys) next_ok = fetch(j + BN);
     // Two buffers: the barrier of the last tile already had every wave past reading this one.
     __syncthreads();
+    if (WIN && wave_sees.none(j, BN)) continue;
     f32x16 s[NQ][KT];
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
@@ -133,7 +162,18 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         for (int n = 0; n < NQ; ++n) s[n][t] = mma(fk, fq[n][kk], s[n][t]);
       }
     }
-    if (bits != kAll) {
+    if (WIN && !(bits == kAll && wave_sees.all(j, BN))) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const uint64_t mine = bits & window_bits(see[n], j);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          const uint32_t w = (uint32_t)(mine >> (32 * t)) >> (4 * h);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[n][t][r] = w & (1u << (8 * (r >> 2) + (r & 3))) ? s[n][t][r] : -INFINITY;
+        }
+      }
+    } else if (!WIN && bits != kAll) {
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
         const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
@@ -216,7 +256,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 // channels each, with a share of U keys in flight and as many being worked on; every group of LPK lanes keeps
 // its own running maximum, sum and output over its keys, and they are joined at the end (lanes, waves, then
 // k_attn_join for the parts of the key axis).
-template <typename T, int LPK, int R, bool VEC>
+template <typename T, int LPK, int R, bool VEC, bool WIN>
 __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
   typedef typename Raw8<T>::type frag;
   constexpr int U = 4, KPW = 64 / LPK, STEP = 4 * KPW * U;  // keys of a wave's round: KPW * U
@@ -233,12 +273,18 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
   seq_rows(a.ko, b, a.nk, k0, k1);
   const int64_t rows = (q1 - q0) * a.group;
   if (tile * R >= rows) return;
-  if (a.splits > 1) {
+  WindowAxis axis = {};  // as in k_attn_fwd
+  const int64_t lq = q1 - q0, lk = k1 - k0;
+  int64_t x0 = 0, x1 = 0;
+  if constexpr (WIN) {
+    axis = window_axis(a.win, tile * R / a.group, ((tile + 1) * R < rows ? (tile + 1) * R - 1 : rows - 1) / a.group, lq, lk);
+    split_axis(axis.keys, a.splits, split, 1, x0, x1);
+  } else if (a.splits > 1) {
     const int64_t part = (k1 - k0 + a.splits - 1) / a.splits;
     k0 = k0 + split * part < k1 ? k0 + split * part : k1;
     k1 = k0 + part < k1 ? k0 + part : k1;
   }
-  const int keys = (int)(k1 - k0);
+  const int keys = WIN ? (int)(x1 - x0) : (int)(k1 - k0);
   const T* kp = (const T*)a.k + kh * a.ks[1] + k0 * a.ks[0] + d;
   const T* vp = (const T*)a.v + kh * a.vs[1] + k0 * a.vs[0] + d;
   frag fk[U], fv[U];
@@ -248,21 +294,25 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int x = j + u * KPW + g;
-      const bool in = x < keys && (!a.mask || a.mask[k0 + x]);
-      fk[u] = load8<T>(kp + (int64_t)x * a.ks[0], in ? a.dim - d : 0, VEC);
-      fv[u] = load8<T>(vp + (int64_t)x * a.vs[0], in ? a.dim - d : 0, VEC);
+      int64_t key = x;
+      if constexpr (WIN) key = axis.key(x0 + x);
+      const bool in = x < keys && (!a.mask || a.mask[k0 + key]);
+      fk[u] = load8<T>(kp + key * a.ks[0], in ? a.dim - d : 0, VEC);
+      fv[u] = load8<T>(vp + key * a.vs[0], in ? a.dim - d : 0, VEC);
       ok |= (in ? 1u : 0u) << u;
     }
   };
   fetch(wave * KPW * U);
 
   float q[R][8], o[R][8], m[R], l[R];
+  WindowRow see[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t x = tile * R + r;
     int64_t qi;
     int head;
     split_row(x < rows ? x : 0, a.group, qi, head);
+    if constexpr (WIN) see[r] = window_row(a.win, axis, qi, lq, lk);
     const frag f = load8<T>((const T*)a.q + (q0 + qi) * a.qs[0] + (kh * a.group + head) * a.qs[1] + d,
                             x < rows ? a.dim - d : 0, VEC);
 #pragma unroll
@@ -290,7 +340,12 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[u] = fmaf(q[r][i], k[u][i], s[u]);
         s[u] = lanes_sum<LPK>(s[u]);
-        s[u] = now >> u & 1 ? s[u] : -INFINITY;
+        bool keep = now >> u & 1;
+        if constexpr (WIN) {
+          const int x = (int)x0 + j + u * KPW + g;
+          keep = keep && (x < see[r].first || (x >= see[r].low && x < see[r].high));
+        }
+        s[u] = keep ? s[u] : -INFINITY;
         top = fmaxf(top, s[u]);
       }
       const float base = top == -INFINITY ? 0.f : top;
@@ -455,14 +510,26 @@ void join(const AttnArgs& a, hipStream_t s) {
 template <typename T, int DP>
 void fwd_go(const AttnArgs& a, unsigned wgs, hipStream_t s) {
   constexpr int NQ = FwdShape<T, DP>::NQ, BN = FwdShape<T, DP>::BN, WPE = FwdShape<T, DP>::WPE;
-  if (a.qvec && a.kvec) k_attn_fwd<T, DP, NQ, BN, WPE, true><<<wgs, kNT, 0, s>>>(a);
-  else k_attn_fwd<T, DP, NQ, BN, WPE, false><<<wgs, kNT, 0, s>>>(a);
+  const bool vec = a.qvec && a.kvec;
+  if (a.windowed) {
+    if (vec) k_attn_fwd<T, DP, NQ, BN, WPE, true, true><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_fwd<T, DP, NQ, BN, WPE, false, true><<<wgs, kNT, 0, s>>>(a);
+  } else {
+    if (vec) k_attn_fwd<T, DP, NQ, BN, WPE, true, false><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_fwd<T, DP, NQ, BN, WPE, false, false><<<wgs, kNT, 0, s>>>(a);
+  }
 }
 
 template <typename T, int LPK, int R>
 void few_go(const AttnArgs& a, unsigned wgs, hipStream_t s) {
-  if (a.qvec && a.kvec) k_attn_few<T, LPK, R, true><<<wgs, kNT, 0, s>>>(a);
-  else k_attn_few<T, LPK, R, false><<<wgs, kNT, 0, s>>>(a);
+  const bool vec = a.qvec && a.kvec;
+  if (a.windowed) {
+    if (vec) k_attn_few<T, LPK, R, true, true><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_few<T, LPK, R, false, true><<<wgs, kNT, 0, s>>>(a);
+  } else {
+    if (vec) k_attn_few<T, LPK, R, true, false><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_few<T, LPK, R, false, false><<<wgs, kNT, 0, s>>>(a);
+  }
 }
 template <typename T, int LPK>
 void few_r(const AttnArgs& a, int rows, unsigned wgs, hipStream_t s) {
@@ -490,7 +557,9 @@ void fwd_t(const AttnArgs& a, int dtype, hipStream_t s) {
 
 }  // namespace
 
-int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim) {
+int attn_fwd_splits(int dtype, const AttnArgs& a) {
+  const int64_t nq = a.nq, nk = a.nk;
+  const int batch = a.batch, heads = a.heads, kv_heads = a.kv_heads, dim = a.dim;
   // Parts of the key axis: none while the query tiles alone fill the GPU, else enough for that, each of
   // at least 256 keys.
   const int bm = fwd_rows(dtype, dim, nq, batch, heads / kv_heads);
@@ -503,7 +572,10 @@ int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int
   // heads of 16, the first three of these sizes: 117 / 104 / 106, 68 / 62 / 63 and 46 / 45 / 45.
   const int64_t fill = bm <= kFewRows ? 2048 : dtype == IGC_F32 && dim <= 32 ? 768 : 512;
   const int64_t want = wgs >= fill ? 1 : fill / std::max<int64_t>(1, wgs);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxParts), nk / batch / 256));
+  int64_t keys = nk / batch;  // that a tile walks
+  if (a.windowed && a.win.left >= 0 && a.win.right >= 0)
+    keys = std::min<int64_t>(keys, a.win.left + a.win.right + bm / a.group + a.win.sinks);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxParts), keys / 256));
 }
 
 int launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s) {

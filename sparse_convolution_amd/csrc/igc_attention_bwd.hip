@@ -29,8 +29,8 @@ constexpr int kNT = 256;
 // lse in base 2; +infinity for rows without keys, whose probabilities are then exp2(-infinity) = 0.
 __device__ __forceinline__ float lse_base2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-// dq and delta: four waves of 32 NQ query rows over tiles of BN keys (see k_attn_fwd for rows).
-template <typename T, int DP, int NQ, int BN, int WPE, bool VEC>
+// dq and delta: four waves of 32 NQ query rows over tiles of BN keys (see k_attn_fwd for rows and windows).
+template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, bool WIN>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dq(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int LD = lds_ld<DP>(), PS = BN * LD;
@@ -52,25 +52,46 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   seq_rows(a.ko, b, a.nk, k0, k1);
   const int64_t rows = (q1 - q0) * a.group;
   if (tile * BM >= rows) return;
+  WindowAxis axis = {};  // as in k_attn_fwd
+  const int64_t lq = q1 - q0, lk = k1 - k0;
+  int64_t x0 = 0, x1 = 0;
   if (!a.dq) k1 = k0;  // only delta is wanted
-  if (a.splits > 1) {
+  if constexpr (WIN) {
+    axis = window_axis(a.win, tile * BM / a.group, ((tile + 1) * BM < rows ? (tile + 1) * BM - 1 : rows - 1) / a.group, lq, lk);
+    split_axis(a.dq ? axis.keys : 0, a.splits, split, BN, x0, x1);
+  } else if (a.splits > 1) {
     const int64_t part = ((k1 - k0 + a.splits - 1) / a.splits + BN - 1) / BN * BN;
     k0 = k0 + split * part < k1 ? k0 + split * part : k1;
     k1 = k0 + part < k1 ? k0 + part : k1;
   }
-  const int keys = (int)(k1 - k0);
+  const int keys = WIN ? (int)(x1 - x0) : (int)(k1 - k0);
   Stage<T, BN, DP, kNT, VEC> sk, sv;
   sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], 0, a.ks[0], 0, 1, a.dim);
   sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], 0, a.vs[0], 0, 1, a.dim);
   // As in k_attn_fwd: the ballot comes a tile later, so that it waits for no loads (100,003 queries, masked: 231 and 213 us).
-  auto key_ok = [&](int j) -> int { return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + j + lane] : 1) : 0; };
-  sk.load(keys);
-  sv.load(keys);
-  int next_ok = key_ok(0);
+  auto key_ok = [&](int j) -> int {
+    if constexpr (WIN) return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + axis.key(x0 + j + lane)] : 1) : 0;
+    return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + j + lane] : 1) : 0;
+  };
+  auto fetch = [&](int j) {
+    if constexpr (WIN) {
+      const int64_t x = x0 + j, cut = axis.sinks - x;
+      const int64_t r = cut > 0 ? x : x + axis.jump;
+      const int until = cut > 0 && cut < BN ? (int)cut : BN;
+      sk.load_at((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], r, keys - j, until, axis.jump * sk.row_stride);
+      sv.load_at((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], r, keys - j, until, axis.jump * sv.row_stride);
+    } else {
+      sk.load(keys - j);
+      sv.load(keys - j);
+    }
+    return key_ok(j);
+  };
+  int next_ok = fetch(0);
 
   int64_t row[NQ];  // row of out and lse, -1: none
   frag fq[NQ][DP / 16], fo[NQ][DP / 16];
   float delta[NQ], lse[NQ];
+  WindowRow see[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
@@ -96,7 +117,15 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     delta[n] += __shfl_xor(delta[n], 32, 64);
     if (row[n] >= 0 && h == 0 && split == 0) a.delta[row[n]] = delta[n];
     lse[n] = lse_base2(row[n] >= 0 ? a.lse_in[row[n]] : -INFINITY);
+    if constexpr (WIN) {
+      int64_t i;
+      split_row(r < rows ? r : rows - 1, a.group, i, head);
+      see[n] = window_row(a.win, axis, i, lq, lk);
+      see[n].first -= (int)x0, see[n].low -= (int)x0, see[n].high -= (int)x0;
+    }
   }
+  WindowWave wave_sees;
+  if constexpr (WIN) wave_sees.start(see[0], see[NQ - 1]);
   const float c = a.scale * kLog2e;
   f32x16 dq[NQ][DT];
 #pragma unroll
@@ -114,14 +143,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       sk.template store<LD, PS>(s_k(buf));
       sv.template store<LD, PS>(s_v(buf));
     }
-    if (j + BN < keys) {
-      sk.load(keys - j - BN);
-      sv.load(keys - j - BN);
-      next_ok = key_ok(j + BN);
-    }
+    if (j + BN < keys) next_ok = fetch(j + BN);
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
+      if (WIN && wave_sees.none(j + 32 * t, 32)) continue;
       f32x16 s[NQ], dp[NQ];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) s[n] = zero16(), dp[n] = zero16();
@@ -140,7 +166,14 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], c, -lse[n])) * (dp[n][i] - delta[n]);
-      if (bits != kAll) {
+      if (WIN && !(bits == kAll && wave_sees.all(j + 32 * t, 32))) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const uint32_t w = (uint32_t)((bits & window_bits(see[n], j)) >> (32 * t)) >> (4 * h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[n][i] = w & (1u << (8 * (i >> 2) + (i & 3))) ? s[n][i] : 0.f;
+        }
+      } else if (!WIN && bits != kAll) {
         const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -189,7 +222,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 // neighbours are. A score costs its exponential, two multiplications, three roundings and a remainder: the products with dout
 // start from -delta (read into their accumulators from LDS), and what the mask leaves out is cleared in the results
 // instead of per score (100,003 queries, three sequences of ~800 keys, 4 heads of 64, ds rounded once: 252 and 223 us).
-template <typename T, int DP, int NK, int BQ, int WPE, bool VEC>
+//
+// WIN: the workgroup of a key tile walks the rows whose windows hold any of its keys. Sinks among its keys are seen by all later
+// rows too: those are walked by far_parts workgroups of their own for each tile with sinks (the launch's first), so that none walks
+// a whole sequence alone, and k_attn_sinks adds up.
+template <typename T, int DP, int NK, int BQ, int WPE, bool VEC, bool WIN>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int LD = lds_ld<DP>(), PS = BQ * LD;
@@ -202,18 +239,40 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];  // s_delta: -delta
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
-  const int kh = blockIdx.x % a.kv_heads;
-  const int split = (blockIdx.x / a.kv_heads) % a.splits;
+  const bool far = WIN && blockIdx.x < a.far_wgs;
+  const unsigned wg = WIN && !far ? blockIdx.x - a.far_wgs : blockIdx.x;
+  const int kh = wg % a.kv_heads;
+  const int parts = far ? a.far_parts : a.splits;
+  const int split = (wg / a.kv_heads) % parts;
   int b;
-  const int64_t tile = find_tile(a.ko, a.batch, a.nk, 1, BM, blockIdx.x / (a.kv_heads * a.splits), b);
+  int64_t tile = wg / (a.kv_heads * parts);
+  if (far && !a.far_by_key) {
+    const int tiles = (a.win.sinks + BM - 1) / BM;
+    b = (int)(tile / tiles);
+    tile %= tiles;
+  } else {
+    tile = find_tile(a.ko, a.batch, a.nk, 1, BM, tile, b);
+  }
   int64_t q0, q1, k0, k1;
   seq_rows(a.qo, b, a.nq, q0, q1);
   seq_rows(a.ko, b, a.nk, k0, k1);
   if (k0 + tile * BM >= k1) return;
   int64_t r0 = 0, r1 = (q1 - q0) * a.group;
-  if (a.splits > 1) {
-    const int64_t part = ((r1 + a.splits - 1) / a.splits + BQ - 1) / BQ * BQ;
-    r0 = split * part < r1 ? split * part : r1;
+  const int64_t lq = q1 - q0, lk = k1 - k0;
+  bool sinks = false;  // some of the tile's keys are
+  if constexpr (WIN) {
+    sinks = tile * BM < a.win.sinks;
+    if (far && !sinks) return;
+    int64_t from, to, none;
+    window_queries(a.win, tile * BM, lq, lk, true, from, none);
+    window_queries(a.win, (tile + 1) * BM < lk ? (tile + 1) * BM - 1 : lk - 1, lq, lk, true, none, to);
+    r0 = (far ? to : from) * a.group;
+    r1 = far ? r1 : to * a.group;
+    if (r1 < r0) r1 = r0;
+  }
+  if (parts > 1) {
+    const int64_t part = ((r1 - r0 + parts - 1) / parts + BQ - 1) / BQ * BQ;
+    r0 = r0 + split * part < r1 ? r0 + split * part : r1;
     r1 = r0 + part < r1 ? r0 + part : r1;
   }
   // Query rows step through the heads of the group before the next query.
@@ -245,6 +304,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   int64_t key[NK];
   bool keep[NK];
   frag fk[NK][DP / 16], fv[NK][DP / 16];
+  int from[NK], to[NK];               // rows that see this lane's key, from this part's first on
+  int any_from = 0, any_to = 0, all_from = 0, all_to = 0;  // rows that see any, and all, of the wave's keys
 #pragma unroll
   for (int n = 0; n < NK; ++n) {
     const int64_t j = k0 + tile * BM + (wave * NK + n) * 32 + (lane & 31);
@@ -257,6 +318,28 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       fk[n][kk] = to_parts(load8<T>((const T*)a.k + at * a.ks[0] + kh * a.ks[1] + d, have, VEC));
       fv[n][kk] = to_parts(load8<T>((const T*)a.v + at * a.vs[0] + kh * a.vs[1] + d, have, VEC));
     }
+    if constexpr (WIN) {
+      int64_t x, y;
+      window_queries(a.win, j - k0, lq, lk, false, x, y);
+      if (j >= k1 || (far && j - k0 >= a.win.sinks)) x = y = 0;  // nothing to do for it here
+      from[n] = (int)(clamp64(x * a.group, r0, r1) - r0);
+      to[n] = (int)(clamp64(y * a.group, r0, r1) - r0);
+    }
+  }
+  if constexpr (WIN) {
+    any_from = all_to = n_rows;
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+      any_from = min(any_from, from[n] < to[n] ? from[n] : n_rows), any_to = max(any_to, from[n] < to[n] ? to[n] : 0);
+      all_from = max(all_from, from[n]), all_to = min(all_to, to[n]);
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      any_from = min(any_from, __shfl_xor(any_from, m, 64)), any_to = max(any_to, __shfl_xor(any_to, m, 64));
+      all_from = max(all_from, __shfl_xor(all_from, m, 64)), all_to = min(all_to, __shfl_xor(all_to, m, 64));
+    }
+    any_from = __builtin_amdgcn_readfirstlane(any_from), any_to = __builtin_amdgcn_readfirstlane(any_to);
+    all_from = __builtin_amdgcn_readfirstlane(all_from), all_to = __builtin_amdgcn_readfirstlane(all_to);
   }
   const float c = a.scale * kLog2e;
   f32x16 dk[NK][DT], dv[NK][DT];
@@ -274,6 +357,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
+      const int r32 = t0 + 32 * t;
+      if (WIN && (any_to <= r32 || any_from >= r32 + 32)) continue;
       f32x16 s[NK], dp[NK];
 #pragma unroll
       for (int n = 0; n < NK; ++n) {
@@ -293,6 +378,15 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         for (int n = 0; n < NK; ++n) {
           s[n] = mma(fq, fk[n][kk], s[n]);
           dp[n] = mma(fo, fv[n][kk], dp[n]);
+        }
+      }
+      if (WIN && !(all_from <= r32 && all_to >= r32 + 32)) {
+        // Scores of rows that do not see the key would not be below their lse: minus infinity, so that p is 0.
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
+          const uint32_t w = (uint32_t)(low_bits(to[n] - r32) & ~low_bits(from[n] - r32)) >> (4 * h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[n][i] = w & (1u << (8 * (i >> 2) + (i & 3))) ? s[n][i] : -INFINITY;
         }
       }
 #pragma unroll
@@ -338,10 +432,23 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   void* const s_out = s_mem + wave * (32 * (DP + 4) * 4);
 #pragma unroll
   for (int n = 0; n < NK; ++n) {
-    const int64_t row = key[n] < 0 ? -1 : key[n] * a.kv_heads + kh;
+    int64_t row = key[n] < 0 ? -1 : key[n] * a.kv_heads + kh;
     if (!keep[n]) {
 #pragma unroll
       for (int t = 0; t < DT; ++t) dk[n][t] = zero16(), dv[n][t] = zero16();
+    }
+    if (WIN && sinks) {
+      // A sink's share: to far, but for the parts of an axis that is split, which lie with the other keys'.
+      const int64_t j = key[n] - k0, at = a.far_by_key ? key[n] : (int64_t)b * a.win.sinks + j;
+      const int64_t to_far = key[n] >= 0 && j < a.win.sinks ? at * a.kv_heads + kh : -1;
+      if (far || a.splits == 1) {
+        float* const out = a.far + (far ? 1 + split : 0) * a.far_rows * a.kv_heads * a.dim;
+        store_tile<float, DP>(out, s_out, dk[n], a.scale, to_far, a.dim, a.dim % 4 == 0);
+        store_tile<float, DP>(out + (1 + a.far_parts) * a.far_rows * a.kv_heads * a.dim, s_out, dv[n], 1.f, to_far, a.dim,
+                              a.dim % 4 == 0);
+        if (to_far >= 0) row = -1;
+      }
+      if (far) continue;
     }
     if (a.splits > 1) {
       const int64_t first = (int64_t)split * a.nk * a.kv_heads * a.dim;
@@ -395,6 +502,43 @@ __global__ __launch_bounds__(kNT) void k_attn_sum(const float* __restrict__ part
   }
 }
 
+// Gradients of the sinks: the window's share (of a split axis: of its parts) and the far parts', in order. A thread for
+// each row, key head and channel in turn, dk and dv as blockIdx.y.
+template <typename T>
+__device__ __forceinline__ void sum_sink(const AttnArgs& a, int64_t e) {
+  const int64_t width = (int64_t)a.kv_heads * a.dim, r = e / width, c = e % width;
+  int b = 0;
+  if (a.far_by_key) {
+    for (int hi = a.batch; a.ko && hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (a.ko[mid] <= r) b = mid;
+      else hi = mid;
+    }
+  } else {
+    b = (int)(r / a.win.sinks);
+  }
+  int64_t k0, k1;
+  seq_rows(a.ko, b, a.nk, k0, k1);
+  const int64_t j = a.far_by_key ? r - k0 : r % a.win.sinks;
+  if (j < 0 || j >= a.win.sinks || k0 + j >= k1) return;
+  const float* far = a.far + (blockIdx.y ? (1 + a.far_parts) * a.far_rows * width : 0) + e;
+  float sum = 0.f;
+  if (a.splits > 1) {
+    const float* part = (blockIdx.y ? a.part_b : a.part_a) + (k0 + j) * width + c;
+    for (int s = 0; s < a.splits; ++s) sum += part[(int64_t)s * a.nk * width];
+  } else {
+    sum = *far;
+  }
+#pragma unroll 8
+  for (int p = 1; p <= a.far_parts; ++p) sum += far[p * a.far_rows * width];
+  ((T*)(blockIdx.y ? a.dv : a.dk))[(k0 + j) * width + c] = (T)sum;
+}
+template <typename T>
+__global__ __launch_bounds__(kNT) void k_attn_sinks(AttnArgs a) {
+  const int64_t n = a.far_rows * a.kv_heads * a.dim;
+  for (int64_t e = (int64_t)blockIdx.x * kNT + threadIdx.x; e < n; e += (int64_t)gridDim.x * kNT) sum_sink<T>(a, e);
+}
+
 template <typename T>
 void sum_go(const float* part0, const float* part1, int splits, const int32_t* off, int batch, int64_t rows, int heads,
             int dim, bool vec, void* out0, void* out1, hipStream_t s) {
@@ -435,6 +579,11 @@ BwdRows bwd_rows_t(int dim) {
 }
 BwdRows bwd_rows(int dtype, int dim) { return dtype == IGC_BF16 ? bwd_rows_t<bf16_t>(dim) : bwd_rows_t<float>(dim); }
 
+// Key tiles of `bm` that may hold sinks.
+int64_t far_tiles(const AttnArgs& a, bool by_key, int bm) {
+  return a.win.sinks == 0 ? 0 : by_key ? a.nk / bm + a.batch : (int64_t)a.batch * ((a.win.sinks + bm - 1) / bm);
+}
+
 template <typename T, int DP>
 void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
   typedef BwdShape<T, DP> S;
@@ -446,8 +595,13 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     d.splits = a.dq ? p.dq_splits : 1;
     d.part_a = ws;
     const unsigned wgs = (unsigned)((a.nq * a.group / (128 * S::NQ) + a.batch) * a.kv_heads * d.splits);
-    if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true><<<wgs, kNT, 0, s>>>(d);
-    else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false><<<wgs, kNT, 0, s>>>(d);
+    if (a.windowed) {
+      if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true, true><<<wgs, kNT, 0, s>>>(d);
+      else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false, true><<<wgs, kNT, 0, s>>>(d);
+    } else {
+      if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true, false><<<wgs, kNT, 0, s>>>(d);
+      else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false, false><<<wgs, kNT, 0, s>>>(d);
+    }
     if (a.dq && d.splits > 1)
       sum_go<T>(ws, nullptr, d.splits, a.qo, a.batch, a.nq, a.heads, a.dim, a.ovec, a.dq, nullptr, s);
   }
@@ -457,10 +611,22 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     a.part_a = ws;
     a.part_b = ws + (p.dkv_splits > 1 ? p.dkv_splits * n : 0);
     const unsigned wgs = (unsigned)((a.nk / (128 * S::NK) + a.batch) * a.kv_heads * a.splits);
-    if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true><<<wgs, kNT, 0, s>>>(a);
-    else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false><<<wgs, kNT, 0, s>>>(a);
+    if (a.windowed) {
+      a.far_parts = p.far_parts, a.far_by_key = p.far_by_key, a.far_rows = p.far_rows;
+      a.far = a.delta + p.far_at;
+      a.far_wgs = (unsigned)(far_tiles(a, p.far_by_key, 128 * S::NK) * a.kv_heads * a.far_parts);
+      if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, true><<<wgs + a.far_wgs, kNT, 0, s>>>(a);
+      else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false, true><<<wgs + a.far_wgs, kNT, 0, s>>>(a);
+    } else {
+      if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, false><<<wgs, kNT, 0, s>>>(a);
+      else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false, false><<<wgs, kNT, 0, s>>>(a);
+    }
     if (a.splits > 1)
       sum_go<T>(a.part_a, a.part_b, a.splits, a.ko, a.batch, a.nk, a.kv_heads, a.dim, a.ovec, a.dk, a.dv, s);
+    if (a.far_rows > 0) {
+      const int64_t n = a.far_rows * a.kv_heads * a.dim;
+      k_attn_sinks<T><<<dim3((unsigned)std::min<int64_t>((n + kNT - 1) / kNT, kMaxWgs), 2), kNT, 0, s>>>(a);
+    }
   }
 }
 
@@ -481,16 +647,32 @@ int parts(int64_t wgs, int64_t axis, int64_t least) {
 
 }  // namespace
 
-AttnBwdPlan attn_bwd_plan(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim) {
+AttnBwdPlan attn_bwd_plan(int dtype, const AttnArgs& a) {
+  const int64_t nq = a.nq, nk = a.nk;
+  const int batch = a.batch, heads = a.heads, kv_heads = a.kv_heads, dim = a.dim;
   AttnBwdPlan p;
   const BwdRows t = bwd_rows(dtype, dim);
   const int64_t rows = (nq + batch - 1) / batch * (heads / kv_heads), keys = (nk + batch - 1) / batch;
-  p.dq_splits = parts(batch * ((rows + t.q - 1) / t.q) * kv_heads, keys, 256);
-  p.dkv_splits = parts(batch * ((keys + t.k - 1) / t.k) * kv_heads, rows, 64);
+  int64_t seen_keys = keys, seen_rows = rows;  // that a tile walks
+  if (a.windowed && a.win.left >= 0 && a.win.right >= 0) {
+    seen_keys = std::min<int64_t>(keys, a.win.left + a.win.right + t.q / a.group + a.win.sinks);
+    seen_rows = std::min<int64_t>(rows, (a.win.left + a.win.right + t.k) * a.group);
+  }
+  p.dq_splits = parts(batch * ((rows + t.q - 1) / t.q) * kv_heads, seen_keys, 256);
+  p.dkv_splits = parts(batch * ((keys + t.k - 1) / t.k) * kv_heads, seen_rows, 64);
   const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * nq * heads * dim : 0;
   const size_t dkv = p.dkv_splits > 1 ? (size_t)2 * p.dkv_splits * nk * kv_heads * dim : 0;
   // The two kernels run one after the other, so their partial results share the space.
   p.floats = (size_t)(nq * heads + 63) / 64 * 64 + std::max(dq, dkv);
+  if (a.windowed && a.win.sinks > 0 && nk > 0) {
+    // Rows behind the window of a tile with sinks: parts about as long as the rows that other tiles walk, while they are few.
+    p.far_by_key = (int64_t)batch * a.win.sinks >= nk;
+    p.far_rows = p.far_by_key ? nk : (int64_t)batch * a.win.sinks;
+    const int64_t tiles = far_tiles(a, p.far_by_key, t.k) * kv_heads;
+    p.far_parts = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, 1024 / tiles), rows / std::max<int64_t>(512, seen_rows)));
+    p.far_at = (p.floats + 3) / 4 * 4;
+    p.floats = p.far_at + (size_t)2 * (1 + p.far_parts) * p.far_rows * kv_heads * dim;
+  }
   return p;
 }
 

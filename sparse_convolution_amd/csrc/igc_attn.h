@@ -240,6 +240,19 @@ struct Stage {
       off[i] = (Off)(q2 * row_stride + g2 * head_stride + col(i) * (int)sizeof(T));
     }
   }
+  // Loads the tile of rows r, r + 1, ... of the sequence (keys only: group 1) without stepping: rows from `have` on are
+  // zero, rows from `cut` on lie `jump` bytes further.
+  __device__ __forceinline__ void load_at(const T* first, int64_t r0, int have, int cut, int64_t jump) {
+    base = (const char*)first + r0 * row_stride;
+    if (VEC && have >= ROWS && cut >= ROWS && dim == DP && (ROWS * CG) % NT == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = *(const typename Raw8<T>::type*)(base + off[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        r[i] = load8<T>((const T*)(base + off[i] + (row(i) >= cut ? jump : 0)), mine(i) && row(i) < have ? dim - col(i) : 0, VEC);
+    }
+  }
   // Loads the tile and steps to the next one. Rows from `have` on are zero.
   __device__ __forceinline__ void load(int have) {
     if (VEC && have >= ROWS && dim == DP && (ROWS * CG) % NT == 0) {
@@ -292,6 +305,23 @@ struct Stage {
     for (int k = 0; k < kParts<T>; ++k) *(bf16x8v*)(s + k * PS + row(i) * LD + col(i)) = f.p[k];
   }
 };
+
+// What of 32 NQ window rows, consecutive and in the lanes, a wave needs to know of a tile of places [j, j + n): whether
+// all rows see all of it, or none sees any.
+struct WindowWave {
+  WindowRow first, last;  // of the wave's first and last row
+  __device__ __forceinline__ void start(const WindowRow& lane_first, const WindowRow& lane_last) {
+    first.first = __builtin_amdgcn_readlane(lane_first.first, 0), last.first = __builtin_amdgcn_readlane(lane_last.first, 31);
+    first.low = __builtin_amdgcn_readlane(lane_first.low, 0), last.low = __builtin_amdgcn_readlane(lane_last.low, 31);
+    first.high = __builtin_amdgcn_readlane(lane_first.high, 0), last.high = __builtin_amdgcn_readlane(lane_last.high, 31);
+  }
+  __device__ __forceinline__ bool all(int j, int n) const { return (last.low <= j && first.high >= j + n) || first.first >= j + n; }
+  __device__ __forceinline__ bool none(int j, int n) const { return last.first <= j && (last.high <= j || first.low >= j + n); }
+};
+// Which of the places j .. j + 63 a row sees.
+__device__ __forceinline__ uint64_t window_bits(const WindowRow& r, int j) {
+  return low_bits(r.first - j) | (low_bits(r.high - j) & ~low_bits(r.low - j));
+}
 
 // LDS bytes a workgroup of four waves needs for its tiles (values of bf16) and for store_tile.
 template <typename T, int DP>

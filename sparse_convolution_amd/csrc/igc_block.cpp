@@ -1,5 +1,5 @@
 // extern "C" entry points of the operators between convolutions: layer norm, 8-bit activation
-// checkpoints, cross attention, norm and rotation of queries and keys, dropout. Every check runs on the host before any launch.
+// checkpoints, cross and window attention, norm and rotation of queries and keys, dropout. Every check runs on the host before any launch.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -118,13 +118,87 @@ size_t forward_bytes(const AttnArgs& a) {
 }
 
 // Checks a workspace of which `need` bytes are used.
-int check_workspace(const char* fn, const void* ws, size_t ws_bytes, size_t need) {
+int check_workspace(const char* fn, bool windowed, const void* ws, size_t ws_bytes, size_t need) {
   if (need == 0) return IGC_OK;
+  const std::string family = windowed ? "igc_window_attention" : "igc_cross_attention";
   if (!ws || ws_bytes < need)
     return set_error(IGC_ERR_CAPACITY, std::string(fn) + ": needs " + std::to_string(need) +
-                                           " bytes of workspace (igc_cross_attention_workspace)");
+                                           " bytes of workspace (" + family + "_workspace)");
   if (!aligned16(ws)) return set_error(IGC_ERR_INVALID_ARG, std::string(fn) + ": d_ws must be aligned to 16 bytes");
   return IGC_OK;
+}
+
+// Checks a window (null: none) and adds it to the device arguments.
+int window_args(const char* fn, const Window* w, AttnArgs& a) {
+  if (!w) return IGC_OK;
+  const std::string f(fn);
+  if (w->left < -1 || w->right < -1) return set_error(IGC_ERR_INVALID_ARG, f + ": left and right must be -1 (no limit) or more");
+  if (w->sinks < 0) return set_error(IGC_ERR_INVALID_ARG, f + ": sinks is negative");
+  a.windowed = w->left >= 0 || w->right >= 0;
+  a.win = *w;
+  if (w->left < 0) a.win.sinks = 0;  // all keys before a query are visible anyway
+  return IGC_OK;
+}
+
+int attention_workspace(const char* fn, const igc_attention_t* p, const Window* w, int32_t backward, size_t* bytes) {
+  AttnArgs a;
+  int rc = attention_args(fn, p, a);
+  if (!rc) rc = window_args(fn, w, a);
+  if (rc) return rc;
+  if (!bytes) return set_error(IGC_ERR_INVALID_ARG, std::string(fn) + ": bytes is null");
+  if (backward) {
+    *bytes = attn_bwd_plan(p->dtype, a).floats * sizeof(float);
+  } else {
+    a.splits = attn_fwd_splits(p->dtype, a);
+    *bytes = forward_bytes(a);
+  }
+  return IGC_OK;
+}
+
+int attention_forward(const char* fn, const igc_attention_t* p, const Window* w, const void* d_q, const void* d_k, const void* d_v,
+                      void* d_out, float* d_lse, void* d_ws, size_t ws_bytes, hipStream_t stream) {
+  const std::string f(fn);
+  AttnArgs a;
+  int rc = attention_args(fn, p, a);
+  if (!rc) rc = window_args(fn, w, a);
+  if (rc || a.nq == 0) return rc;
+  if (!d_q || !d_out || !d_lse || (a.nk > 0 && (!d_k || !d_v)))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": d_q, d_k, d_v, d_out or d_lse is null");
+  if (d_out == d_q || (d_out == d_k && a.nk > 0) || (d_out == d_v && a.nk > 0))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": d_out aliases an input");
+  a.q = d_q, a.k = d_k, a.v = d_v, a.out = d_out, a.lse = d_lse;
+  attention_alignment(p, a, d_out);
+  a.splits = attn_fwd_splits(p->dtype, a);
+  if (const int bad = check_workspace(fn, w, d_ws, ws_bytes, forward_bytes(a))) return bad;
+  a.part_a = (float*)d_ws;
+  a.part_b = a.part_a + forward_results(a);
+  return launch_attn_fwd(a, p->dtype, stream);
+}
+
+int attention_backward(const char* fn, const igc_attention_t* p, const Window* w, const void* d_q, const void* d_k, const void* d_v,
+                       const void* d_out, const float* d_lse, const void* d_dout, void* d_dq, void* d_dk, void* d_dv, void* d_ws,
+                       size_t ws_bytes, hipStream_t stream) {
+  const std::string f(fn);
+  AttnArgs a;
+  int rc = attention_args(fn, p, a);
+  if (!rc) rc = window_args(fn, w, a);
+  if (rc) return rc;
+  if (!d_dk != !d_dv) return set_error(IGC_ERR_INVALID_ARG, f + ": d_dk and d_dv come together");
+  if ((!d_dq || a.nq == 0) && (!d_dk || a.nk == 0)) return IGC_OK;
+  if (a.nq > 0 && (!d_q || !d_out || !d_lse || !d_dout))
+    return set_error(IGC_ERR_INVALID_ARG, f + ": d_q, d_out, d_lse or d_dout is null");
+  if (a.nk > 0 && (!d_k || !d_v)) return set_error(IGC_ERR_INVALID_ARG, f + ": d_k or d_v is null");
+  const void* in[] = {d_q, d_k, d_v, d_out, d_dout};
+  for (const void* g : {(const void*)d_dq, (const void*)d_dk, (const void*)d_dv})
+    for (const void* x : in)
+      if (g && g == x) return set_error(IGC_ERR_INVALID_ARG, f + ": a gradient aliases an input");
+  a.q = d_q, a.k = d_k, a.v = d_v, a.out_in = d_out, a.lse_in = d_lse, a.dout = d_dout;
+  a.dq = d_dq, a.dk = d_dk, a.dv = d_dv;
+  attention_alignment(p, a, (const void*)((uintptr_t)d_out | (uintptr_t)d_dout | (uintptr_t)d_dq | (uintptr_t)d_dk |
+                                          (uintptr_t)d_dv));
+  const AttnBwdPlan plan = attn_bwd_plan(p->dtype, a);
+  if (const int bad = check_workspace(fn, w, d_ws, ws_bytes, plan.floats * sizeof(float))) return bad;
+  return launch_attn_bwd(a, p->dtype, plan, d_ws, stream);
 }
 
 // Checks the problem's description and fills the device arguments (fn names the call).
@@ -245,63 +319,39 @@ int igc_dropout(const void* d_x, const void* d_residual, int64_t count, int32_t 
 }
 
 int igc_cross_attention_workspace(const igc_attention_t* p, int32_t backward, size_t* bytes) {
-  const char* fn = "igc_cross_attention_workspace";
-  AttnArgs a;
-  const int rc = attention_args(fn, p, a);
-  if (rc) return rc;
-  if (!bytes) return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_workspace: bytes is null");
-  if (backward) {
-    *bytes = attn_bwd_plan(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim).floats * sizeof(float);
-  } else {
-    a.splits = attn_fwd_splits(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
-    *bytes = forward_bytes(a);
-  }
-  return IGC_OK;
+  return attention_workspace("igc_cross_attention_workspace", p, nullptr, backward, bytes);
 }
 
 int igc_cross_attention(const igc_attention_t* p, const void* d_q, const void* d_k, const void* d_v, void* d_out,
                         float* d_lse, void* d_ws, size_t ws_bytes, igc_stream stream) {
-  const char* fn = "igc_cross_attention";
-  AttnArgs a;
-  const int rc = attention_args(fn, p, a);
-  if (rc || a.nq == 0) return rc;
-  if (!d_q || !d_out || !d_lse || (a.nk > 0 && (!d_k || !d_v)))
-    return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention: d_q, d_k, d_v, d_out or d_lse is null");
-  if (d_out == d_q || (d_out == d_k && a.nk > 0) || (d_out == d_v && a.nk > 0))
-    return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention: d_out aliases an input");
-  a.q = d_q, a.k = d_k, a.v = d_v, a.out = d_out, a.lse = d_lse;
-  attention_alignment(p, a, d_out);
-  a.splits = attn_fwd_splits(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
-  if (const int bad = check_workspace(fn, d_ws, ws_bytes, forward_bytes(a))) return bad;
-  a.part_a = (float*)d_ws;
-  a.part_b = a.part_a + forward_results(a);
-  return launch_attn_fwd(a, p->dtype, (hipStream_t)stream);
+  return attention_forward("igc_cross_attention", p, nullptr, d_q, d_k, d_v, d_out, d_lse, d_ws, ws_bytes, (hipStream_t)stream);
 }
 
 int igc_cross_attention_backward(const igc_attention_t* p, const void* d_q, const void* d_k, const void* d_v,
                                  const void* d_out, const float* d_lse, const void* d_dout, void* d_dq, void* d_dk,
                                  void* d_dv, void* d_ws, size_t ws_bytes, igc_stream stream) {
-  const char* fn = "igc_cross_attention_backward";
-  AttnArgs a;
-  const int rc = attention_args(fn, p, a);
-  if (rc) return rc;
-  if (!d_dk != !d_dv) return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_backward: d_dk and d_dv come together");
-  if ((!d_dq || a.nq == 0) && (!d_dk || a.nk == 0)) return IGC_OK;
-  if (a.nq > 0 && (!d_q || !d_out || !d_lse || !d_dout))
-    return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_backward: d_q, d_out, d_lse or d_dout is null");
-  if (a.nk > 0 && (!d_k || !d_v))
-    return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_backward: d_k or d_v is null");
-  const void* in[] = {d_q, d_k, d_v, d_out, d_dout};
-  for (const void* g : {(const void*)d_dq, (const void*)d_dk, (const void*)d_dv})
-    for (const void* x : in)
-      if (g && g == x) return set_error(IGC_ERR_INVALID_ARG, "igc_cross_attention_backward: a gradient aliases an input");
-  a.q = d_q, a.k = d_k, a.v = d_v, a.out_in = d_out, a.lse_in = d_lse, a.dout = d_dout;
-  a.dq = d_dq, a.dk = d_dk, a.dv = d_dv;
-  attention_alignment(p, a, (const void*)((uintptr_t)d_out | (uintptr_t)d_dout | (uintptr_t)d_dq | (uintptr_t)d_dk |
-                                          (uintptr_t)d_dv));
-  const AttnBwdPlan plan = attn_bwd_plan(p->dtype, a.nq, a.nk, a.batch, a.heads, a.kv_heads, a.dim);
-  if (const int bad = check_workspace(fn, d_ws, ws_bytes, plan.floats * sizeof(float))) return bad;
-  return launch_attn_bwd(a, p->dtype, plan, d_ws, (hipStream_t)stream);
+  return attention_backward("igc_cross_attention_backward", p, nullptr, d_q, d_k, d_v, d_out, d_lse, d_dout, d_dq, d_dk, d_dv, d_ws,
+                            ws_bytes, (hipStream_t)stream);
+}
+
+int igc_window_attention_workspace(const igc_attention_t* p, int32_t left, int32_t right, int32_t sinks, int32_t backward,
+                                   size_t* bytes) {
+  const Window w = {left, right, sinks};
+  return attention_workspace("igc_window_attention_workspace", p, &w, backward, bytes);
+}
+
+int igc_window_attention(const igc_attention_t* p, int32_t left, int32_t right, int32_t sinks, const void* d_q, const void* d_k,
+                         const void* d_v, void* d_out, float* d_lse, void* d_ws, size_t ws_bytes, igc_stream stream) {
+  const Window w = {left, right, sinks};
+  return attention_forward("igc_window_attention", p, &w, d_q, d_k, d_v, d_out, d_lse, d_ws, ws_bytes, (hipStream_t)stream);
+}
+
+int igc_window_attention_backward(const igc_attention_t* p, int32_t left, int32_t right, int32_t sinks, const void* d_q,
+                                  const void* d_k, const void* d_v, const void* d_out, const float* d_lse, const void* d_dout,
+                                  void* d_dq, void* d_dk, void* d_dv, void* d_ws, size_t ws_bytes, igc_stream stream) {
+  const Window w = {left, right, sinks};
+  return attention_backward("igc_window_attention_backward", p, &w, d_q, d_k, d_v, d_out, d_lse, d_dout, d_dq, d_dk, d_dv, d_ws,
+                            ws_bytes, (hipStream_t)stream);
 }
 
 int igc_layer_norm(const void* d_x, int64_t n, int32_t c, int32_t dtype, const void* d_w, const void* d_b,

@@ -8,6 +8,7 @@
 
 #include "../../include/igconv.h"
 #include "igc_internal.h"
+#include "igc_ragged.h"
 
 struct igc_grid {
   int device = 0;
@@ -269,6 +270,15 @@ struct AttnArgs {
   int splits = 1;
   int qvec = 0, kvec = 0, ovec = 0;  // 16-byte loads of q, of k and v, of the dense outputs allowed
   float scale = 1.f;
+  // Window attention (windowed != 0). The first `sinks` keys of a sequence, which later queries see too, get their gradients from
+  // far_parts further workgroups for each of their tiles, whose results are added up in `far`: [1 + far_parts][rows][kv_heads]
+  // [dim] for dk, then dv. Row b * sinks + j is key j of sequence b, or, where that takes more rows than keys
+  // (far_by_key), row r is key row r.
+  int windowed = 0, far_parts = 0, far_by_key = 0;
+  unsigned far_wgs = 0;
+  int64_t far_rows = 0;
+  float* far = nullptr;
+  Window win = {-1, -1, 0};
 };
 constexpr int32_t kAttnMaxDim = 128;
 // Keys, and query rows (queries times the heads that share a key head), of a problem at most: the kernels count those of a
@@ -276,13 +286,15 @@ constexpr int32_t kAttnMaxDim = 128;
 constexpr int64_t kAttnMaxRows = INT32_MAX - 1023;
 // Parts the key axis is split into; where there is more than one, the forward workspace holds dim partial results and two
 // statistics for each part, query and head.
-int attn_fwd_splits(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim);
+int attn_fwd_splits(int dtype, const AttnArgs& a);
 int launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s);
 struct AttnBwdPlan {
   int dq_splits = 1, dkv_splits = 1;
-  size_t floats = 0;  // workspace
+  int far_parts = 0, far_by_key = 0;  // as in AttnArgs
+  int64_t far_rows = 0;
+  size_t floats = 0, far_at = 0;  // workspace, and where `far` starts in it
 };
-AttnBwdPlan attn_bwd_plan(int dtype, int64_t nq, int64_t nk, int batch, int heads, int kv_heads, int dim);
+AttnBwdPlan attn_bwd_plan(int dtype, const AttnArgs& a);
 int launch_attn_bwd(const AttnArgs& a, int dtype, const AttnBwdPlan& p, void* ws, hipStream_t s);
 
 }  // namespace igc

@@ -53,4 +53,61 @@ __host__ __device__ __forceinline__ void split_row(int64_t r, int group, int64_t
   g = (int)(x - q * (uint32_t)group);
 }
 
+// Part `part` of `parts` of an axis of n places, [begin, end): all but the last a multiple of `step` long.
+__host__ __device__ __forceinline__ void split_axis(int64_t n, int parts, int part, int step, int64_t& begin, int64_t& end) {
+  const int64_t each = ((n + parts - 1) / parts + step - 1) / step * step;
+  begin = part * each < n ? part * each : n;
+  end = begin + each < n ? begin + each : n;
+}
+
+// A sliding window: query i of a sequence of lq queries and lk keys stands at p = i + lk - lq and sees the keys j <= p + right
+// that are no more than `left` behind it or among the first `sinks`. left or right -1: no limit.
+struct Window {
+  int64_t left, right;
+  int32_t sinks;
+};
+
+// The keys that the queries i0 .. i1 of a sequence see, as one axis of `keys` places: place x is key x before `sinks`, key x +
+// jump from there on.
+struct WindowAxis {
+  int64_t keys, sinks, jump;
+  __host__ __device__ __forceinline__ int64_t key(int64_t x) const { return x < sinks ? x : x + jump; }
+};
+__host__ __device__ __forceinline__ WindowAxis window_axis(const Window& w, int64_t i0, int64_t i1, int64_t lq, int64_t lk) {
+  const int64_t high = w.right < 0 ? lk : clamp64(i1 + lk - lq + w.right + 1, 0, lk);
+  const int64_t low = w.left < 0 ? 0 : clamp64(i0 + lk - lq - w.left, 0, high);
+  WindowAxis a;
+  a.sinks = w.sinks < low ? w.sinks : low;
+  a.jump = low - a.sinks;
+  a.keys = high - a.jump;
+  return a;
+}
+
+// The places that query i sees on that axis: those before `first` and those of [low, high).
+struct WindowRow {
+  int32_t first, low, high;
+};
+__host__ __device__ __forceinline__ WindowRow window_row(const Window& w, const WindowAxis& a, int64_t i, int64_t lq, int64_t lk) {
+  const int64_t p = i + lk - lq;
+  const int64_t high = w.right < 0 ? lk : clamp64(p + w.right + 1, 0, lk);
+  const int64_t low = w.left < 0 ? 0 : clamp64(p - w.left, 0, lk);
+  WindowRow r;
+  r.first = (int32_t)(w.sinks < high ? w.sinks : high);
+  r.low = (int32_t)clamp64(low - a.jump, 0, lk);
+  r.high = (int32_t)clamp64(high - a.jump, 0, lk);
+  return r;
+}
+
+// The queries [begin, end) that see key j; `window`: of a sink, only those whose window holds it too.
+__host__ __device__ __forceinline__ void window_queries(const Window& w, int64_t j, int64_t lq, int64_t lk, bool window,
+                                                        int64_t& begin, int64_t& end) {
+  begin = w.right < 0 ? 0 : clamp64(j - w.right - (lk - lq), 0, lq);
+  end = w.left < 0 || (!window && j < w.sinks) ? lq : clamp64(j + w.left + 1 - (lk - lq), begin, lq);
+}
+
+// The lowest n of 64 bits.
+__host__ __device__ __forceinline__ uint64_t low_bits(int32_t n) {
+  return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1;
+}
+
 }  // namespace igc

@@ -143,3 +143,43 @@ def test_binding_on_the_device():
         igc.dropout(x, 0.1, -1)
     with pytest.raises(igc.IgcError, match="p must be"):
         igc.dropout(x, 1.5, 3)
+
+
+@pytest.mark.parametrize("left,right,sinks,word", [(-2, 0, 0, b"left"), (3, -2, 0, b"right"), (3, 0, -1, b"sinks")])
+def test_windows(lib, left, right, sinks, word):
+    from tests.test_block_refusals import _problem
+    p, size = ctypes.byref(_problem()), ctypes.c_size_t(0)
+    _refused(lib, INVALID, lib.igc_window_attention_workspace(p, left, right, sinks, 0, ctypes.byref(size)), word)
+    _refused(lib, INVALID, lib.igc_window_attention(p, left, right, sinks, P, P, P, Q, Q, Q, 1 << 40, None), word)
+    _refused(lib, INVALID, lib.igc_window_attention_backward(p, left, right, sinks, P, P, P, P, P, P, Q, Q, Q, Q, 1 << 40, None), word)
+
+
+def test_window_problems_and_operands(lib):
+    from tests.test_block_refusals import _problem
+    size = ctypes.c_size_t(0)
+    for change, status, word in (({"dtype": 3}, INVALID, b"dtype"), ({"dim": 129}, UNSUPPORTED, b"128"), ({"n_k": 1 << 31}, RANGE, b"2^31"),
+                                 ({"batch": 2}, INVALID, b"offsets"), ({"scale": 0.0}, INVALID, b"scale")):
+        p = ctypes.byref(_problem(**change))
+        _refused(lib, status, lib.igc_window_attention_workspace(p, 9, 0, 2, 1, ctypes.byref(size)), word)
+        _refused(lib, status, lib.igc_window_attention(p, 9, 0, 2, P, P, P, Q, Q, Q, 1 << 40, None), word)
+        assert b"igc_window_attention:" in lib.igc_last_error()
+    p, few = ctypes.byref(_problem()), ctypes.byref(_problem(n_q=1, n_k=100000))
+    fwd, bwd = lib.igc_window_attention, lib.igc_window_attention_backward
+    _refused(lib, INVALID, fwd(None, 9, 0, 2, P, P, P, Q, Q, None, 0, None), b"problem")
+    _refused(lib, INVALID, fwd(p, 9, 0, 2, None, P, P, Q, Q, None, 0, None), b"d_q")
+    _refused(lib, INVALID, fwd(p, 9, 0, 2, P, P, P, P, Q, None, 0, None), b"aliases")
+    _refused(lib, CAPACITY, fwd(few, 9000, 0, 2, P, P, P, Q, Q, None, 0, None), b"igc_window_attention_workspace")
+    _refused(lib, CAPACITY, bwd(p, 9, 0, 2, P, P, P, P, P, P, Q, Q, Q, Q, 8, None), b"igc_window_attention_workspace")
+    _refused(lib, INVALID, bwd(p, 9, 0, 2, P, P, P, P, P, P, Q, Q, Q, ctypes.c_void_p(8196), 1 << 40, None), b"aligned")
+    _refused(lib, INVALID, bwd(p, 9, 0, 2, P, P, P, P, P, P, Q, Q, None, Q, 1 << 40, None), b"together")
+    _refused(lib, INVALID, lib.igc_window_attention_workspace(p, 9, 0, 2, 0, None), b"bytes")
+    none = ctypes.byref(_problem(n_q=0, n_k=0))
+    assert fwd(none, 9, 0, 2, None, None, None, None, None, None, 0, None) == 0
+    assert bwd(none, 9, 0, 2, None, None, None, None, None, None, None, None, None, None, 0, None) == 0
+    import sparse_convolution_amd as igc
+    x = torch.zeros(4, 2, 8)
+    with pytest.raises(TypeError, match="q must be a CUDA"):
+        igc.window_attention(x, x, x, 3, 0)
+    for kw in (dict(left=-1), dict(right=-1), dict(sinks=-1), dict(left=1 << 31), dict(sinks=1 << 31)):
+        with pytest.raises(ValueError, match="must be 0 to"):
+            igc.window_attention(x, x, x, **kw)
