@@ -30,20 +30,23 @@ constexpr int kNT = 256;
 // almost always. 215,003 queries on 5 x ~1024 keys, 4 heads of 64, measured in turn: 306 us without, 293 with.
 constexpr float kSlack = 8.f;
 
-// Four waves of 32 NQ query rows each over tiles of BN keys. A row is a (query, head of the group
+// NW waves of 32 NQ query rows each over tiles of BN keys. A row is a (query, head of the group
 // that shares the key head) pair, so few queries with shared key heads still fill a tile.
 // splits > 1: each workgroup takes one part of the sequence's keys and leaves an unnormalised result.
-// WIN: a query sees the keys of a window and a few first ones (see igc_ragged.h). The tile's workgroup walks the keys that any of its
-// queries sees, a wave passes over tiles that none of its own sees, and only tiles on an edge are masked.
-template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, bool WIN>
-__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_fwd(AttnArgs a) {
+// WIN 1: a query sees the keys of a window and a few first ones (see igc_ragged.h); 2: and a key mask keeps some. The workgroup walks the
+// keys that any of its queries sees; a wave passes over those that none of its own sees, and masks by rows only where an
+// edge runs through, 32 keys at a time. The key mask enters as a bias.
+template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, int WIN, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_fwd(AttnArgs a) {
   typedef Frag<T> frag;
+  constexpr int NT = 64 * NW;
   constexpr int LD = lds_ld<DP>(), PS = BN * LD;
-  constexpr int BM = 128 * NQ;
+  constexpr int BM = 32 * NQ * NW;
   constexpr int KT = BN / 32, DT = DP / 32;
   constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
   constexpr int TILE = kParts<T> * PS;
-  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE)];
+  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE, NW)];
+  __shared__ __attribute__((aligned(16))) float s_bias[WIN == 2 ? 2 : 1][WIN == 2 ? BN : 1];
   auto s_k = [&](int buf) { return (bf16_t*)s_mem + buf * TILE; };
   auto s_v = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
 
@@ -60,10 +63,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   // WIN: the tile's keys as one axis, of which this workgroup takes places x0 .. x0 + keys.
   WindowAxis axis = {};
   const int64_t lq = q1 - q0, lk = k1 - k0;
-  int64_t x0 = 0, x1 = 0;
+  int64_t x0 = 0, x1 = 0, i0 = 0;
+  WindowTile tile_sees = {};
   if constexpr (WIN) {
-    axis = window_axis(a.win, tile * BM / a.group, ((tile + 1) * BM < rows ? (tile + 1) * BM - 1 : rows - 1) / a.group, lq, lk);
+    i0 = row_query(tile * BM, a.group);
+    axis = window_axis(a.win, i0, row_query(((tile + 1) * BM < rows ? (tile + 1) * BM : rows) - 1, a.group), lq, lk);
     split_axis(axis.keys, a.splits, split, BN, x0, x1);
+    tile_sees = window_tile(a.win, axis, x0, i0, lq, lk);
   } else if (a.splits > 1) {
     const int64_t part = ((k1 - k0 + a.splits - 1) / a.splits + BN - 1) / BN * BN;
     k0 = k0 + split * part < k1 ? k0 + split * part : k1;
@@ -71,26 +77,31 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   }
   int keys = WIN ? (int)(x1 - x0) : (int)(k1 - k0);
 
-  Stage<T, BN, DP, kNT, VEC> sk, sv;
+  Stage<T, BN, DP, NT, VEC> sk, sv;
   sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], 0, a.ks[0], 0, 1, a.dim);
   sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], 0, a.vs[0], 0, 1, a.dim);
   // Whether key j + lane exists and the mask keeps it. The ballot of these comes a tile later: at once it would wait for
   // the tile's loads too.
   auto key_ok = [&](int j) -> int {
-    if constexpr (WIN) return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + axis.key(x0 + j + lane)] : 1) : 0;
+    if constexpr (WIN == 1) return 1;
+    if constexpr (WIN == 2) return lane < BN && j + lane < keys ? a.mask[k0 + axis.key(x0 + j + lane)] : 0;
     return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + j + lane] : 1) : 0;
   };
+  // Tiles up to the one behind the last sink start where the axis says, others a tile behind the last.
+  const int near_sinks = WIN ? (int)clamp64(axis.sinks - x0 + BN, 0, keys) : 0;
   auto fetch = [&](int j) {
     if constexpr (WIN) {
-      const int64_t x = x0 + j, cut = axis.sinks - x;
-      const int64_t r = cut > 0 ? x : x + axis.jump;
-      const int until = cut > 0 && cut < BN ? (int)cut : BN;
-      sk.load_at((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], r, keys - j, until, axis.jump * sk.row_stride);
-      sv.load_at((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], r, keys - j, until, axis.jump * sv.row_stride);
-    } else {
-      sk.load(keys - j);
-      sv.load(keys - j);
+      if (j == 0 || j < near_sinks) {
+        const int64_t x = x0 + j, cut = axis.sinks - x;
+        const int64_t r = cut > 0 ? x : x + axis.jump;
+        const int until = cut > 0 && cut < BN ? (int)cut : BN;
+        sk.load_at((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], r, keys - j, until, axis.jump * sk.row_stride);
+        sv.load_at((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], r, keys - j, until, axis.jump * sv.row_stride);
+        return key_ok(j);
+      }
     }
+    sk.load(keys - j);
+    sv.load(keys - j);
     return key_ok(j);
   };
   int next_ok = fetch(0);
@@ -104,7 +115,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
     int64_t qi;
     int head;
-    split_row(r < rows ? r : 0, a.group, qi, head);
+    // WIN: rows behind the last one see what it sees.
+    split_row(r < rows ? r : WIN ? rows - 1 : 0, a.group, qi, head);
+    if constexpr (WIN) see[n] = tile_sees.row((int)(qi - i0));
     qi += q0;
     head += kh * a.group;
     row[n] = r < rows ? qi * a.heads + head : -1;
@@ -114,12 +127,6 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       const int d = kk * 16 + h * 8;
       fq[n][kk] = to_parts(load8<T>(p + d, r < rows ? a.dim - d : 0, VEC));
     }
-    if constexpr (WIN) {  // rows behind the last one see what it sees
-      int64_t i;
-      split_row(r < rows ? r : rows - 1, a.group, i, head);
-      see[n] = window_row(a.win, axis, i, lq, lk);
-      see[n].first -= (int)x0, see[n].low -= (int)x0, see[n].high -= (int)x0;
-    }
   }
   WindowWave wave_sees;
   if constexpr (WIN) wave_sees.start(see[0], see[NQ - 1]);
@@ -128,54 +135,46 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   const float c = a.scale * kLog2e, slack = fminf(kSlack / c, 3.4e38f);
   f32x16 o[NQ][DT];
   float m[NQ], l[NQ];  // references (in the scores' units) and this lane's part of the sums
+  float from[NQ];      // what scores are counted from: m, 0 before there is one
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     m[n] = -INFINITY;
+    from[n] = 0.f;
     l[n] = 0.f;
 #pragma unroll
     for (int t = 0; t < DT; ++t) o[n][t] = zero16();
   }
 
-  int buf = 0;
-  for (int j = 0; j < keys; j += BN, buf ^= 1) {
-    const uint64_t bits = __ballot(next_ok != 0);
-    if (a.mask) {  // what a masked place holds must not meet a zero probability
-      sk.template store<LD, PS>(s_k(buf), bits);
-      sv.template store<LD, PS>(s_v(buf), bits);
-    } else {
-      sk.template store<LD, PS>(s_k(buf));
-      sv.template store<LD, PS>(s_v(buf));
-    }
-    if (j + BN < keys) next_ok = fetch(j + BN);
-    // Two buffers: the barrier of the last tile already had every wave past reading this one.
-    __syncthreads();
-    if (WIN && wave_sees.none(j, BN)) continue;
-    f32x16 s[NQ][KT];
+  int buf = 0, j = 0;
+  uint64_t bits = kAll;
+  // The tile's blocks of 32 keys from t0 on, C of them: scores, softmax and the product with v.
+  auto blocks = [&](auto count, int t0) {
+    constexpr int C = decltype(count)::value;
+    f32x16 s[NQ][C];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
+    for (int t = 0; t < C; ++t) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) s[n][t] = zero16();
+      if constexpr (WIN == 2) {
+        s[0][t] = from_bias(s_bias[buf] + (t0 + t) * 32);
+#pragma unroll
+        for (int n = 1; n < NQ; ++n) s[n][t] = s[0][t];
+      }
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
-        const frag fk = load_row<T, PS>(s_k(buf) + (t * 32 + (lane & 31)) * LD + kk * 16 + h * 8);
+        const frag fk = load_row<T, PS>(s_k(buf) + ((t0 + t) * 32 + (lane & 31)) * LD + kk * 16 + h * 8);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) s[n][t] = mma(fk, fq[n][kk], s[n][t]);
       }
     }
-    if (WIN && !(bits == kAll && wave_sees.all(j, BN))) {
+    if (WIN && !wave_sees.all(j + 32 * t0, 32 * C)) {
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        const uint64_t mine = bits & window_bits(see[n], j);
+      for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          const uint32_t w = (uint32_t)(mine >> (32 * t)) >> (4 * h);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[n][t][r] = w & (1u << (8 * (r >> 2) + (r & 3))) ? s[n][t][r] : -INFINITY;
-        }
-      }
+        for (int t = 0; t < C; ++t) clear_unseen(s[n][t], see[n], wave_sees, j + 32 * (t0 + t), -INFINITY);
     } else if (!WIN && bits != kAll) {
 #pragma unroll
-      for (int t = 0; t < KT; ++t) {
+      for (int t = 0; t < C; ++t) {
         const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
@@ -189,7 +188,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     for (int n = 0; n < NQ; ++n) {
       float top = max16(s[n][0]);
 #pragma unroll
-      for (int t = 1; t < KT; ++t) top = fmaxf(top, max16(s[n][t]));
+      for (int t = 1; t < C; ++t) top = fmaxf(top, max16(s[n][t]));
       const float m_new = fmaxf(m[n], halves_max(top));
       if (__any(m_new > m[n] + slack)) {
         asm volatile("");  // a branch: the compiler would multiply always and select
@@ -200,10 +199,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[n][t][r] *= f;
         m[n] = m_new;
+        if constexpr (WIN) from[n] = m_new == -INFINITY ? 0.f : m_new;
       }
-      const float base = m[n] == -INFINITY ? 0.f : m[n];
+      const float base = WIN ? from[n] : m[n] == -INFINITY ? 0.f : m[n];
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+      for (int t = 0; t < C; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           // bf16 data: one instruction. fp32: the difference first, which is exact near the reference.
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         }
     }
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+    for (int t = 0; t < C; ++t)
 #pragma unroll
       for (int mm = 0; mm < 2; ++mm) {
         // bf16 data: p rounded once, since the matrix cores take bf16. out is then off by 1.26 to 1.39 times what its own
@@ -224,11 +224,32 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
         for (int n = 0; n < NQ; ++n) p[n] = to_frag<T>(s[n][t], mm);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const frag fv = load_tr<T, LD, PS>(s_v(buf), t * 32 + mm * 16, d * 32);
+          const frag fv = load_tr<T, LD, PS>(s_v(buf), (t0 + t) * 32 + mm * 16, d * 32);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) o[n][d] = mma(fv, p[n], o[n][d]);
         }
       }
+  };
+  for (; j < keys; j += BN, buf ^= 1) {
+    if constexpr (WIN != 1) bits = __ballot(next_ok != 0);
+    if (WIN != 1 && a.mask) {  // what a masked place holds must not meet a zero probability
+      sk.template store<LD, PS>(s_k(buf), bits);
+      sv.template store<LD, PS>(s_v(buf), bits);
+      if (WIN == 2 && wave == 0 && lane < BN) s_bias[buf][lane] = next_ok ? 0.f : -INFINITY;
+    } else {
+      sk.template store<LD, PS>(s_k(buf));
+      sv.template store<LD, PS>(s_v(buf));
+    }
+    if (j + BN < keys) next_ok = fetch(j + BN);
+    // Two buffers: the barrier of the last tile already had every wave past reading this one.
+    __syncthreads();
+    if constexpr (!WIN) {
+      blocks(std::integral_constant<int, KT>{}, 0);
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < KT; ++t)
+        if (!wave_sees.none(j + 32 * t, 32)) blocks(std::integral_constant<int, 1>{}, t);
+    }
   }
 
   __syncthreads();  // every wave is past reading the tiles: their space takes the results
@@ -275,10 +296,13 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
   if (tile * R >= rows) return;
   WindowAxis axis = {};  // as in k_attn_fwd
   const int64_t lq = q1 - q0, lk = k1 - k0;
-  int64_t x0 = 0, x1 = 0;
+  int64_t x0 = 0, x1 = 0, i0 = 0;
+  WindowTile tile_sees = {};
   if constexpr (WIN) {
-    axis = window_axis(a.win, tile * R / a.group, ((tile + 1) * R < rows ? (tile + 1) * R - 1 : rows - 1) / a.group, lq, lk);
+    i0 = row_query(tile * R, a.group);
+    axis = window_axis(a.win, i0, row_query(((tile + 1) * R < rows ? (tile + 1) * R : rows) - 1, a.group), lq, lk);
     split_axis(axis.keys, a.splits, split, 1, x0, x1);
+    tile_sees = window_tile(a.win, axis, x0, i0, lq, lk);
   } else if (a.splits > 1) {
     const int64_t part = (k1 - k0 + a.splits - 1) / a.splits;
     k0 = k0 + split * part < k1 ? k0 + split * part : k1;
@@ -311,8 +335,8 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
     const int64_t x = tile * R + r;
     int64_t qi;
     int head;
-    split_row(x < rows ? x : 0, a.group, qi, head);
-    if constexpr (WIN) see[r] = window_row(a.win, axis, qi, lq, lk);
+    split_row(x < rows ? x : WIN ? rows - 1 : 0, a.group, qi, head);
+    if constexpr (WIN) see[r] = tile_sees.row((int)(qi - i0));
     const frag f = load8<T>((const T*)a.q + (q0 + qi) * a.qs[0] + (kh * a.group + head) * a.qs[1] + d,
                             x < rows ? a.dim - d : 0, VEC);
 #pragma unroll
@@ -342,7 +366,7 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
         s[u] = lanes_sum<LPK>(s[u]);
         bool keep = now >> u & 1;
         if constexpr (WIN) {
-          const int x = (int)x0 + j + u * KPW + g;
+          const int x = j + u * KPW + g;
           keep = keep && (x < see[r].first || (x >= see[r].low && x < see[r].high));
         }
         s[u] = keep ? s[u] : -INFINITY;
@@ -413,6 +437,9 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
 }
 
 constexpr int kMaxParts = 128;
+// Rows from which on a wave joins each (k_attn_join_rows) instead of a workgroup: 18,002 rows of 2 parts 8 us instead of 18, 512
+// rows of 4 parts 0.5 us slower.
+constexpr int64_t kJoinRows = 1024;
 
 // Joins the parts of a split key axis, one workgroup per row of a sequence: a lane per part weighs it, then the waves
 // share the parts and the lanes the channels.
@@ -471,6 +498,36 @@ struct FwdShape<float, DP> {
   static constexpr int NQ = 1, BN = 32, WPE = DP <= 64 ? 2 : 1;
 };
 
+// Shapes of window attention: 32 NQ rows of a wave, keys of a tile, waves per SIMD, waves of a workgroup. Other than without
+// windows, where heads of 64 do best with two tiles of rows a wave and two waves per SIMD: a wave's rows see few keys each and
+// more of them beside its own rows' windows, so one tile of rows and more waves do better. us, bf16, heads of 64, windows of 256
+// to either side over 200,003 rows / 64 over 200,003 / 2,047 before over 60,000, 4 heads: (1, 32, 4, 4) 207, 108, 186; (1, 64, 3,
+// 4) 228, 108, 196; (2, 64, 2, 4) 273, 149, 199; (2, 32, 2, 2) 240, 126, 207; (1, 32, 4, 2) 304, 138, 265. Heads of 32, 256 to
+// either side, 8 heads: (1, 64, 3, 4) 292, (1, 64, 2, 4) 298, (2, 64, 3, 4) 334. fp32, 50,003 rows, 4 heads, 256 to either side, heads
+// of 32 and the small case of 7,131 rows, 64 to either side: (1, 32, 2, 2) 123 and 14.1, (1, 32, 3, 4) 119 and 17.5; heads of 64: (1,
+// 32, 3, 4) 205, (1, 32, 2, 4) 213, (1, 32, 2, 2) 309.
+template <int Q, int N, int E, int W>
+struct Shape {
+  static constexpr int NQ = Q, BN = N, WPE = E, NW = W;
+};
+template <typename T, int DP>
+struct WinShape : Shape<1, 32, 1, 4> {};
+template <int DP>
+struct WinShape<bf16_t, DP> : Shape<1, 64, 2, 4> {};
+template <>
+struct WinShape<bf16_t, 32> : Shape<1, 64, 3, 4> {};
+template <>
+struct WinShape<bf16_t, 64> : Shape<1, 32, 4, 4> {};
+template <>
+struct WinShape<float, 32> : Shape<1, 32, 2, 2> {};
+template <>
+struct WinShape<float, 64> : Shape<1, 32, 3, 4> {};
+template <typename T>
+int win_rows(int dim) {
+  auto rows = [](auto s) { return 32 * s.NQ * s.NW; };
+  return dim <= 32 ? rows(WinShape<T, 32>{}) : dim <= 64 ? rows(WinShape<T, 64>{}) : dim <= 96 ? rows(WinShape<T, 96>{}) : rows(WinShape<T, 128>{});
+}
+
 constexpr int kFewRows = 4;
 
 // Query rows of a tile: a few (k_attn_few) or those of the matrix kernel. Decided from the average number of rows
@@ -493,30 +550,83 @@ constexpr int kFewRows = 4;
 // So a few rows take k_attn_few, but for bf16 heads over 64, where the matrix kernel is ahead throughout. What the rule
 // gives away is up to 11 us a call on small problems, bf16 in the main, whose parts of 256 keys leave the GPU half empty.
 // 8 rows of bf16, 64 x 4096 keys, 8 heads of 64: 184 / 101.
-int fwd_rows(int dtype, int dim, int64_t nq, int batch, int group) {
+int fwd_rows(int dtype, int dim, int64_t nq, int batch, int group, bool windowed) {
   const int64_t rows = (nq + batch - 1) / batch * group;
   if (dtype == IGC_F32 || dim <= 64) {
     for (int r = 1; r <= kFewRows; r *= 2)
       if (rows <= r) return r;
   }
+  if (windowed) return dtype == IGC_BF16 ? win_rows<bf16_t>(dim) : win_rows<float>(dim);
   return dtype == IGC_BF16 && dim <= 64 ? 256 : 128;
+}
+
+// The same, a wave for each row: for many rows, whose parts are few. Sums in k_attn_join's order, so the same bits.
+template <typename T>
+__global__ __launch_bounds__(kNT) void k_attn_join_rows(AttnArgs a) {
+  const int lane = lane_id();
+  const int64_t rows = a.nq * a.heads, row = (int64_t)blockIdx.x * (kNT / 64) + (threadIdx.x >> 6);
+  int64_t q0, q1;
+  covered_rows(a.qo, a.batch, a.nq, q0, q1);
+  if (row < q0 * a.heads || row >= q1 * a.heads) return;
+  float m[2], l[2], w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int part = lane + 64 * i;
+    const float2 ml = part < a.splits ? ((const float2*)a.part_b)[part * rows + row] : make_float2(-INFINITY, 0.f);
+    m[i] = ml.x;
+    l[i] = ml.y;
+  }
+  const float top = lanes_reduce<64>(fmaxf(m[0], m[1]), [](float x, float y) { return fmaxf(x, y); });
+  const float base = top == -INFINITY ? 0.f : top;
+  float total = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[i] = __builtin_amdgcn_exp2f(m[i] - base);
+    total += w[i] * l[i];
+  }
+  total = lanes_sum<64>(total);
+  const float* po = a.part_a + row * a.dim;
+  float o[4][2] = {};
+  for (int first = 0; first < a.splits; first += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int part = first + i;
+      if (part >= a.splits) break;
+      const float x = __shfl(part < 64 ? w[0] : w[1], part & 63, 64);
+      const float* p = po + part * rows * a.dim;
+      if (lane < a.dim) o[i][0] += x * p[lane];
+      if (lane + 64 < a.dim) o[i][1] += x * p[lane + 64];
+    }
+  }
+  const float f = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 64 * i < a.dim) ((T*)a.out)[row * a.dim + lane + 64 * i] = (T)(((o[0][i] + o[1][i]) + (o[2][i] + o[3][i])) * f);
+  if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : kLn2 * (top + log2f(total));
 }
 
 template <typename T>
 void join(const AttnArgs& a, hipStream_t s) {
-  if (a.splits > 1) k_attn_join<T><<<(unsigned)(a.nq * a.heads), kNT, 0, s>>>(a);
+  if (a.splits == 1) return;
+  const int64_t rows = a.nq * a.heads;
+  if (rows > kJoinRows) k_attn_join_rows<T><<<(unsigned)((rows + kNT / 64 - 1) / (kNT / 64)), kNT, 0, s>>>(a);
+  else k_attn_join<T><<<(unsigned)rows, kNT, 0, s>>>(a);
 }
 
 template <typename T, int DP>
 void fwd_go(const AttnArgs& a, unsigned wgs, hipStream_t s) {
-  constexpr int NQ = FwdShape<T, DP>::NQ, BN = FwdShape<T, DP>::BN, WPE = FwdShape<T, DP>::WPE;
+  typedef FwdShape<T, DP> F;
+  typedef WinShape<T, DP> W;
   const bool vec = a.qvec && a.kvec;
-  if (a.windowed) {
-    if (vec) k_attn_fwd<T, DP, NQ, BN, WPE, true, true><<<wgs, kNT, 0, s>>>(a);
-    else k_attn_fwd<T, DP, NQ, BN, WPE, false, true><<<wgs, kNT, 0, s>>>(a);
+  if (a.windowed && a.mask) {
+    if (vec) k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, true, 2, W::NW><<<wgs, 64 * W::NW, 0, s>>>(a);
+    else k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, false, 2, W::NW><<<wgs, 64 * W::NW, 0, s>>>(a);
+  } else if (a.windowed) {
+    if (vec) k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, true, 1, W::NW><<<wgs, 64 * W::NW, 0, s>>>(a);
+    else k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, false, 1, W::NW><<<wgs, 64 * W::NW, 0, s>>>(a);
   } else {
-    if (vec) k_attn_fwd<T, DP, NQ, BN, WPE, true, false><<<wgs, kNT, 0, s>>>(a);
-    else k_attn_fwd<T, DP, NQ, BN, WPE, false, false><<<wgs, kNT, 0, s>>>(a);
+    if (vec) k_attn_fwd<T, DP, F::NQ, F::BN, F::WPE, true, 0, 4><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_fwd<T, DP, F::NQ, F::BN, F::WPE, false, 0, 4><<<wgs, kNT, 0, s>>>(a);
   }
 }
 
@@ -540,7 +650,7 @@ void few_r(const AttnArgs& a, int rows, unsigned wgs, hipStream_t s) {
 
 template <typename T>
 void fwd_t(const AttnArgs& a, int dtype, hipStream_t s) {
-  const int rows = fwd_rows(dtype, a.dim, a.nq, a.batch, a.group);
+  const int rows = fwd_rows(dtype, a.dim, a.nq, a.batch, a.group, a.windowed);
   const unsigned wgs = (unsigned)((a.nq * a.group / rows + a.batch) * a.kv_heads * a.splits);
   if (rows <= kFewRows) {
     if (a.dim <= 32) few_r<T, 4>(a, rows, wgs, s);
@@ -562,7 +672,7 @@ int attn_fwd_splits(int dtype, const AttnArgs& a) {
   const int batch = a.batch, heads = a.heads, kv_heads = a.kv_heads, dim = a.dim;
   // Parts of the key axis: none while the query tiles alone fill the GPU, else enough for that, each of
   // at least 256 keys.
-  const int bm = fwd_rows(dtype, dim, nq, batch, heads / kv_heads);
+  const int bm = fwd_rows(dtype, dim, nq, batch, heads / kv_heads, a.windowed);
   const int64_t per_seq = (nq + batch - 1) / batch * (heads / kv_heads);
   const int64_t wgs = batch * ((per_seq + bm - 1) / bm) * kv_heads;
   // Workgroups that fill it: two a CU of the matrix kernel, three of its fp32 form for short heads, which is small enough
@@ -575,7 +685,10 @@ int attn_fwd_splits(int dtype, const AttnArgs& a) {
   int64_t keys = nk / batch;  // that a tile walks
   if (a.windowed && a.win.left >= 0 && a.win.right >= 0)
     keys = std::min<int64_t>(keys, a.win.left + a.win.right + bm / a.group + a.win.sinks);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxParts), keys / 256));
+  // Rows of windows are many, and so is what their parts leave to be joined. Parts of at least 256 / 384 / 1,024 keys, us: 9,001
+  // rows of 2 sequences, 2 heads of 64, bf16, 511 keys before: 26 / 19 / 19; 4,000 rows, 1,999 before: 27 / 26 / 32.
+  const int64_t least = a.windowed && bm > kFewRows ? kWindowPart : 256;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxParts), keys / least));
 }
 
 int launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s) {

@@ -29,16 +29,17 @@ constexpr int kNT = 256;
 // lse in base 2; +infinity for rows without keys, whose probabilities are then exp2(-infinity) = 0.
 __device__ __forceinline__ float lse_base2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-// dq and delta: four waves of 32 NQ query rows over tiles of BN keys (see k_attn_fwd for rows and windows).
-template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, bool WIN>
-__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dq(AttnArgs a) {
+// dq and delta: NW waves of 32 NQ query rows over tiles of BN keys (see k_attn_fwd for rows, WIN and the key mask's bias).
+template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, int WIN, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dq(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int LD = lds_ld<DP>(), PS = BN * LD;
-  constexpr int BM = 128 * NQ;
+  constexpr int NT = 64 * NW, BM = 32 * NQ * NW;
   constexpr int KT = BN / 32, DT = DP / 32;
   constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
   constexpr int TILE = kParts<T> * PS;
-  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE)];
+  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE, NW)];
+  __shared__ __attribute__((aligned(16))) float s_bias[WIN == 2 ? 2 : 1][WIN == 2 ? BN : 1];
   auto s_k = [&](int buf) { return (bf16_t*)s_mem + buf * TILE; };
   auto s_v = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
 
@@ -54,36 +55,44 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   if (tile * BM >= rows) return;
   WindowAxis axis = {};  // as in k_attn_fwd
   const int64_t lq = q1 - q0, lk = k1 - k0;
-  int64_t x0 = 0, x1 = 0;
+  int64_t x0 = 0, x1 = 0, i0 = 0;
+  WindowTile tile_sees = {};
   if (!a.dq) k1 = k0;  // only delta is wanted
   if constexpr (WIN) {
-    axis = window_axis(a.win, tile * BM / a.group, ((tile + 1) * BM < rows ? (tile + 1) * BM - 1 : rows - 1) / a.group, lq, lk);
+    i0 = row_query(tile * BM, a.group);
+    axis = window_axis(a.win, i0, row_query(((tile + 1) * BM < rows ? (tile + 1) * BM : rows) - 1, a.group), lq, lk);
     split_axis(a.dq ? axis.keys : 0, a.splits, split, BN, x0, x1);
+    tile_sees = window_tile(a.win, axis, x0, i0, lq, lk);
   } else if (a.splits > 1) {
     const int64_t part = ((k1 - k0 + a.splits - 1) / a.splits + BN - 1) / BN * BN;
     k0 = k0 + split * part < k1 ? k0 + split * part : k1;
     k1 = k0 + part < k1 ? k0 + part : k1;
   }
   const int keys = WIN ? (int)(x1 - x0) : (int)(k1 - k0);
-  Stage<T, BN, DP, kNT, VEC> sk, sv;
+  Stage<T, BN, DP, NT, VEC> sk, sv;
   sk.start((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], 0, a.ks[0], 0, 1, a.dim);
   sv.start((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], 0, a.vs[0], 0, 1, a.dim);
   // As in k_attn_fwd: the ballot comes a tile later, so that it waits for no loads (100,003 queries, masked: 231 and 213 us).
   auto key_ok = [&](int j) -> int {
-    if constexpr (WIN) return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + axis.key(x0 + j + lane)] : 1) : 0;
+    if constexpr (WIN == 1) return 1;
+    if constexpr (WIN == 2) return lane < BN && j + lane < keys ? a.mask[k0 + axis.key(x0 + j + lane)] : 0;
     return lane < BN && j + lane < keys ? (a.mask ? a.mask[k0 + j + lane] : 1) : 0;
   };
+  // Tiles up to the one behind the last sink start where the axis says, others a tile behind the last.
+  const int near_sinks = WIN ? (int)clamp64(axis.sinks - x0 + BN, 0, keys) : 0;
   auto fetch = [&](int j) {
     if constexpr (WIN) {
-      const int64_t x = x0 + j, cut = axis.sinks - x;
-      const int64_t r = cut > 0 ? x : x + axis.jump;
-      const int until = cut > 0 && cut < BN ? (int)cut : BN;
-      sk.load_at((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], r, keys - j, until, axis.jump * sk.row_stride);
-      sv.load_at((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], r, keys - j, until, axis.jump * sv.row_stride);
-    } else {
-      sk.load(keys - j);
-      sv.load(keys - j);
+      if (j == 0 || j < near_sinks) {
+        const int64_t x = x0 + j, cut = axis.sinks - x;
+        const int64_t r = cut > 0 ? x : x + axis.jump;
+        const int until = cut > 0 && cut < BN ? (int)cut : BN;
+        sk.load_at((const T*)a.k + kh * a.ks[1] + k0 * a.ks[0], r, keys - j, until, axis.jump * sk.row_stride);
+        sv.load_at((const T*)a.v + kh * a.vs[1] + k0 * a.vs[0], r, keys - j, until, axis.jump * sv.row_stride);
+        return key_ok(j);
+      }
     }
+    sk.load(keys - j);
+    sv.load(keys - j);
     return key_ok(j);
   };
   int next_ok = fetch(0);
@@ -97,7 +106,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
     int64_t qi;
     int head;
-    split_row(r < rows ? r : 0, a.group, qi, head);
+    split_row(r < rows ? r : WIN ? rows - 1 : 0, a.group, qi, head);
+    if constexpr (WIN) see[n] = tile_sees.row((int)(qi - i0));
     qi += q0;
     head += kh * a.group;
     const int64_t at = qi * a.heads + head;
@@ -117,12 +127,6 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
     delta[n] += __shfl_xor(delta[n], 32, 64);
     if (row[n] >= 0 && h == 0 && split == 0) a.delta[row[n]] = delta[n];
     lse[n] = lse_base2(row[n] >= 0 ? a.lse_in[row[n]] : -INFINITY);
-    if constexpr (WIN) {
-      int64_t i;
-      split_row(r < rows ? r : rows - 1, a.group, i, head);
-      see[n] = window_row(a.win, axis, i, lq, lk);
-      see[n].first -= (int)x0, see[n].low -= (int)x0, see[n].high -= (int)x0;
-    }
   }
   WindowWave wave_sees;
   if constexpr (WIN) wave_sees.start(see[0], see[NQ - 1]);
@@ -135,10 +139,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 
   int buf = 0;
   for (int j = 0; j < keys; j += BN, buf ^= 1) {
-    const uint64_t bits = __ballot(next_ok != 0);
-    if (a.mask) {
+    const uint64_t bits = WIN == 1 ? kAll : __ballot(next_ok != 0);
+    if (WIN != 1 && a.mask) {
       sk.template store<LD, PS>(s_k(buf), bits);
       sv.template store<LD, PS>(s_v(buf), bits);
+      if (WIN == 2 && wave == 0 && lane < BN) s_bias[buf][lane] = next_ok ? 0.f : -INFINITY;
     } else {
       sk.template store<LD, PS>(s_k(buf));
       sv.template store<LD, PS>(s_v(buf));
@@ -150,7 +155,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
       if (WIN && wave_sees.none(j + 32 * t, 32)) continue;
       f32x16 s[NQ], dp[NQ];
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) s[n] = zero16(), dp[n] = zero16();
+      for (int n = 0; n < NQ; ++n) {
+        s[n] = WIN == 2 ? n ? s[0] : from_bias(s_bias[buf] + 32 * t) : zero16();
+        dp[n] = zero16();
+      }
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
         const int at = (t * 32 + (lane & 31)) * LD + kk * 16 + h * 8;
@@ -166,13 +174,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], c, -lse[n])) * (dp[n][i] - delta[n]);
-      if (WIN && !(bits == kAll && wave_sees.all(j + 32 * t, 32))) {
+      if (WIN && !wave_sees.all(j + 32 * t, 32)) {
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          const uint32_t w = (uint32_t)((bits & window_bits(see[n], j)) >> (32 * t)) >> (4 * h);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[n][i] = w & (1u << (8 * (i >> 2) + (i & 3))) ? s[n][i] : 0.f;
-        }
+        for (int n = 0; n < NQ; ++n) clear_unseen(s[n], see[n], wave_sees, j + 32 * t, 0.f);
       } else if (!WIN && bits != kAll) {
         const uint32_t w = (uint32_t)(bits >> (32 * t)) >> (4 * h);
 #pragma unroll
@@ -214,7 +218,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   }
 }
 
-// dk and dv: four waves of 32 NK keys each over tiles of BQ query rows of the sequence. bf16 data: ds in two parts for the
+// dk and dv: NW waves of 32 NK keys each over tiles of BQ query rows of the sequence. bf16 data: ds in two parts for the
 // product with q, as for dq, since its terms cancel too: rounded once, dk is off by 1.40 to 1.46 times what its own rounding
 // to bf16 costs (30 to 1,500 keys a sequence, 256 queries, heads of 64, rms against 64 bits), in two parts by 1.00. The
 // second product costs 4 to 12% of the backward pass over 300 to 1,500 keys (60,000 queries on 1,500 keys, heads of 128 and of
@@ -226,14 +230,14 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 // WIN: the workgroup of a key tile walks the rows whose windows hold any of its keys. Sinks among its keys are seen by all later
 // rows too: those are walked by far_parts workgroups of their own for each tile with sinks (the launch's first), so that none walks
 // a whole sequence alone, and k_attn_sinks adds up.
-template <typename T, int DP, int NK, int BQ, int WPE, bool VEC, bool WIN>
-__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
+template <typename T, int DP, int NK, int BQ, int WPE, bool VEC, int WIN, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int LD = lds_ld<DP>(), PS = BQ * LD;
-  constexpr int BM = 128 * NK;
+  constexpr int NT = 64 * NW, BM = 32 * NK * NW;
   constexpr int QT = BQ / 32, DT = DP / 32;
   constexpr int TILE = kParts<T> * PS;
-  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE)];
+  __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE, NW)];
   auto s_q = [&](int buf) { return (bf16_t*)s_mem + buf * TILE; };
   auto s_o = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];  // s_delta: -delta
@@ -277,7 +281,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
   }
   // Query rows step through the heads of the group before the next query.
   const int n_rows = (int)(r1 - r0);
-  Stage<T, BQ, DP, kNT, VEC> sq, so;
+  Stage<T, BQ, DP, NT, VEC> sq, so;
   float n_lse = 0.f, n_delta = 0.f;  // as loaded: worked on a tile later (with ds rounded once 223 and 211 us)
   auto fetch = [&](int t0) {
     sq.load(n_rows - t0);
@@ -380,14 +384,14 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
           dp[n] = mma(fo, fv[n][kk], dp[n]);
         }
       }
-      if (WIN && !(all_from <= r32 && all_to >= r32 + 32)) {
-        // Scores of rows that do not see the key would not be below their lse: minus infinity, so that p is 0.
+      // Scores of rows that do not see the key need not be below their lse: minus infinity, so that p is 0.
+      if (WIN && all_from > r32) {
 #pragma unroll
-        for (int n = 0; n < NK; ++n) {
-          const uint32_t w = (uint32_t)(low_bits(to[n] - r32) & ~low_bits(from[n] - r32)) >> (4 * h);
+        for (int n = 0; n < NK; ++n) clear_before(s[n], from[n] - r32, -INFINITY);
+      }
+      if (WIN && all_to < r32 + 32) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[n][i] = w & (1u << (8 * (i >> 2) + (i & 3))) ? s[n][i] : -INFINITY;
-        }
+        for (int n = 0; n < NK; ++n) clear_behind(s[n], to[n] - r32, -INFINITY);
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -463,13 +467,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(WPE))) void
 
 // out[e] = sum over splits of part[split][e] in a fixed order, over the rows (of `width` values) that the sequences of
 // `off` cover: eight groups of threads take every eighth part, and
-// their sums are added in order. Two results of n values each (blockIdx.y). With one thread for all parts of an
+// their sums are added in order (up to eight parts: one thread takes them all, to the same bits). Two results of n values each (blockIdx.y). With one thread for all parts of an
 // element, 128 parts of 77 keys x 256 channels took 31 us.
-template <typename T, int V>
+template <typename T, int V, int G>
 __global__ __launch_bounds__(kNT) void k_attn_sum(const float* __restrict__ part0, const float* __restrict__ part1,
                                                   int splits, const int32_t* __restrict__ off, int batch, int64_t rows,
                                                   int64_t width, T* __restrict__ out0, T* __restrict__ out1) {
-  constexpr int G = 8, EL = kNT / G;
+  constexpr int EL = kNT / G;
   __shared__ float s_sum[G][EL][V];
   const float* part = blockIdx.y ? part1 : part0;
   T* out = blockIdx.y ? out1 : out0;
@@ -543,12 +547,11 @@ template <typename T>
 void sum_go(const float* part0, const float* part1, int splits, const int32_t* off, int batch, int64_t rows, int heads,
             int dim, bool vec, void* out0, void* out1, hipStream_t s) {
   const int64_t width = (int64_t)heads * dim, n = rows * width;
-  const int per = vec && dim % 4 == 0 ? 128 : 32;  // values of a workgroup
+  const int v = vec && dim % 4 == 0 ? 4 : 1, per = v * (splits <= 8 ? kNT : kNT / 8);  // values of a workgroup
   const dim3 grid((unsigned)((n + per - 1) / per), out1 ? 2 : 1);
-  if (per == 128)
-    k_attn_sum<T, 4><<<grid, kNT, 0, s>>>(part0, part1, splits, off, batch, rows, width, (T*)out0, (T*)out1);
-  else
-    k_attn_sum<T, 1><<<grid, kNT, 0, s>>>(part0, part1, splits, off, batch, rows, width, (T*)out0, (T*)out1);
+  auto go = [&](auto kernel) { kernel<<<grid, kNT, 0, s>>>(part0, part1, splits, off, batch, rows, width, (T*)out0, (T*)out1); };
+  if (splits <= 8) go(v == 4 ? k_attn_sum<T, 4, 1> : k_attn_sum<T, 1, 1>);
+  else go(v == 4 ? k_attn_sum<T, 4, 8> : k_attn_sum<T, 1, 8>);
 }
 
 // Tiles of the two kernels: 32 NQ (NK) query rows (keys) of a wave, rows of an LDS tile, waves per SIMD.
@@ -568,16 +571,49 @@ template <int DP>
 struct BwdShape<float, DP> {
   static constexpr int NQ = 1, QWPE = DP <= 64 ? 2 : 1, QB = 32, NK = 1, KWPE = DP <= 32 ? 2 : 1, KB = 32;
 };
+// Window attention: for dq rows, waves per SIMD, keys of a tile and waves of a workgroup, then the same for dk and dv. One tile of rows
+// and three waves per SIMD for dq, since the masks of two spill. us, dq (1, 3, 32, 4) / (2, 2, 32, 4) / (1, 2, 64, 4): 100,003 rows, 512
+// to either side, masked, 4 heads on 2 of 64: 605 / 672 / 622; 100,003 rows, 256 to either side, 4 heads: 388 / 491 / 387. Heads of 32
+// (200,003 rows, 8 heads, 256 to either side): 901, with the shapes without windows 996; of 96 (100,003 rows, 4 heads) 645 and 705.
+// fp32, heads of 32, two waves / four waves: 50,003 rows, 4 heads, 256 to either side 358 / 359, 7,131 rows, 2 heads, 64: 44 / 54.
+template <int Q, int QE, int QN, int QW, int K, int KE, int KN, int KW>
+struct Shape {
+  static constexpr int NQ = Q, QWPE = QE, QB = QN, QNW = QW, NK = K, KWPE = KE, KB = KN, KNW = KW;
+};
+template <typename T, int DP>
+struct WinShape : Shape<1, 1, 32, 4, 1, 1, 32, 4> {};
+template <>
+struct WinShape<bf16_t, 32> : Shape<1, 3, 64, 4, 1, 3, 64, 4> {};
+template <>
+struct WinShape<bf16_t, 64> : Shape<1, 3, 32, 4, 1, 2, 64, 4> {};
+template <>
+struct WinShape<bf16_t, 96> : Shape<1, 2, 64, 4, 1, 2, 32, 4> {};
+template <>
+struct WinShape<bf16_t, 128> : Shape<1, 2, 64, 4, 1, 1, 64, 4> {};
+template <>
+struct WinShape<float, 32> : Shape<1, 2, 32, 2, 1, 2, 32, 2> {};
+template <>
+struct WinShape<float, 64> : Shape<1, 2, 32, 4, 1, 1, 32, 4> {};
 struct BwdRows {
   int q, k;
 };
-template <typename T>
-BwdRows bwd_rows_t(int dim) {
-  if (dim <= 32) return {128 * BwdShape<T, 32>::NQ, 128 * BwdShape<T, 32>::NK};
-  if (dim <= 64) return {128 * BwdShape<T, 64>::NQ, 128 * BwdShape<T, 64>::NK};
-  return {128 * BwdShape<T, 128>::NQ, 128 * BwdShape<T, 128>::NK};
+template <typename T, int DP>
+BwdRows rows_of(bool windowed) {
+  typedef BwdShape<T, DP> B;
+  typedef WinShape<T, DP> W;
+  if (windowed) return {32 * W::NQ * W::QNW, 32 * W::NK * W::KNW};
+  return {128 * B::NQ, 128 * B::NK};
 }
-BwdRows bwd_rows(int dtype, int dim) { return dtype == IGC_BF16 ? bwd_rows_t<bf16_t>(dim) : bwd_rows_t<float>(dim); }
+template <typename T>
+BwdRows bwd_rows_t(int dim, bool windowed) {
+  if (dim <= 32) return rows_of<T, 32>(windowed);
+  if (dim <= 64) return rows_of<T, 64>(windowed);
+  if (dim <= 96) return rows_of<T, 96>(windowed);
+  return rows_of<T, 128>(windowed);
+}
+BwdRows bwd_rows(int dtype, int dim, bool windowed) {
+  return dtype == IGC_BF16 ? bwd_rows_t<bf16_t>(dim, windowed) : bwd_rows_t<float>(dim, windowed);
+}
 
 // Key tiles of `bm` that may hold sinks.
 int64_t far_tiles(const AttnArgs& a, bool by_key, int bm) {
@@ -587,6 +623,8 @@ int64_t far_tiles(const AttnArgs& a, bool by_key, int bm) {
 template <typename T, int DP>
 void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
   typedef BwdShape<T, DP> S;
+  typedef WinShape<T, DP> W;
+  const BwdRows tile = rows_of<T, DP>(a.windowed);
   const bool vec = a.qvec && a.kvec && a.ovec;
   a.delta = ws;
   ws += (a.nq * a.heads + 63) / 64 * 64;
@@ -594,13 +632,16 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     AttnArgs d = a;
     d.splits = a.dq ? p.dq_splits : 1;
     d.part_a = ws;
-    const unsigned wgs = (unsigned)((a.nq * a.group / (128 * S::NQ) + a.batch) * a.kv_heads * d.splits);
-    if (a.windowed) {
-      if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true, true><<<wgs, kNT, 0, s>>>(d);
-      else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false, true><<<wgs, kNT, 0, s>>>(d);
+    const unsigned wgs = (unsigned)((a.nq * a.group / tile.q + a.batch) * a.kv_heads * d.splits);
+    if (a.windowed && a.mask) {
+      if (vec) k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, true, 2, W::QNW><<<wgs, 64 * W::QNW, 0, s>>>(d);
+      else k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, false, 2, W::QNW><<<wgs, 64 * W::QNW, 0, s>>>(d);
+    } else if (a.windowed) {
+      if (vec) k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, true, 1, W::QNW><<<wgs, 64 * W::QNW, 0, s>>>(d);
+      else k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, false, 1, W::QNW><<<wgs, 64 * W::QNW, 0, s>>>(d);
     } else {
-      if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true, false><<<wgs, kNT, 0, s>>>(d);
-      else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false, false><<<wgs, kNT, 0, s>>>(d);
+      if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true, 0, 4><<<wgs, kNT, 0, s>>>(d);
+      else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false, 0, 4><<<wgs, kNT, 0, s>>>(d);
     }
     if (a.dq && d.splits > 1)
       sum_go<T>(ws, nullptr, d.splits, a.qo, a.batch, a.nq, a.heads, a.dim, a.ovec, a.dq, nullptr, s);
@@ -610,16 +651,16 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     a.splits = p.dkv_splits;
     a.part_a = ws;
     a.part_b = ws + (p.dkv_splits > 1 ? p.dkv_splits * n : 0);
-    const unsigned wgs = (unsigned)((a.nk / (128 * S::NK) + a.batch) * a.kv_heads * a.splits);
+    const unsigned wgs = (unsigned)((a.nk / tile.k + a.batch) * a.kv_heads * a.splits);
     if (a.windowed) {
       a.far_parts = p.far_parts, a.far_by_key = p.far_by_key, a.far_rows = p.far_rows;
       a.far = a.delta + p.far_at;
-      a.far_wgs = (unsigned)(far_tiles(a, p.far_by_key, 128 * S::NK) * a.kv_heads * a.far_parts);
-      if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, true><<<wgs + a.far_wgs, kNT, 0, s>>>(a);
-      else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false, true><<<wgs + a.far_wgs, kNT, 0, s>>>(a);
+      a.far_wgs = (unsigned)(far_tiles(a, p.far_by_key, tile.k) * a.kv_heads * a.far_parts);
+      if (vec) k_attn_dkv<T, DP, W::NK, W::KB, W::KWPE, true, 1, W::KNW><<<wgs + a.far_wgs, 64 * W::KNW, 0, s>>>(a);
+      else k_attn_dkv<T, DP, W::NK, W::KB, W::KWPE, false, 1, W::KNW><<<wgs + a.far_wgs, 64 * W::KNW, 0, s>>>(a);
     } else {
-      if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, false><<<wgs, kNT, 0, s>>>(a);
-      else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false, false><<<wgs, kNT, 0, s>>>(a);
+      if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, 0, 4><<<wgs, kNT, 0, s>>>(a);
+      else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false, 0, 4><<<wgs, kNT, 0, s>>>(a);
     }
     if (a.splits > 1)
       sum_go<T>(a.part_a, a.part_b, a.splits, a.ko, a.batch, a.nk, a.kv_heads, a.dim, a.ovec, a.dk, a.dv, s);
@@ -651,25 +692,25 @@ AttnBwdPlan attn_bwd_plan(int dtype, const AttnArgs& a) {
   const int64_t nq = a.nq, nk = a.nk;
   const int batch = a.batch, heads = a.heads, kv_heads = a.kv_heads, dim = a.dim;
   AttnBwdPlan p;
-  const BwdRows t = bwd_rows(dtype, dim);
+  const BwdRows t = bwd_rows(dtype, dim, a.windowed);
   const int64_t rows = (nq + batch - 1) / batch * (heads / kv_heads), keys = (nk + batch - 1) / batch;
   int64_t seen_keys = keys, seen_rows = rows;  // that a tile walks
   if (a.windowed && a.win.left >= 0 && a.win.right >= 0) {
     seen_keys = std::min<int64_t>(keys, a.win.left + a.win.right + t.q / a.group + a.win.sinks);
     seen_rows = std::min<int64_t>(rows, (a.win.left + a.win.right + t.k) * a.group);
   }
-  p.dq_splits = parts(batch * ((rows + t.q - 1) / t.q) * kv_heads, seen_keys, 256);
-  p.dkv_splits = parts(batch * ((keys + t.k - 1) / t.k) * kv_heads, seen_rows, 64);
+  p.dq_splits = parts(batch * ((rows + t.q - 1) / t.q) * kv_heads, seen_keys, a.windowed ? kWindowPart : 256);
+  p.dkv_splits = parts(batch * ((keys + t.k - 1) / t.k) * kv_heads, seen_rows, a.windowed ? kWindowPart : 64);
   const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * nq * heads * dim : 0;
   const size_t dkv = p.dkv_splits > 1 ? (size_t)2 * p.dkv_splits * nk * kv_heads * dim : 0;
   // The two kernels run one after the other, so their partial results share the space.
   p.floats = (size_t)(nq * heads + 63) / 64 * 64 + std::max(dq, dkv);
   if (a.windowed && a.win.sinks > 0 && nk > 0) {
-    // Rows behind the window of a tile with sinks: parts about as long as the rows that other tiles walk, while they are few.
+    // Rows behind the window of a tile with sinks: parts about as long as what the others walk, while they are few.
     p.far_by_key = (int64_t)batch * a.win.sinks >= nk;
     p.far_rows = p.far_by_key ? nk : (int64_t)batch * a.win.sinks;
     const int64_t tiles = far_tiles(a, p.far_by_key, t.k) * kv_heads;
-    p.far_parts = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, 1024 / tiles), rows / std::max<int64_t>(512, seen_rows)));
+    p.far_parts = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, 1024 / tiles), rows * p.dkv_splits / std::max<int64_t>(128, seen_rows)));
     p.far_at = (p.floats + 3) / 4 * 4;
     p.floats = p.far_at + (size_t)2 * (1 + p.far_parts) * p.far_rows * kv_heads * dim;
   }

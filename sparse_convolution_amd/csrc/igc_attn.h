@@ -241,7 +241,7 @@ struct Stage {
     }
   }
   // Loads the tile of rows r, r + 1, ... of the sequence (keys only: group 1) without stepping: rows from `have` on are
-  // zero, rows from `cut` on lie `jump` bytes further.
+  // zero, rows from `cut` on lie `jump` bytes further. load() goes on behind it, if cut is not within the tile.
   __device__ __forceinline__ void load_at(const T* first, int64_t r0, int have, int cut, int64_t jump) {
     base = (const char*)first + r0 * row_stride;
     if (VEC && have >= ROWS && cut >= ROWS && dim == DP && (ROWS * CG) % NT == 0) {
@@ -252,6 +252,7 @@ struct Stage {
       for (int i = 0; i < N; ++i)
         r[i] = load8<T>((const T*)(base + off[i] + (row(i) >= cut ? jump : 0)), mine(i) && row(i) < have ? dim - col(i) : 0, VEC);
     }
+    base += ROWS * row_stride;
   }
   // Loads the tile and steps to the next one. Rows from `have` on are zero.
   __device__ __forceinline__ void load(int have) {
@@ -318,15 +319,49 @@ struct WindowWave {
   __device__ __forceinline__ bool all(int j, int n) const { return (last.low <= j && first.high >= j + n) || first.first >= j + n; }
   __device__ __forceinline__ bool none(int j, int n) const { return last.first <= j && (last.high <= j || first.low >= j + n); }
 };
-// Which of the places j .. j + 63 a row sees.
-__device__ __forceinline__ uint64_t window_bits(const WindowRow& r, int j) {
-  return low_bits(r.first - j) | (low_bits(r.high - j) & ~low_bits(r.low - j));
+// Clears (sets to `none`) the entries of a 32 x 32 tile whose row is before low, or at or behind high: one comparison and one
+// select each.
+__device__ __forceinline__ void clear_before(f32x16& s, int low, float none) {
+  const int at = low - 4 * (lane_id() >> 5);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s[r] = 8 * (r >> 2) + (r & 3) >= at ? s[r] : none;
+}
+__device__ __forceinline__ void clear_behind(f32x16& s, int high, float none) {
+  const int at = high - 4 * (lane_id() >> 5);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) s[r] = 8 * (r >> 2) + (r & 3) < at ? s[r] : none;
+}
+// Clears the entries (rows: places j .. j + 31, columns: window rows) that a row does not see, where the wave has any.
+__device__ __forceinline__ void clear_unseen(f32x16& s, const WindowRow& see, const WindowWave& wave, int j, float none) {
+  if (wave.last.first > j) {  // sinks among the places: seen before `first` too
+    const int at = 4 * (lane_id() >> 5) + j;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int x = 8 * (r >> 2) + (r & 3) + at;
+      s[r] = x < see.first || (x >= see.low && x < see.high) ? s[r] : none;
+    }
+    return;
+  }
+  if (wave.last.low > j) clear_before(s, see.low - j, none);
+  if (wave.first.high < j + 32) clear_behind(s, see.high - j, none);
+}
+// A 32 x 32 tile of scores whose rows are keys: starts from the keys' biases (0, or -infinity for a key that the mask
+// leaves out), so that masked scores cost no instruction each.
+__device__ __forceinline__ f32x16 from_bias(const float* bias) {
+  f32x16 s;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const f32x4v x = *(const f32x4v*)(bias + 8 * g + 4 * (lane_id() >> 5));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[4 * g + i] = x[i];
+  }
+  return s;
 }
 
-// LDS bytes a workgroup of four waves needs for its tiles (values of bf16) and for store_tile.
+// LDS bytes a workgroup needs for its tiles (values of bf16) and for store_tile.
 template <typename T, int DP>
-constexpr int lds_bytes(int tile_values) {
-  const int out = 4 * 32 * (DP + 4) * 4;  // fp32 results: the larger form
+constexpr int lds_bytes(int tile_values, int waves = 4) {
+  const int out = waves * 32 * (DP + 4) * 4;  // fp32 results: the larger form
   return tile_values * 2 > out ? tile_values * 2 : out;
 }
 

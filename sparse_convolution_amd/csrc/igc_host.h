@@ -284,6 +284,8 @@ constexpr int32_t kAttnMaxDim = 128;
 // Keys, and query rows (queries times the heads that share a key head), of a problem at most: the kernels count those of a
 // sequence in 32 bits and step up to 256 past its end.
 constexpr int64_t kAttnMaxRows = INT32_MAX - 1023;
+// Keys, or query rows, of a part of a split axis at least, for window attention's tiles.
+constexpr int64_t kWindowPart = 384;
 // Parts the key axis is split into; where there is more than one, the forward workspace holds dim partial results and two
 // statistics for each part, query and head.
 int attn_fwd_splits(int dtype, const AttnArgs& a);

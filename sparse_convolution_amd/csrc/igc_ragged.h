@@ -53,9 +53,16 @@ __host__ __device__ __forceinline__ void split_row(int64_t r, int group, int64_t
   g = (int)(x - q * (uint32_t)group);
 }
 
-// Part `part` of `parts` of an axis of n places, [begin, end): all but the last a multiple of `step` long.
+// Query of row r of a sequence.
+__host__ __device__ __forceinline__ int64_t row_query(int64_t r, int group) {
+  return group == 1 ? r : (uint32_t)r / (uint32_t)group;
+}
+
+// Part `part` of `parts` of an axis of n places (below 2^31 - 1024), [begin, end): all but the last a multiple of `step` long.
 __host__ __device__ __forceinline__ void split_axis(int64_t n, int parts, int part, int step, int64_t& begin, int64_t& end) {
-  const int64_t each = ((n + parts - 1) / parts + step - 1) / step * step;
+  begin = 0, end = n;
+  if (parts == 1) return;
+  const int64_t each = ((uint32_t)(n + parts - 1) / (uint32_t)parts + step - 1) / step * step;
   begin = part * each < n ? part * each : n;
   end = begin + each < n ? begin + each : n;
 }
@@ -83,19 +90,30 @@ __host__ __device__ __forceinline__ WindowAxis window_axis(const Window& w, int6
   return a;
 }
 
-// The places that query i sees on that axis: those before `first` and those of [low, high).
+// The places that a query sees on that axis, counted from place x0: those before `first` and those of [low, high).
 struct WindowRow {
   int32_t first, low, high;
 };
-__host__ __device__ __forceinline__ WindowRow window_row(const Window& w, const WindowAxis& a, int64_t i, int64_t lq, int64_t lk) {
-  const int64_t p = i + lk - lq;
-  const int64_t high = w.right < 0 ? lk : clamp64(p + w.right + 1, 0, lk);
-  const int64_t low = w.left < 0 ? 0 : clamp64(p - w.left, 0, lk);
-  WindowRow r;
-  r.first = (int32_t)(w.sinks < high ? w.sinks : high);
-  r.low = (int32_t)clamp64(low - a.jump, 0, lk);
-  r.high = (int32_t)clamp64(high - a.jump, 0, lk);
-  return r;
+// The same for query i0 + i of a tile (i < 1024) in 32 bits: what leads far outside of the axis saturates.
+struct WindowTile {
+  int32_t sinks, low, high, end;
+  __host__ __device__ __forceinline__ WindowRow row(int32_t i) const {
+    WindowRow r;
+    r.low = low + i;
+    r.high = high + i < end ? high + i : end;
+    r.first = sinks < r.high ? sinks : r.high;  // places before the jump: the row's window never ends there
+    return r;
+  }
+};
+__host__ __device__ __forceinline__ WindowTile window_tile(const Window& w, const WindowAxis& a, int64_t x0, int64_t i0, int64_t lq,
+                                                           int64_t lk) {
+  const int64_t p = i0 + lk - lq - a.jump - x0, far = INT32_MAX - 1023;
+  WindowTile t;
+  t.sinks = (int32_t)clamp64(w.sinks - x0, -far, far);
+  t.low = (int32_t)(w.left < 0 ? -far : clamp64(p - w.left, -far, far));
+  t.high = (int32_t)(w.right < 0 ? far : clamp64(p + w.right + 1, -far, far));
+  t.end = (int32_t)(a.keys - x0);
+  return t;
 }
 
 // The queries [begin, end) that see key j; `window`: of a sink, only those whose window holds it too.
@@ -103,11 +121,6 @@ __host__ __device__ __forceinline__ void window_queries(const Window& w, int64_t
                                                         int64_t& begin, int64_t& end) {
   begin = w.right < 0 ? 0 : clamp64(j - w.right - (lk - lq), 0, lq);
   end = w.left < 0 || (!window && j < w.sinks) ? lq : clamp64(j + w.left + 1 - (lk - lq), begin, lq);
-}
-
-// The lowest n of 64 bits.
-__host__ __device__ __forceinline__ uint64_t low_bits(int32_t n) {
-  return n <= 0 ? 0 : n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1;
 }
 
 }  // namespace igc

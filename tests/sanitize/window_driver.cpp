@@ -37,11 +37,10 @@ static int walk(const Window& w, int64_t lq, int64_t lk, int bm, int bn, int par
         const int64_t j = a.key(x);
         if (j < 0 || j >= lk || met[(size_t)j]++) return fail(w, lq, lk, x, "a place leads nowhere or to a key met before");
         for (int64_t i = i0; i <= i1; ++i) {
-          WindowRow r = window_row(w, a, i, lq, lk);
-          r.first -= (int32_t)x0, r.low -= (int32_t)x0, r.high -= (int32_t)x0;
-          const int32_t tile = (int32_t)((x - x0) / bn * bn);
-          const uint64_t bits = low_bits(r.first - tile) | (low_bits(r.high - tile) & ~low_bits(r.low - tile));
-          if ((bits >> (x - x0 - tile) & 1) != sees(w, i, j, lq, lk)) return fail(w, lq, lk, i, "a row's places are not its keys");
+          const WindowRow r = window_tile(w, a, x0, i0, lq, lk).row((int32_t)(i - i0));
+          const int32_t at = (int32_t)(x - x0);
+          if ((at < r.first || (at >= r.low && at < r.high)) != sees(w, i, j, lq, lk))
+            return fail(w, lq, lk, i, "a row's places are not its keys");
         }
       }
     }
@@ -96,10 +95,13 @@ int main() {
       for (int64_t right : {(int64_t)-1, (int64_t)0, (int64_t)INT32_MAX}) {
         const Window w = {left, right, left < 0 ? 0 : 7};
         const WindowAxis a = window_axis(w, i, i, big, big);
-        const WindowRow r = window_row(w, a, i, big, big);
+        const WindowRow r = window_tile(w, a, 0, i, big, big).row(0);
         int64_t from, to;
         window_queries(w, i, big, big, false, from, to);
-        if (a.keys < 0 || a.keys > big || r.low < 0 || r.high < 0 || from > i || to <= i) bad += fail(w, big, big, i, "far rows");
+        if (a.keys < 0 || a.keys > big || r.high < 0 || r.high <= r.low || from > i || to <= i) bad += fail(w, big, big, i, "far rows");
+        // The row's own key is on the axis where the formula puts it.
+        const int64_t x = i - a.jump;
+        if (a.key(x) != i || !(x < r.first || (x >= r.low && x < r.high))) bad += fail(w, big, big, i, "the key of a far row");
       }
   if (bad) return 1;
   std::puts("window driver: ok");
