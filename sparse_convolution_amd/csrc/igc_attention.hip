@@ -54,7 +54,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   const int kh = blockIdx.x % a.kv_heads;
   const int split = (blockIdx.x / a.kv_heads) % a.splits;
   int b;
-  const int64_t tile = find_tile(a.qo, a.batch, a.nq, a.group, BM, blockIdx.x / (a.kv_heads * a.splits), b);
+  const int64_t tile = tile_of<WIN != 0>(a.qo, a.batch, a.nq, a.group, BM, blockIdx.x / (a.kv_heads * a.splits), b);
   int64_t q0, q1, k0, k1;
   seq_rows(a.qo, b, a.nq, q0, q1);
   seq_rows(a.ko, b, a.nk, k0, k1);
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
   const int kh = blockIdx.x % a.kv_heads;
   const int split = (blockIdx.x / a.kv_heads) % a.splits;
   int b;
-  const int64_t tile = find_tile(a.qo, a.batch, a.nq, a.group, R, blockIdx.x / (a.kv_heads * a.splits), b);
+  const int64_t tile = tile_of<WIN != 0>(a.qo, a.batch, a.nq, a.group, R, blockIdx.x / (a.kv_heads * a.splits), b);
   int64_t q0, q1, k0, k1;
   seq_rows(a.qo, b, a.nq, q0, q1);
   seq_rows(a.ko, b, a.nk, k0, k1);
@@ -437,8 +437,8 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
 }
 
 constexpr int kMaxParts = 128;
-// Rows from which on a wave joins each (k_attn_join_rows) instead of a workgroup: 18,002 rows of 2 parts 8 us instead of 18, 512
-// rows of 4 parts 0.5 us slower.
+// Rows from which on a wave joins each (k_attn_join_rows), if it has up to eight parts, instead of a workgroup: 18,002 rows of 2
+// parts 8 us instead of 18; 512 rows of 4 parts 0.5 us slower, 2,400 rows of 32 parts 4.
 constexpr int64_t kJoinRows = 1024;
 
 // Joins the parts of a split key axis, one workgroup per row of a sequence: a lane per part weighs it, then the waves
@@ -609,7 +609,7 @@ template <typename T>
 void join(const AttnArgs& a, hipStream_t s) {
   if (a.splits == 1) return;
   const int64_t rows = a.nq * a.heads;
-  if (rows > kJoinRows) k_attn_join_rows<T><<<(unsigned)((rows + kNT / 64 - 1) / (kNT / 64)), kNT, 0, s>>>(a);
+  if (rows > kJoinRows && a.splits <= 8) k_attn_join_rows<T><<<(unsigned)((rows + kNT / 64 - 1) / (kNT / 64)), kNT, 0, s>>>(a);
   else k_attn_join<T><<<(unsigned)rows, kNT, 0, s>>>(a);
 }
 
@@ -685,6 +685,9 @@ int attn_fwd_splits(int dtype, const AttnArgs& a) {
   int64_t keys = nk / batch;  // that a tile walks
   if (a.windowed && a.win.left >= 0 && a.win.right >= 0)
     keys = std::min<int64_t>(keys, a.win.left + a.win.right + bm / a.group + a.win.sinks);
+  // Single tokens: a workgroup on every CU reads up to 2,048 keys each sooner than parts of them are joined. 64 queries, 8 heads on 4
+  // of 64, bf16, us whole / in parts for 2,048 workgroups: 1,028 keys 27 / 37, 3,005 keys 59 / 50.
+  if (a.windowed && bm <= kFewRows && wgs >= 256 && keys <= 2048) return 1;
   // Rows of windows are many, and so is what their parts leave to be joined. Parts of at least 256 / 384 / 1,024 keys, us: 9,001
   // rows of 2 sequences, 2 heads of 64, bf16, 511 keys before: 26 / 19 / 19; 4,000 rows, 1,999 before: 27 / 26 / 32.
   const int64_t least = a.windowed && bm > kFewRows ? kWindowPart : 256;

@@ -47,7 +47,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   const int kh = blockIdx.x % a.kv_heads;
   const int split = (blockIdx.x / a.kv_heads) % a.splits;
   int b;
-  const int64_t tile = find_tile(a.qo, a.batch, a.nq, a.group, BM, blockIdx.x / (a.kv_heads * a.splits), b);
+  const int64_t tile = tile_of<WIN != 0>(a.qo, a.batch, a.nq, a.group, BM, blockIdx.x / (a.kv_heads * a.splits), b);
   int64_t q0, q1, k0, k1;
   seq_rows(a.qo, b, a.nq, q0, q1);
   seq_rows(a.ko, b, a.nk, k0, k1);
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
     b = (int)(tile / tiles);
     tile %= tiles;
   } else {
-    tile = find_tile(a.ko, a.batch, a.nk, 1, BM, tile, b);
+    tile = tile_of<WIN != 0>(a.ko, a.batch, a.nk, 1, BM, tile, b);
   }
   int64_t q0, q1, k0, k1;
   seq_rows(a.qo, b, a.nq, q0, q1);

@@ -139,6 +139,25 @@ __device__ __forceinline__ Frag<T> load_tr(const bf16_t* s, int row0, int col0) 
   return f;
 }
 
+// find_tile; for windows by all 64 lanes: one round of loads for up to 64 sequences, where halving takes six (one query for each of 64 sequences,
+// 3,005 keys: 47 us instead of 50). For ascending offsets the same sequence.
+template <bool WIN>
+__device__ __forceinline__ int64_t tile_of(const int32_t* off, int batch, int64_t n, int mul, int bm, int64_t slot, int& b) {
+  if constexpr (!WIN) return find_tile(off, batch, n, mul, bm, slot, b);
+  b = 0;
+  if (!off) return slot;
+  const int64_t first = clamp64(off[0], 0, n);
+  int hi = batch;  // slots of hi and beyond start after `slot`
+  while (hi - b > 1) {
+    const int step = (hi - b + 63) >> 6, at = b + lane_id() * step;
+    const bool before = at == b || (at < hi && (clamp64(off[at], 0, n) - first) * mul / bm + at <= slot);
+    const uint64_t found = __ballot(before);
+    b += step * (63 - __builtin_clzll(found));
+    hi = b + step < hi ? b + step : hi;
+  }
+  return slot - ((clamp64(off[b], 0, n) - first) * mul / bm + b);
+}
+
 // x - part[i] in one instruction, a dot product with (-1, 0) or (0, -1); exact where part[i] is x rounded to bf16. An
 // infinite neighbour makes it NaN, so the neighbours have to belong to the same sum. The pair comes from a register: as an
 // inline constant, which the compiler would take for (-1, 0), the instruction reads -1 into the other half.
