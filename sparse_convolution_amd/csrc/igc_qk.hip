@@ -5,8 +5,12 @@
 //   y1 = amplitude (z1 cos - z2 sin), y2 = amplitude (z2 cos + z1 sin); channels behind the pairs: y = z
 //   backward: g = the transposed rotation of dy, h = g w, dx = rstd (h - xhat mean(h xhat)), dw = sum of g xhat, xhat = x rstd
 //
-// A row's cosines and sines are computed once for all of its heads: the workgroup's rows first make a table in LDS, then
-// the LPR lanes of a row keep what their channels need of it and walk the heads, V channels a load.
+// A row's cosines and sines are computed once for all of its heads: the LPR lanes of a row first make a table in LDS, then
+// keep what their channels need of it and walk the heads, V channels a load, with the loads of the next heads in flight.
+//
+// Memory bound, each array moved once (a copy of 4 GiB reaches 4.8 TB/s); the vector unit is busy for 60% of the time with bf16
+// data. 1,000,003 rows of 4 + 4 heads of 64 by voxel coordinates, bf16: 393 us, 5.2 TB/s; gradients 602 us, 5.1 TB/s. Rotation alone of
+// 500,003 rows of 4 heads of 48, fp32: 144 us, 5.4 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -39,30 +43,33 @@ __device__ __forceinline__ float2 cos_sin(int32_t position, float frequency) {
   return make_float2(q == 1 || q == 2 ? -u : u, q >= 2 ? -v : v);
 }
 
-// What a lane holds of a head: NV times V channels.
+// What a lane holds of a head: NV times V channels. The LPR lanes of a row, and with them its table, lie in one wave.
 template <typename T, int V, int LPR, int NV>
 struct Head {
   static constexpr int SL = kNT / LPR;       // rows of a workgroup
+  static constexpr int WS = 64 / LPR;        // and of a wave
   static constexpr int DP = LPR * NV * V;    // channels that the lanes could hold
-  // Rows of the table: cosines and sines of a row's pairs.
-  static constexpr int kTable = SL * (DP / 2 > 0 ? DP / 2 : 1);
+  static constexpr int kPairs = DP / 2 > 0 ? DP / 2 : 1;
+  typedef typename VecOf<T, V>::type Raw;
 
-  static __device__ __forceinline__ int channel(int j, int i) { return (j * LPR + (int)threadIdx.x % LPR) * V + i; }
+  static __device__ __forceinline__ int lane_in() { return (int)threadIdx.x % LPR; }
+  static __device__ __forceinline__ int channel(int j, int i) { return (j * LPR + lane_in()) * V + i; }
 
-  // Table of the workgroup's rows from r0 on.
-  static __device__ __forceinline__ void fill(const QkArgs& a, int64_t r0, float2* s_table) {
+  // Cosines and sines of row r's pairs: each lane of the row makes every LPR-th.
+  static __device__ __forceinline__ void fill(const QkArgs& a, int64_t r, bool live, float2* s_table) {
     const int pairs = a.axes * a.pairs;
-    for (int e = threadIdx.x; e < SL * pairs; e += kNT) {
-      const int slot = e / pairs, p = e % pairs;
-      const int64_t r = r0 + slot;
-      if (r >= a.n) break;
-      float2 t = cos_sin(a.positions[r * a.axes + p / a.pairs], a.frequencies[p]);
-      s_table[e] = make_float2(t.x * a.amplitude, t.y * a.amplitude);
-    }
+    float2* const mine = s_table + lane_id() / LPR * kPairs;
+    if (live)
+      for (int p = lane_in(); p < pairs; p += LPR) {
+        const int axis = (p >= a.pairs) + (p >= 2 * a.pairs);
+        const float2 t = cos_sin(a.positions[r * a.axes + axis], a.frequencies[p]);
+        mine[p] = make_float2(t.x * a.amplitude, t.y * a.amplitude);
+      }
   }
   // This lane's factors: y[c] = z[c] co[c] + z[partner of c] si[c].
   static __device__ __forceinline__ void factors(const QkArgs& a, const float2* s_table, float (&co)[NV][V], float (&si)[NV][V]) {
-    const int pairs = a.axes * a.pairs, slot = threadIdx.x / LPR;
+    const int pairs = a.axes * a.pairs;
+    const float2* const mine = s_table + lane_id() / LPR * kPairs;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -71,131 +78,168 @@ struct Head {
         co[j][i] = 1.f, si[j][i] = 0.f;
         if (ch < 2 * pairs) {
           const bool second = a.interleaved ? ch & 1 : ch >= pairs;
-          const float2 t = s_table[slot * pairs + (a.interleaved ? ch >> 1 : second ? ch - pairs : ch)];
+          const float2 t = mine[a.interleaved ? ch >> 1 : second ? ch - pairs : ch];
           co[j][i] = t.x;
           si[j][i] = second ? t.y : -t.y;
         }
       }
   }
-  // The partners' values of v; 0 for channels behind the pairs, whose own may be infinite. Channel c of a slot lies at (c % V) * 64 + its lane in the wave's part of LDS, so that neither
-  // the writes nor the reads, whose channels lie a fixed distance apart, meet in a bank.
-  static __device__ __forceinline__ void partners(const QkArgs& a, float* s_x, const float (&v)[NV][V], float (&o)[NV][V]) {
-    const int pairs = a.axes * a.pairs;
-    if (V % 2 == 0 && a.interleaved) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[j][i] = channel(j, i) < 2 * pairs ? v[j][i ^ 1] : 0.f;
-      return;
-    }
-    const int lane = lane_id(), first = lane / LPR * LPR;
-    wave_sync();  // the last values have been read
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) s_x[(j * V + i) * 64 + lane] = v[j][i];
-    wave_sync();
+  // Where the partners of this lane's channels lie in the wave's exchange (see partners); channels behind the pairs read its last
+  // place, which holds 0.
+  static constexpr int kExchange = NV * V * 64 + 1;
+  static __device__ __forceinline__ void places(const QkArgs& a, float* s_x, int (&at)[NV][V]) {
+    s_x[kExchange - 1] = 0.f;
+    const int pairs = a.axes * a.pairs, first = lane_id() / LPR * LPR;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int ch = channel(j, i);
-        const bool turns = ch < 2 * pairs;
-        const int to = !turns ? ch : a.interleaved ? ch ^ 1 : ch < pairs ? ch + pairs : ch - pairs;
-        const int group = to / V;
-        const float x = s_x[(group / LPR * V + to % V) * 64 + first + group % LPR];
-        o[j][i] = turns ? x : 0.f;
+        const int ch = channel(j, i), to = a.interleaved ? ch ^ 1 : ch < pairs ? ch + pairs : ch - pairs, group = to / V;
+        at[j][i] = ch < 2 * pairs ? (group / LPR * V + to % V) * 64 + first + group % LPR : kExchange - 1;
       }
   }
-  static __device__ __forceinline__ void load(const T* p, int dim, bool live, float (&v)[NV][V]) {
+  // The partners' values of v; 0 for channels behind the pairs, whose own may be infinite. Channel c of a row lies at (c % V) * 64 +
+  // its lane in the wave's part of LDS, so that neither the writes nor the reads, whose channels lie a fixed distance apart, meet
+  // in a bank.
+  static __device__ __forceinline__ void partners(const QkArgs& a, float* s_x, const int (&at)[NV][V], const float (&v)[NV][V],
+                                                  float (&o)[NV][V]) {
+    if (V % 2 == 0 && a.interleaved) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[j][i] = at[j][i] < kExchange - 1 ? v[j][i ^ 1] : 0.f;
+      return;
+    }
+    wave_sync();  // the last values have been read
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_x[(j * V + i) * 64 + lane_id()] = v[j][i];
+    wave_sync();
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[j][i] = s_x[at[j][i]];
+  }
+  // p: the head's values from this lane's first channel on.
+  static __device__ __forceinline__ void load(const T* p, int dim, bool live, Raw (&v)[NV]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int ch = channel(j, 0);
-      if (live && ch < dim) {
-        load_vec<T, V>(p + ch, *(float(*)[V])&v[j]);
+      v[j] = Raw{};
+      if (live && channel(j, 0) < dim) v[j] = *(const Raw*)(p + j * LPR * V);
+    }
+  }
+  static __device__ __forceinline__ void floats(const Raw (&r)[NV], float (&v)[NV][V]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (V == 1) {
+        v[j][0] = (float)r[j];
       } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[j][i] = 0.f;
+        for (int i = 0; i < V; ++i) v[j][i] = (float)r[j][i];
       }
     }
   }
   static __device__ __forceinline__ void store(T* p, int dim, bool live, const float (&v)[NV][V]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int ch = channel(j, 0);
-      if (live && ch < dim) store_vec<T, V>(p + ch, v[j]);
+      if (live && channel(j, 0) < dim) store_vec<T, V>(p + j * LPR * V, v[j]);
     }
   }
-  static __device__ __forceinline__ void weights(const void* w, int f32, int dim, float (&v)[NV][V]) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int ch = channel(j, 0);
-      if (ch < dim) {
-        load_params<V>(w, ch, f32, 1.f, v[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[j][i] = 0.f;
-      }
+  // The weights of queries and keys, 0 behind the head, kept in LDS: a head's are read where its turn comes.
+  static __device__ __forceinline__ void keep_weights(const QkArgs& a, float (*s_w)[DP]) {
+    for (int e = threadIdx.x; e < 2 * DP; e += kNT) {
+      const void* w = a.w[e / DP];
+      const int ch = e % DP;
+      float x = ch < a.dim ? 1.f : 0.f;
+      if (w && ch < a.dim) x = a.wf32 ? ((const float*)w)[ch] : (float)((const bf16_t*)w)[ch];
+      s_w[e / DP][ch] = x;
     }
+    __syncthreads();
   }
 };
 
-// blockIdx.x: the rows, blockIdx.y: a share of the heads.
+// How many heads' loads are in flight; the registers that this takes are bounded by the waves per SIMD (k_qk five, k_qk_bwd
+// four). 1,000,003 rows of 4 + 4 heads of 64, bf16, us: forward 4 heads 393, 3 399, 2 with six waves 459, 1 435; without a bound 457;
+// backward 1 head 602, 2 609, 2 with three waves 663.
+constexpr int kAhead = 4, kAheadBwd = 1;
+
+// blockIdx.x: the rows, blockIdx.y: a share of the heads (those of the queries first).
 template <typename T, int V, int LPR, int NV>
-__global__ __launch_bounds__(kNT) void k_qk(QkArgs a) {
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(5))) void k_qk(QkArgs a) {
   typedef Head<T, V, LPR, NV> H;
-  __shared__ float2 s_table[H::kTable];
-  __shared__ float s_x[kNT / 64][NV * V * 64];
-  float* const s_mine = s_x[threadIdx.x >> 6];
+  __shared__ float2 s_table[kNT / 64][H::WS * H::kPairs];
+  __shared__ float s_x[kNT / 64][H::kExchange];
+  __shared__ float s_w[2][H::DP];
+  const int wave = threadIdx.x >> 6;
   const float inv_d = 1.0f / (float)a.dim;
   const int h0 = blockIdx.y * a.heads_each, h1 = min(h0 + a.heads_each, a.heads[0] + a.heads[1]);
+  int at[NV][V];
+  H::places(a, s_x[wave], at);
+  if (a.norm) H::keep_weights(a, s_w);
   for (int64_t r0 = (int64_t)blockIdx.x * H::SL; r0 < a.n; r0 += (int64_t)gridDim.x * H::SL) {
     const int64_t r = r0 + threadIdx.x / LPR;
     const bool live = r < a.n;
-    float co[NV][V], si[NV][V];
-    __syncthreads();
-    H::fill(a, r0, s_table);
-    __syncthreads();
-    H::factors(a, s_table, co, si);
+    typename H::Raw raw[kAhead][NV];
+    // This lane's first channel of its row's first head: a head is a uniform step away.
+    const T *px[2];
+    T* py[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int first = max(h0 - (t ? a.heads[0] : 0), 0), last = min(h1 - (t ? a.heads[0] : 0), a.heads[t]);
-      if (first >= last) continue;
-      float w[NV][V];
-      H::weights(a.w[t], a.wf32, a.dim, w);
-      for (int h = first; h < last; ++h) {
+      px[t] = (const T*)a.x[t] + r * a.xs[t][0] + H::channel(0, 0);
+      py[t] = (T*)a.y[t] + r * ((int64_t)a.heads[t] * a.dim) + H::channel(0, 0);
+    }
+    auto fetch = [&](int h, typename H::Raw (&x)[NV]) {
+      if (h >= h1) return;
+      if (h < a.heads[0]) H::load(px[0] + h * a.xs[0][1], a.dim, live, x);
+      else H::load(px[1] + (h - a.heads[0]) * a.xs[1][1], a.dim, live, x);
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(h0 + u, raw[u]);
+    float co[NV][V], si[NV][V];
+    wave_sync();  // the last row's table has been read
+    H::fill(a, r, live, s_table[wave]);
+    wave_sync();
+    H::factors(a, s_table[wave], co, si);
+    for (int h = h0; h < h1; h += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (h + u >= h1) break;
+        const int t = h + u >= a.heads[0], g = h + u - (t ? a.heads[0] : 0);
         float x[NV][V], o[NV][V];
-        H::load((const T*)a.x[t] + r * a.xs[t][0] + h * a.xs[t][1], a.dim, live, x);
-        float rstd = 1.f;
+        H::floats(raw[u], x);
+        fetch(h + u + kAhead, raw[u]);
         if (a.norm) {
           float ss = 0.f;
 #pragma unroll
           for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) ss = fmaf(x[j][i], x[j][i], ss);
-          rstd = rsqrtf(fmaf(lanes_sum<LPR>(ss), inv_d, a.eps));
+          const float rstd = rsqrtf(fmaf(lanes_sum<LPR>(ss), inv_d, a.eps));
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[j][i] *= rstd * s_w[t][H::channel(j, i)];
         }
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < V; ++i) x[j][i] *= rstd * w[j][i];
-        H::partners(a, s_mine, x, o);
+        H::partners(a, s_x[wave], at, x, o);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int i = 0; i < V; ++i) x[j][i] = fmaf(x[j][i], co[j][i], o[j][i] * si[j][i]);
-        H::store((T*)a.y[t] + (r * a.heads[t] + h) * a.dim, a.dim, live, x);
+        if (t == 0) H::store(py[0] + (int64_t)g * a.dim, a.dim, live, x);
+        else H::store(py[1] + (int64_t)g * a.dim, a.dim, live, x);
       }
     }
   }
 }
 
 template <typename T, int V, int LPR, int NV>
-__global__ __launch_bounds__(kNT) void k_qk_bwd(QkArgs a) {
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4))) void k_qk_bwd(QkArgs a) {
   typedef Head<T, V, LPR, NV> H;
-  __shared__ float2 s_table[H::kTable];
-  __shared__ float s_x[kNT / 64][NV * V * 64];
-  float* const s_mine = s_x[threadIdx.x >> 6];
+  __shared__ float2 s_table[kNT / 64][H::WS * H::kPairs];
+  __shared__ float s_x[kNT / 64][H::kExchange];
+  __shared__ float s_w[2][H::DP];
+  const int wave = threadIdx.x >> 6;
   const float inv_d = 1.0f / (float)a.dim;
   const int h0 = blockIdx.y * a.heads_each, h1 = min(h0 + a.heads_each, a.heads[0] + a.heads[1]);
   float aw[2][NV][V];
@@ -205,35 +249,59 @@ __global__ __launch_bounds__(kNT) void k_qk_bwd(QkArgs a) {
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) aw[t][j][i] = 0.f;
+  int at[NV][V];
+  H::places(a, s_x[wave], at);
+  if (a.norm) H::keep_weights(a, s_w);
   for (int64_t r0 = (int64_t)blockIdx.x * H::SL; r0 < a.n; r0 += (int64_t)gridDim.x * H::SL) {
     const int64_t r = r0 + threadIdx.x / LPR;
     const bool live = r < a.n;
-    float co[NV][V], si[NV][V];
-    __syncthreads();
-    H::fill(a, r0, s_table);
-    __syncthreads();
-    H::factors(a, s_table, co, si);
+    typename H::Raw raw_g[kAheadBwd][NV], raw_x[kAheadBwd][NV];
+    const T *px[2];
+    int64_t dense[2];  // of dy and dx
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int first = max(h0 - (t ? a.heads[0] : 0), 0), last = min(h1 - (t ? a.heads[0] : 0), a.heads[t]);
-      if (first >= last) continue;
-      float w[NV][V];
-      H::weights(a.w[t], a.wf32, a.dim, w);
-      for (int h = first; h < last; ++h) {
+      px[t] = (const T*)a.x[t] + r * a.xs[t][0] + H::channel(0, 0);
+      dense[t] = r * ((int64_t)a.heads[t] * a.dim) + H::channel(0, 0);
+    }
+    auto fetch = [&](int h, typename H::Raw (&g)[NV], typename H::Raw (&x)[NV]) {
+      if (h >= h1) return;
+      if (h < a.heads[0]) {
+        H::load((const T*)a.dy[0] + (int64_t)h * a.dim + dense[0], a.dim, live, g);
+        if (a.norm) H::load(px[0] + h * a.xs[0][1], a.dim, live, x);
+      } else {
+        const int k = h - a.heads[0];
+        H::load((const T*)a.dy[1] + (int64_t)k * a.dim + dense[1], a.dim, live, g);
+        if (a.norm) H::load(px[1] + k * a.xs[1][1], a.dim, live, x);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kAheadBwd; ++u) fetch(h0 + u, raw_g[u], raw_x[u]);
+    float co[NV][V], si[NV][V];
+    wave_sync();
+    H::fill(a, r, live, s_table[wave]);
+    wave_sync();
+    H::factors(a, s_table[wave], co, si);
+    for (int h = h0; h < h1; h += kAheadBwd) {
+#pragma unroll
+      for (int u = 0; u < kAheadBwd; ++u) {
+        if (h + u >= h1) break;
+        const int t = h + u >= a.heads[0], k = h + u - (t ? a.heads[0] : 0);
         float g[NV][V], x[NV][V], o[NV][V];
-        H::load((const T*)a.dy[t] + (r * a.heads[t] + h) * a.dim, a.dim, live, g);
-        if (a.norm) H::load((const T*)a.x[t] + r * a.xs[t][0] + h * a.xs[t][1], a.dim, live, x);
-        H::partners(a, s_mine, g, o);
+        H::floats(raw_g[u], g);
+        if (a.norm) H::floats(raw_x[u], x);
+        fetch(h + u + kAheadBwd, raw_g[u], raw_x[u]);
+        H::partners(a, s_x[wave], at, g, o);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int i = 0; i < V; ++i) g[j][i] = fmaf(g[j][i], co[j][i], -o[j][i] * si[j][i]);
         if (a.norm) {
-          float ss = 0.f, dot = 0.f;
+          float ss = 0.f, dot = 0.f, w[NV][V];
 #pragma unroll
           for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+              w[j][i] = s_w[t][H::channel(j, i)];
               ss = fmaf(x[j][i], x[j][i], ss);
               dot = fmaf(g[j][i] * w[j][i], x[j][i], dot);
             }
@@ -244,12 +312,14 @@ __global__ __launch_bounds__(kNT) void k_qk_bwd(QkArgs a) {
           for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              const float xhat = x[j][i] * rstd;
-              aw[t][j][i] = fmaf(g[j][i], xhat, aw[t][j][i]);
+              const float xhat = x[j][i] * rstd, add = g[j][i] * xhat;
+              if (t) aw[1][j][i] += add;
+              else aw[0][j][i] += add;
               g[j][i] = rstd * fmaf(-xhat, mean, g[j][i] * w[j][i]);
             }
         }
-        H::store((T*)a.y[t] + (r * a.heads[t] + h) * a.dim, a.dim, live, g);
+        if (t == 0) H::store((T*)a.y[0] + (int64_t)k * a.dim + dense[0], a.dim, live, g);
+        else H::store((T*)a.y[1] + (int64_t)k * a.dim + dense[1], a.dim, live, g);
       }
     }
   }
@@ -270,7 +340,7 @@ __global__ __launch_bounds__(kNT) void k_qk_bwd(QkArgs a) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) s_sum[threadIdx.x >> 6][t][H::channel(j, i)] = aw[t][j][i];
+        for (int i = 0; i < V; ++i) s_sum[wave][t][H::channel(j, i)] = aw[t][j][i];
   __syncthreads();
   float* const part = a.part + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.dim;
   for (int e = threadIdx.x; e < 2 * a.dim; e += kNT) {
@@ -336,7 +406,8 @@ QkGrid qk_grid(int dtype, int64_t n, int heads, int dim, int64_t most) {
   return g;
 }
 
-constexpr int64_t kBwdWgs = 2048;
+// Workgroups of the backward pass, each with partial weight gradients: as many as run at a time.
+constexpr int64_t kBwdWgs = 1024;
 
 template <typename T>
 void qk_t(QkArgs a, bool backward, hipStream_t s) {
