@@ -392,14 +392,16 @@ int igc_cross_attention_backward(const igc_attention_t* problem, const void* d_q
  * window of keys and a few first ones. Query i (0-based) of a sequence of lq queries and lk keys stands at p = i + lk - lq (its
  * last queries are its last keys; one query: the newest of a cache), and sees key j if
  *     j <= p + right and (j >= p - left or j < sinks)
- * and the mask keeps it. left, right -1: no limit to that side (left 0, right 0: itself). All else is as for
+ * and the mask keeps it. left, right -1: no limit to that side (left 0, right 0: itself). d_kv_lengths (int32 [batch] on the
+ * device, may be NULL): only the first of a sequence's key rows are in use, lk of them (caches with room; clamped to the rows; the
+ * others may hold anything), in the forward call alone and with a limit to one side (left 2^31 - 1 leaves nothing out). All else is as for
  * igc_cross_attention: problem, results (no visible key: 0 and -infinity), precision, workspaces. k and v of keys that the mask keeps must be
  * finite, or rows beyond their windows may become NaN too. */
 int igc_window_attention_workspace(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks,
                                    int32_t backward, size_t* bytes);
-int igc_window_attention(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks, const void* d_q,
-                         const void* d_k, const void* d_v, void* d_out, float* d_lse, void* d_ws, size_t ws_bytes,
-                         igc_stream stream);
+int igc_window_attention(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks,
+                         const int32_t* d_kv_lengths, const void* d_q, const void* d_k, const void* d_v, void* d_out,
+                         float* d_lse, void* d_ws, size_t ws_bytes, igc_stream stream);
 /* Its gradients, as igc_cross_attention_backward. */
 int igc_window_attention_backward(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks,
                                   const void* d_q, const void* d_k, const void* d_v, const void* d_out, const float* d_lse,

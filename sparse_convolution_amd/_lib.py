@@ -118,7 +118,7 @@ def load() -> ctypes.CDLL:
         "igc_cross_attention": [P, P, P, P, P, P, P, size, P],
         "igc_cross_attention_backward": [P, P, P, P, P, P, P, P, P, P, P, size, P],
         "igc_window_attention_workspace": [P, i32, i32, i32, i32, ctypes.POINTER(size)],
-        "igc_window_attention": [P, i32, i32, i32, P, P, P, P, P, P, size, P],
+        "igc_window_attention": [P, i32, i32, i32, P, P, P, P, P, P, P, size, P],
         "igc_window_attention_backward": [P, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, size, P],
         "igc_qk_norm_rotary_workspace": [P, ctypes.POINTER(size)],
         "igc_qk_norm_rotary": [P, P, P, P, P, i32, P, P, P],

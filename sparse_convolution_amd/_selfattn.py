@@ -38,20 +38,25 @@ def _window_workspace(backward: int, window: tuple, code: int, batch: int, heads
 
 def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int | None = None, right: int | None = None,
                      sinks: int = 0, q_offsets: torch.Tensor | None = None, kv_offsets: torch.Tensor | None = None,
-                     key_mask: torch.Tensor | None = None, scale: float | None = None):
+                     key_mask: torch.Tensor | None = None, scale: float | None = None, kv_lengths: torch.Tensor | None = None):
     """cross_attention among rows in order, where a query sees a window of keys and a few first ones: query i of a
     sequence of lq queries and lk keys stands at p = i + lk - lq and sees key j if j <= p + right and (j >= p - left or j < sinks) and
     key_mask keeps it. None: no limit to that side; right 0 is causal. With as many queries as keys this is attention within
-    a sequence, with fewer that of its last rows to a cache (single tokens). k and v must be finite where key_mask keeps them. Returns (out, lse) as
-    cross_attention (igc_window_attention)."""
+    a sequence, with fewer that of its last rows to a cache (single tokens); kv_lengths (int32 [batch] on the device) says how many
+    of a sequence's key rows are in use where a cache has room for more (its lk then; without gradients). k and v in use must be finite where
+    key_mask keeps them. Returns (out, lse) as cross_attention (igc_window_attention)."""
     window = _window(left, right, sinks)
     p, sizes = _attention_problem(q, k, v, q_offsets, kv_offsets, key_mask, scale)
     dev = q.device
+    if kv_lengths is not None:
+        _same(kv_lengths, "kv_lengths", torch.int32, (sizes[1],), dev.index)
+        if window[0] < 0 and window[1] < 0:  # lengths need a limit: one that leaves nothing out
+            window = (2 ** 31 - 1, -1, 0)
     out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
     n = _window_workspace(0, window, *sizes)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    _call("igc_window_attention", dev.index, p, *window, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+    _call("igc_window_attention", dev.index, p, *window, _ptr(kv_lengths), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
           _ptr(ws), n)
     return out, lse
 

@@ -58,6 +58,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   int64_t q0, q1, k0, k1;
   seq_rows(a.qo, b, a.nq, q0, q1);
   seq_rows(a.ko, b, a.nk, k0, k1);
+  if (WIN && a.kl) k1 = clamp64(k0 + a.kl[b], k0, k1);
   const int64_t rows = (q1 - q0) * a.group;
   if (tile * BM >= rows) return;
   // WIN: the tile's keys as one axis, of which this workgroup takes places x0 .. x0 + keys.
@@ -292,6 +293,7 @@ __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
   int64_t q0, q1, k0, k1;
   seq_rows(a.qo, b, a.nq, q0, q1);
   seq_rows(a.ko, b, a.nk, k0, k1);
+  if (WIN && a.kl) k1 = clamp64(k0 + a.kl[b], k0, k1);
   const int64_t rows = (q1 - q0) * a.group;
   if (tile * R >= rows) return;
   WindowAxis axis = {};  // as in k_attn_fwd

@@ -135,6 +135,8 @@ int window_args(const char* fn, const Window* w, AttnArgs& a) {
   if (w->left < -1 || w->right < -1) return set_error(IGC_ERR_INVALID_ARG, f + ": left and right must be -1 (no limit) or more");
   if (w->sinks < 0) return set_error(IGC_ERR_INVALID_ARG, f + ": sinks is negative");
   a.windowed = w->left >= 0 || w->right >= 0;
+  if (a.kl && !a.windowed)  // whose workspace would be cross attention's
+    return set_error(IGC_ERR_INVALID_ARG, f + ": d_kv_lengths need a limit to one side (left 2^31-1 leaves nothing out)");
   a.win = *w;
   if (w->left < 0) a.win.sinks = 0;  // all keys before a query are visible anyway
   return IGC_OK;
@@ -155,10 +157,11 @@ int attention_workspace(const char* fn, const igc_attention_t* p, const Window* 
   return IGC_OK;
 }
 
-int attention_forward(const char* fn, const igc_attention_t* p, const Window* w, const void* d_q, const void* d_k, const void* d_v,
+int attention_forward(const char* fn, const igc_attention_t* p, const Window* w, const int32_t* d_kv_lengths, const void* d_q, const void* d_k, const void* d_v,
                       void* d_out, float* d_lse, void* d_ws, size_t ws_bytes, hipStream_t stream) {
   const std::string f(fn);
   AttnArgs a;
+  a.kl = d_kv_lengths;
   int rc = attention_args(fn, p, a);
   if (!rc) rc = window_args(fn, w, a);
   if (rc || a.nq == 0) return rc;
@@ -324,7 +327,7 @@ int igc_cross_attention_workspace(const igc_attention_t* p, int32_t backward, si
 
 int igc_cross_attention(const igc_attention_t* p, const void* d_q, const void* d_k, const void* d_v, void* d_out,
                         float* d_lse, void* d_ws, size_t ws_bytes, igc_stream stream) {
-  return attention_forward("igc_cross_attention", p, nullptr, d_q, d_k, d_v, d_out, d_lse, d_ws, ws_bytes, (hipStream_t)stream);
+  return attention_forward("igc_cross_attention", p, nullptr, nullptr, d_q, d_k, d_v, d_out, d_lse, d_ws, ws_bytes, (hipStream_t)stream);
 }
 
 int igc_cross_attention_backward(const igc_attention_t* p, const void* d_q, const void* d_k, const void* d_v,
@@ -340,10 +343,11 @@ int igc_window_attention_workspace(const igc_attention_t* p, int32_t left, int32
   return attention_workspace("igc_window_attention_workspace", p, &w, backward, bytes);
 }
 
-int igc_window_attention(const igc_attention_t* p, int32_t left, int32_t right, int32_t sinks, const void* d_q, const void* d_k,
-                         const void* d_v, void* d_out, float* d_lse, void* d_ws, size_t ws_bytes, igc_stream stream) {
+int igc_window_attention(const igc_attention_t* p, int32_t left, int32_t right, int32_t sinks, const int32_t* d_kv_lengths,
+                         const void* d_q, const void* d_k, const void* d_v, void* d_out, float* d_lse, void* d_ws, size_t ws_bytes,
+                         igc_stream stream) {
   const Window w = {left, right, sinks};
-  return attention_forward("igc_window_attention", p, &w, d_q, d_k, d_v, d_out, d_lse, d_ws, ws_bytes, (hipStream_t)stream);
+  return attention_forward("igc_window_attention", p, &w, d_kv_lengths, d_q, d_k, d_v, d_out, d_lse, d_ws, ws_bytes, (hipStream_t)stream);
 }
 
 int igc_window_attention_backward(const igc_attention_t* p, int32_t left, int32_t right, int32_t sinks, const void* d_q,

@@ -279,6 +279,7 @@ struct AttnArgs {
   int64_t far_rows = 0;
   float* far = nullptr;
   Window win = {-1, -1, 0};
+  const int32_t* kl = nullptr;  // forward: keys of each sequence in use (null: all)
 };
 constexpr int32_t kAttnMaxDim = 128;
 // Keys, and query rows (queries times the heads that share a key head), of a problem at most: the kernels count those of a

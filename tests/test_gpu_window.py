@@ -132,6 +132,38 @@ def test_new_rows_behind_a_cache(lq, lk, heads, kv_heads, dim, left, right, sink
 
 
 @TYPES
+@pytest.mark.parametrize("lq,lk,room,heads,kv_heads,dim", [([1] * 5, [5, 1, 800, 0, 64], 900, 4, 2, 64), ([1, 1], [300, 2000], 4096, 8, 2, 128),
+                                                           ([40, 0, 130], [500, 60, 130], 600, 2, 1, 32), ([1] * 90, [37] * 90, 64, 2, 2, 64)])
+@pytest.mark.parametrize("left,right,sinks", [(255, 0, 4), (None, 0, 0), (30, 9, 0), (None, None, 0)])
+def test_caches_with_room(lq, lk, room, heads, kv_heads, dim, left, right, sinks, dtype):
+    # Each sequence's keys lie at the start of `room` rows whose rest holds NaN.
+    igc = _igc()
+    say(f"window caches with room {lq[:4]} {lk[:4]} {dtype}")
+    dev, (qo, _), _ = _case(lq, lk, heads, kv_heads, dim, dtype)
+    q, k, v, do = dev
+    cache = [torch.full((len(lk) * room, kv_heads, dim), float("nan"), dtype=dtype, device="cuda") for _ in range(2)]
+    first = 0
+    for b, n in enumerate(lk):
+        for c, t in zip(cache, (k, v)):
+            c[b * room:b * room + n] = t[first:first + n]
+        first += n
+    ko = (torch.arange(len(lk) + 1) * room).int().cuda()
+    lengths = torch.tensor(lk, dtype=torch.int32).cuda()
+    out, lse = igc.window_attention(q, *cache, left, right, sinks, qo, ko, kv_lengths=lengths)
+    r, b, rl = reference(dev, lq, lk, None, dim ** -0.5, left, right, sinks)
+    got = lse.double().cpu()
+    fin = torch.isfinite(rl)
+    assert torch.equal(torch.isfinite(got), fin) and bool(((got - rl)[fin].abs() <= F * (1 + rl[fin].abs())).all())
+    assert bool(((out.double().cpu() - r["out"]).abs() <= b["out"]).all())
+    # Lengths beyond the rows are the rows, negative ones none.
+    full = igc.window_attention(q, *[c.nan_to_num(0.0) for c in cache], left, right, sinks, qo, ko, kv_lengths=torch.full_like(lengths, 2 ** 31 - 1))
+    same = igc.window_attention(q, *[c.nan_to_num(0.0) for c in cache], left, right, sinks, qo, ko, kv_lengths=torch.full_like(lengths, room))
+    assert torch.equal(full[0], same[0])
+    none = igc.window_attention(q, *cache, left, right, sinks, qo, ko, kv_lengths=torch.full_like(lengths, -5))
+    assert bool((none[0] == 0).all()) and bool((none[1] == -np.inf).all())
+
+
+@TYPES
 def test_more_queries_than_keys(dtype):
     # The first queries stand before the first key: without a look ahead they see nothing.
     for right in (0, 30):
@@ -219,7 +251,7 @@ def test_rows_of_no_sequence_are_left(qo, nq, ko, nk, sinks, dtype):
             _lib.check(lib.igc_window_attention_backward(p, 50, 7, sinks, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                                          do.data_ptr(), *[t.data_ptr() for t in mark[2:]], ws.data_ptr(), size.value, s))
         else:
-            _lib.check(lib.igc_window_attention(p, 50, 7, sinks, q.data_ptr(), k.data_ptr(), v.data_ptr(), mark[0].data_ptr(), mark[1].data_ptr(),
+            _lib.check(lib.igc_window_attention(p, 50, 7, sinks, None, q.data_ptr(), k.data_ptr(), v.data_ptr(), mark[0].data_ptr(), mark[1].data_ptr(),
                                                 ws.data_ptr(), size.value, s))
     torch.cuda.synchronize()
     for t, want, at in zip(mark, (out, lse, *grads), (rows, rows, rows, keys, keys)):

@@ -150,7 +150,7 @@ def test_windows(lib, left, right, sinks, word):
     from tests.test_block_refusals import _problem
     p, size = ctypes.byref(_problem()), ctypes.c_size_t(0)
     _refused(lib, INVALID, lib.igc_window_attention_workspace(p, left, right, sinks, 0, ctypes.byref(size)), word)
-    _refused(lib, INVALID, lib.igc_window_attention(p, left, right, sinks, P, P, P, Q, Q, Q, 1 << 40, None), word)
+    _refused(lib, INVALID, lib.igc_window_attention(p, left, right, sinks, None, P, P, P, Q, Q, Q, 1 << 40, None), word)
     _refused(lib, INVALID, lib.igc_window_attention_backward(p, left, right, sinks, P, P, P, P, P, P, Q, Q, Q, Q, 1 << 40, None), word)
 
 
@@ -161,20 +161,21 @@ def test_window_problems_and_operands(lib):
                                  ({"batch": 2}, INVALID, b"offsets"), ({"scale": 0.0}, INVALID, b"scale")):
         p = ctypes.byref(_problem(**change))
         _refused(lib, status, lib.igc_window_attention_workspace(p, 9, 0, 2, 1, ctypes.byref(size)), word)
-        _refused(lib, status, lib.igc_window_attention(p, 9, 0, 2, P, P, P, Q, Q, Q, 1 << 40, None), word)
+        _refused(lib, status, lib.igc_window_attention(p, 9, 0, 2, None, P, P, P, Q, Q, Q, 1 << 40, None), word)
         assert b"igc_window_attention:" in lib.igc_last_error()
     p, few = ctypes.byref(_problem()), ctypes.byref(_problem(n_q=1, n_k=100000))
     fwd, bwd = lib.igc_window_attention, lib.igc_window_attention_backward
-    _refused(lib, INVALID, fwd(None, 9, 0, 2, P, P, P, Q, Q, None, 0, None), b"problem")
-    _refused(lib, INVALID, fwd(p, 9, 0, 2, None, P, P, Q, Q, None, 0, None), b"d_q")
-    _refused(lib, INVALID, fwd(p, 9, 0, 2, P, P, P, P, Q, None, 0, None), b"aliases")
-    _refused(lib, CAPACITY, fwd(few, 9000, 0, 2, P, P, P, Q, Q, None, 0, None), b"igc_window_attention_workspace")
+    _refused(lib, INVALID, fwd(None, 9, 0, 2, None, P, P, P, Q, Q, None, 0, None), b"problem")
+    _refused(lib, INVALID, fwd(p, 9, 0, 2, None, None, P, P, Q, Q, None, 0, None), b"d_q")
+    _refused(lib, INVALID, fwd(p, 9, 0, 2, None, P, P, P, P, Q, None, 0, None), b"aliases")
+    _refused(lib, CAPACITY, fwd(few, 9000, 0, 2, None, P, P, P, Q, Q, None, 0, None), b"igc_window_attention_workspace")
     _refused(lib, CAPACITY, bwd(p, 9, 0, 2, P, P, P, P, P, P, Q, Q, Q, Q, 8, None), b"igc_window_attention_workspace")
     _refused(lib, INVALID, bwd(p, 9, 0, 2, P, P, P, P, P, P, Q, Q, Q, ctypes.c_void_p(8196), 1 << 40, None), b"aligned")
     _refused(lib, INVALID, bwd(p, 9, 0, 2, P, P, P, P, P, P, Q, Q, None, Q, 1 << 40, None), b"together")
     _refused(lib, INVALID, lib.igc_window_attention_workspace(p, 9, 0, 2, 0, None), b"bytes")
+    _refused(lib, INVALID, fwd(p, -1, -1, 0, P, P, P, P, Q, Q, None, 0, None), b"d_kv_lengths need a limit")
     none = ctypes.byref(_problem(n_q=0, n_k=0))
-    assert fwd(none, 9, 0, 2, None, None, None, None, None, None, 0, None) == 0
+    assert fwd(none, 9, 0, 2, None, None, None, None, None, None, None, 0, None) == 0
     assert bwd(none, 9, 0, 2, None, None, None, None, None, None, None, None, None, None, 0, None) == 0
     import sparse_convolution_amd as igc
     x = torch.zeros(4, 2, 8)
