@@ -36,13 +36,16 @@ constexpr float kSlack = 8.f;
 // WIN 1: a query sees the keys of a window and a few first ones (see igc_ragged.h); 2: and a key mask keeps some. The workgroup walks the
 // keys that any of its queries sees; a wave passes over those that none of its own sees, and masks by rows only where an
 // edge runs through, 32 keys at a time. The key mask enters as a bias.
-template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, int WIN, int NW>
+// KS 2 (WIN): pairs of waves share their rows, each takes every second block of 32 keys, and one adds up: half the
+// latency where there are too few rows to fill the GPU.
+template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, int WIN, int NW, int KS>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_fwd(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int NT = 64 * NW;
   constexpr int LD = lds_ld<DP>(), PS = BN * LD;
-  constexpr int BM = 32 * NQ * NW;
+  constexpr int BM = 32 * NQ * NW / KS;
   constexpr int KT = BN / 32, DT = DP / 32;
+  static_assert(KS == 1 || (NQ == 1 && KT == KS && handover_bytes<DP / 32>(2) * NW / KS <= lds_bytes<T, DP>(4 * kParts<T> * PS, NW)), "KS");
   constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
   constexpr int TILE = kParts<T> * PS;
   __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE, NW)];
@@ -51,6 +54,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   auto s_v = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
 
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
+  const int row_wave = wave / KS, share = wave % KS;
   const int kh = blockIdx.x % a.kv_heads;
   const int split = (blockIdx.x / a.kv_heads) % a.splits;
   int b;
@@ -113,7 +117,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   WindowRow see[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
+    const int64_t r = tile * BM + (row_wave * NQ + n) * 32 + (lane & 31);
     int64_t qi;
     int head;
     // WIN: rows behind the last one see what it sees.
@@ -248,13 +252,32 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
       blocks(std::integral_constant<int, KT>{}, 0);
     } else {
 #pragma unroll 1
-      for (int t = 0; t < KT; ++t)
+      for (int t = share; t < KT; t += KS)
         if (!wave_sees.none(j + 32 * t, 32)) blocks(std::integral_constant<int, 1>{}, t);
     }
   }
 
   __syncthreads();  // every wave is past reading the tiles: their space takes the results
-  void* const s_out = s_mem + wave * (32 * (DP + 4) * 4);
+  if constexpr (KS > 1) {
+    float* const s = (float*)(s_mem + row_wave * handover_bytes<DT>(2));
+    float* const s_ml = s + DT * 16 * 64 + lane;
+    if (share == 1) {
+      hand_over(s, o[0]);
+      s_ml[0] = m[0], s_ml[64] = l[0];
+    }
+    __syncthreads();
+    if (share == 0) {
+      // Two references, counted from 0 where there is none: its results are then 0.
+      const float m1 = s_ml[0], top = fmaxf(m[0], m1), base = top == -INFINITY ? 0.f : top;
+      const float f = __builtin_amdgcn_exp2f((m[0] - base) * c), g = __builtin_amdgcn_exp2f((m1 - base) * c);
+      l[0] = fmaf(s_ml[64], g, l[0] * f);
+      take_over(s, o[0], f, g);
+      m[0] = top;
+    }
+    __syncthreads();
+    if (share == 1) return;
+  }
+  void* const s_out = s_mem + row_wave * (32 * (DP + 4) * 4);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const float total = l[n] + __shfl_xor(l[n], 32, 64);
@@ -508,9 +531,9 @@ struct FwdShape<float, DP> {
 // either side, 8 heads: (1, 64, 3, 4) 292, (1, 64, 2, 4) 298, (2, 64, 3, 4) 334. fp32, 50,003 rows, 4 heads, 256 to either side, heads
 // of 32 and the small case of 7,131 rows, 64 to either side: (1, 32, 2, 2) 123 and 14.1, (1, 32, 3, 4) 119 and 17.5; heads of 64: (1,
 // 32, 3, 4) 205, (1, 32, 2, 4) 213, (1, 32, 2, 2) 309.
-template <int Q, int N, int E, int W>
+template <int Q, int N, int E, int W, int S = 1>
 struct Shape {
-  static constexpr int NQ = Q, BN = N, WPE = E, NW = W;
+  static constexpr int NQ = Q, BN = N, WPE = E, NW = W, KS = S, kRows = 32 * Q * W / S;
 };
 template <typename T, int DP>
 struct WinShape : Shape<1, 32, 1, 4> {};
@@ -524,10 +547,22 @@ template <>
 struct WinShape<float, 32> : Shape<1, 32, 2, 2> {};
 template <>
 struct WinShape<float, 64> : Shape<1, 32, 3, 4> {};
+// The same where rows are few (see window_few): a key axis shared by two waves. Heads over 64 in fp32 have no room for its tiles.
+template <typename T, int DP>
+struct WinFewShape : Shape<1, 64, 2, 4, 2> {};
+template <>
+struct WinFewShape<float, 64> : Shape<1, 64, 1, 4, 2> {};
+template <>
+struct WinFewShape<float, 96> : WinShape<float, 96> {};
+template <>
+struct WinFewShape<float, 128> : WinShape<float, 128> {};
 template <typename T>
-int win_rows(int dim) {
-  auto rows = [](auto s) { return 32 * s.NQ * s.NW; };
-  return dim <= 32 ? rows(WinShape<T, 32>{}) : dim <= 64 ? rows(WinShape<T, 64>{}) : dim <= 96 ? rows(WinShape<T, 96>{}) : rows(WinShape<T, 128>{});
+int win_rows(int dim, bool few) {
+  auto rows = [&](auto s, auto f) { return few ? f.kRows : s.kRows; };
+  return dim <= 32   ? rows(WinShape<T, 32>{}, WinFewShape<T, 32>{})
+         : dim <= 64 ? rows(WinShape<T, 64>{}, WinFewShape<T, 64>{})
+         : dim <= 96 ? rows(WinShape<T, 96>{}, WinFewShape<T, 96>{})
+                     : rows(WinShape<T, 128>{}, WinFewShape<T, 128>{});
 }
 
 constexpr int kFewRows = 4;
@@ -552,13 +587,16 @@ constexpr int kFewRows = 4;
 // So a few rows take k_attn_few, but for bf16 heads over 64, where the matrix kernel is ahead throughout. What the rule
 // gives away is up to 11 us a call on small problems, bf16 in the main, whose parts of 256 keys leave the GPU half empty.
 // 8 rows of bf16, 64 x 4096 keys, 8 heads of 64: 184 / 101.
-int fwd_rows(int dtype, int dim, int64_t nq, int batch, int group, bool windowed) {
+int fwd_rows(int dtype, int dim, int64_t nq, int batch, int group, int kv_heads, bool windowed) {
   const int64_t rows = (nq + batch - 1) / batch * group;
   if (dtype == IGC_F32 || dim <= 64) {
     for (int r = 1; r <= kFewRows; r *= 2)
       if (rows <= r) return r;
   }
-  if (windowed) return dtype == IGC_BF16 ? win_rows<bf16_t>(dim) : win_rows<float>(dim);
+  if (windowed) {
+    const bool few = window_few(dtype, dim, (nq + batch - 1) / batch * group, batch, kv_heads);
+    return dtype == IGC_BF16 ? win_rows<bf16_t>(dim, few) : win_rows<float>(dim, few);
+  }
   return dtype == IGC_BF16 && dim <= 64 ? 256 : 128;
 }
 
@@ -615,20 +653,28 @@ void join(const AttnArgs& a, hipStream_t s) {
   else k_attn_join<T><<<(unsigned)rows, kNT, 0, s>>>(a);
 }
 
+template <typename T, int DP, typename W>
+void win_go(const AttnArgs& a, unsigned wgs, bool vec, hipStream_t s) {
+  if (a.mask) {
+    if (vec) k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, true, 2, W::NW, W::KS><<<wgs, 64 * W::NW, 0, s>>>(a);
+    else k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, false, 2, W::NW, W::KS><<<wgs, 64 * W::NW, 0, s>>>(a);
+  } else {
+    if (vec) k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, true, 1, W::NW, W::KS><<<wgs, 64 * W::NW, 0, s>>>(a);
+    else k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, false, 1, W::NW, W::KS><<<wgs, 64 * W::NW, 0, s>>>(a);
+  }
+}
+
 template <typename T, int DP>
 void fwd_go(const AttnArgs& a, unsigned wgs, hipStream_t s) {
   typedef FwdShape<T, DP> F;
-  typedef WinShape<T, DP> W;
   const bool vec = a.qvec && a.kvec;
-  if (a.windowed && a.mask) {
-    if (vec) k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, true, 2, W::NW><<<wgs, 64 * W::NW, 0, s>>>(a);
-    else k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, false, 2, W::NW><<<wgs, 64 * W::NW, 0, s>>>(a);
-  } else if (a.windowed) {
-    if (vec) k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, true, 1, W::NW><<<wgs, 64 * W::NW, 0, s>>>(a);
-    else k_attn_fwd<T, DP, W::NQ, W::BN, W::WPE, false, 1, W::NW><<<wgs, 64 * W::NW, 0, s>>>(a);
+  if (!a.windowed) {
+    if (vec) k_attn_fwd<T, DP, F::NQ, F::BN, F::WPE, true, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);
+    else k_attn_fwd<T, DP, F::NQ, F::BN, F::WPE, false, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);
+  } else if (window_few(sizeof(T) == 2 ? IGC_BF16 : IGC_F32, a.dim, (a.nq + a.batch - 1) / a.batch * a.group, a.batch, a.kv_heads)) {
+    win_go<T, DP, WinFewShape<T, DP>>(a, wgs, vec, s);
   } else {
-    if (vec) k_attn_fwd<T, DP, F::NQ, F::BN, F::WPE, true, 0, 4><<<wgs, kNT, 0, s>>>(a);
-    else k_attn_fwd<T, DP, F::NQ, F::BN, F::WPE, false, 0, 4><<<wgs, kNT, 0, s>>>(a);
+    win_go<T, DP, WinShape<T, DP>>(a, wgs, vec, s);
   }
 }
 
@@ -652,7 +698,7 @@ void few_r(const AttnArgs& a, int rows, unsigned wgs, hipStream_t s) {
 
 template <typename T>
 void fwd_t(const AttnArgs& a, int dtype, hipStream_t s) {
-  const int rows = fwd_rows(dtype, a.dim, a.nq, a.batch, a.group, a.windowed);
+  const int rows = fwd_rows(dtype, a.dim, a.nq, a.batch, a.group, a.kv_heads, a.windowed);
   const unsigned wgs = (unsigned)((a.nq * a.group / rows + a.batch) * a.kv_heads * a.splits);
   if (rows <= kFewRows) {
     if (a.dim <= 32) few_r<T, 4>(a, rows, wgs, s);
@@ -674,7 +720,7 @@ int attn_fwd_splits(int dtype, const AttnArgs& a) {
   const int batch = a.batch, heads = a.heads, kv_heads = a.kv_heads, dim = a.dim;
   // Parts of the key axis: none while the query tiles alone fill the GPU, else enough for that, each of
   // at least 256 keys.
-  const int bm = fwd_rows(dtype, dim, nq, batch, heads / kv_heads, a.windowed);
+  const int bm = fwd_rows(dtype, dim, nq, batch, heads / kv_heads, kv_heads, a.windowed);
   const int64_t per_seq = (nq + batch - 1) / batch * (heads / kv_heads);
   const int64_t wgs = batch * ((per_seq + bm - 1) / bm) * kv_heads;
   // Workgroups that fill it: two a CU of the matrix kernel, three of its fp32 form for short heads, which is small enough
@@ -682,7 +728,8 @@ int attn_fwd_splits(int dtype, const AttnArgs& a) {
   // 102 / 118 / 111, of 128 125 / 145 / 145; bf16 56 / 58 / 68, 44 / 56 / 57 and 49 / 59 / 60. fp32 heads of 32 at other sizes: 900
   // queries on 8,000 keys, 8 heads, 68 / 65 / 67; 500 on 20,000, 4 heads, 47 / 47 / 48; 100 on 40,000, 8 heads, 48 / 50 / 52;
   // heads of 16, the first three of these sizes: 117 / 104 / 106, 68 / 62 / 63 and 46 / 45 / 45.
-  const int64_t fill = bm <= kFewRows ? 2048 : dtype == IGC_F32 && dim <= 32 ? 768 : 512;
+  const bool wide = a.windowed && dtype == IGC_F32 && dim > 32;  // one or two workgroups a CU
+  const int64_t fill = bm <= kFewRows ? 2048 : wide ? 256 : dtype == IGC_F32 && dim <= 32 ? 768 : 512;
   const int64_t want = wgs >= fill ? 1 : fill / std::max<int64_t>(1, wgs);
   int64_t keys = nk / batch;  // that a tile walks
   if (a.windowed && a.win.left >= 0 && a.win.right >= 0)

@@ -29,12 +29,12 @@ constexpr int kNT = 256;
 // lse in base 2; +infinity for rows without keys, whose probabilities are then exp2(-infinity) = 0.
 __device__ __forceinline__ float lse_base2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-// dq and delta: NW waves of 32 NQ query rows over tiles of BN keys (see k_attn_fwd for rows, WIN and the key mask's bias).
-template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, int WIN, int NW>
+// dq and delta: NW waves of 32 NQ query rows over tiles of BN keys (see k_attn_fwd for rows, WIN, KS and the key mask's bias).
+template <typename T, int DP, int NQ, int BN, int WPE, bool VEC, int WIN, int NW, int KS>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dq(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int LD = lds_ld<DP>(), PS = BN * LD;
-  constexpr int NT = 64 * NW, BM = 32 * NQ * NW;
+  constexpr int NT = 64 * NW, BM = 32 * NQ * NW / KS;
   constexpr int KT = BN / 32, DT = DP / 32;
   constexpr uint64_t kAll = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
   constexpr int TILE = kParts<T> * PS;
@@ -43,7 +43,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   auto s_k = [&](int buf) { return (bf16_t*)s_mem + buf * TILE; };
   auto s_v = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
 
+  static_assert(KS == 1 || (NQ == 1 && KT == KS && handover_bytes<DP / 32>(0) * NW / KS <= lds_bytes<T, DP>(4 * TILE, NW)), "KS");
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
+  const int row_wave = wave / KS, share = wave % KS;
   const int kh = blockIdx.x % a.kv_heads;
   const int split = (blockIdx.x / a.kv_heads) % a.splits;
   int b;
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   WindowRow see[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const int64_t r = tile * BM + (wave * NQ + n) * 32 + (lane & 31);
+    const int64_t r = tile * BM + (row_wave * NQ + n) * 32 + (lane & 31);
     int64_t qi;
     int head;
     split_row(r < rows ? r : WIN ? rows - 1 : 0, a.group, qi, head);
@@ -125,7 +127,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
       for (int i = 0; i < 8; ++i) delta[n] = fmaf((float)g[i], (float)f[i], delta[n]);
     }
     delta[n] += __shfl_xor(delta[n], 32, 64);
-    if (row[n] >= 0 && h == 0 && split == 0) a.delta[row[n]] = delta[n];
+    if (row[n] >= 0 && h == 0 && split == 0 && share == 0) a.delta[row[n]] = delta[n];
     lse[n] = lse_base2(row[n] >= 0 ? a.lse_in[row[n]] : -INFINITY);
   }
   WindowWave wave_sees;
@@ -152,6 +154,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
+      if (KS > 1 && t != share) continue;
       if (WIN && wave_sees.none(j + 32 * t, 32)) continue;
       f32x16 s[NQ], dp[NQ];
 #pragma unroll
@@ -207,7 +210,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   }
   if (!a.dq) return;
   __syncthreads();  // every wave is past reading the tiles: their space takes the results
-  void* const s_out = s_mem + wave * (32 * (DP + 4) * 4);
+  if constexpr (KS > 1) {
+    float* const s = (float*)(s_mem + row_wave * handover_bytes<DT>(0));
+    if (share == 1) hand_over(s, dq[0]);
+    __syncthreads();
+    if (share == 0) take_over(s, dq[0], 1.f, 1.f);
+    __syncthreads();
+    if (share == 1) return;
+  }
+  void* const s_out = s_mem + row_wave * (32 * (DP + 4) * 4);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     if (a.splits > 1)
@@ -230,11 +241,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
 // WIN: the workgroup of a key tile walks the rows whose windows hold any of its keys. Sinks among its keys are seen by all later
 // rows too: those are walked by far_parts workgroups of their own for each tile with sinks (the launch's first), so that none walks
 // a whole sequence alone, and k_attn_sinks adds up.
-template <typename T, int DP, int NK, int BQ, int WPE, bool VEC, int WIN, int NW>
+// KS 2 (WIN): pairs of waves share their keys, each takes every second block of 32 rows.
+template <typename T, int DP, int NK, int BQ, int WPE, bool VEC, int WIN, int NW, int KS>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) void k_attn_dkv(AttnArgs a) {
   typedef Frag<T> frag;
   constexpr int LD = lds_ld<DP>(), PS = BQ * LD;
-  constexpr int NT = 64 * NW, BM = 32 * NK * NW;
+  constexpr int NT = 64 * NW, BM = 32 * NK * NW / KS;
   constexpr int QT = BQ / 32, DT = DP / 32;
   constexpr int TILE = kParts<T> * PS;
   __shared__ __attribute__((aligned(16))) char s_mem[lds_bytes<T, DP>(4 * TILE, NW)];
@@ -242,7 +254,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   auto s_o = [&](int buf) { return (bf16_t*)s_mem + (2 + buf) * TILE; };
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];  // s_delta: -delta
 
+  static_assert(KS == 1 || (NK == 1 && QT == KS && handover_bytes<2 * DP / 32>(0) * NW / KS <= lds_bytes<T, DP>(4 * TILE, NW)), "KS");
   const int lane = lane_id(), wave = threadIdx.x >> 6, h = lane >> 5;
+  const int key_wave = wave / KS, share = wave % KS;
   const bool far = WIN && blockIdx.x < a.far_wgs;
   const unsigned wg = WIN && !far ? blockIdx.x - a.far_wgs : blockIdx.x;
   const int kh = wg % a.kv_heads;
@@ -312,7 +326,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   int any_from = 0, any_to = 0, all_from = 0, all_to = 0;  // rows that see any, and all, of the wave's keys
 #pragma unroll
   for (int n = 0; n < NK; ++n) {
-    const int64_t j = k0 + tile * BM + (wave * NK + n) * 32 + (lane & 31);
+    const int64_t j = k0 + tile * BM + (key_wave * NK + n) * 32 + (lane & 31);
     key[n] = j < k1 ? j : -1;
     keep[n] = j < k1 && (!a.mask || a.mask[j]);
 #pragma unroll
@@ -362,6 +376,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       const int r32 = t0 + 32 * t;
+      if (KS > 1 && t != share) continue;
       if (WIN && (any_to <= r32 || any_from >= r32 + 32)) continue;
       f32x16 s[NK], dp[NK];
 #pragma unroll
@@ -433,7 +448,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
     }
   }
   __syncthreads();
-  void* const s_out = s_mem + wave * (32 * (DP + 4) * 4);
+  if constexpr (KS > 1) {
+    float* const s = (float*)(s_mem + key_wave * handover_bytes<2 * DT>(0));
+    if (share == 1) hand_over(s, dk[0]), hand_over(s + DT * 16 * 64, dv[0]);
+    __syncthreads();
+    if (share == 0) take_over(s, dk[0], 1.f, 1.f), take_over(s + DT * 16 * 64, dv[0], 1.f, 1.f);
+    __syncthreads();
+    if (share == 1) return;
+  }
+  void* const s_out = s_mem + key_wave * (32 * (DP + 4) * 4);
 #pragma unroll
   for (int n = 0; n < NK; ++n) {
     int64_t row = key[n] < 0 ? -1 : key[n] * a.kv_heads + kh;
@@ -576,9 +599,10 @@ struct BwdShape<float, DP> {
 // to either side, masked, 4 heads on 2 of 64: 605 / 672 / 622; 100,003 rows, 256 to either side, 4 heads: 388 / 491 / 387. Heads of 32
 // (200,003 rows, 8 heads, 256 to either side): 901, with the shapes without windows 996; of 96 (100,003 rows, 4 heads) 645 and 705.
 // fp32, heads of 32, two waves / four waves: 50,003 rows, 4 heads, 256 to either side 358 / 359, 7,131 rows, 2 heads, 64: 44 / 54.
-template <int Q, int QE, int QN, int QW, int K, int KE, int KN, int KW>
+template <int Q, int QE, int QN, int QW, int K, int KE, int KN, int KW, int S = 1>
 struct Shape {
-  static constexpr int NQ = Q, QWPE = QE, QB = QN, QNW = QW, NK = K, KWPE = KE, KB = KN, KNW = KW;
+  static constexpr int NQ = Q, QWPE = QE, QB = QN, QNW = QW, NK = K, KWPE = KE, KB = KN, KNW = KW, KS = S;
+  static constexpr int kRows = 32 * Q * QW / S, kKeys = 32 * K * KW / S;
 };
 template <typename T, int DP>
 struct WinShape : Shape<1, 1, 32, 4, 1, 1, 32, 4> {};
@@ -594,37 +618,69 @@ template <>
 struct WinShape<float, 32> : Shape<1, 2, 32, 2, 1, 2, 32, 2> {};
 template <>
 struct WinShape<float, 64> : Shape<1, 2, 32, 4, 1, 1, 32, 4> {};
-struct BwdRows {
-  int q, k;
+// The same where tiles are few (see window_few): two waves share the walked axis. Heads over 64 in fp32 have no room for its tiles.
+template <typename T, int DP>
+struct WinFewShape : Shape<1, 2, 64, 4, 1, 2, 64, 4, 2> {};
+template <>
+struct WinFewShape<bf16_t, 96> : Shape<1, 2, 64, 4, 1, 1, 64, 4, 2> {};
+template <>
+struct WinFewShape<bf16_t, 128> : Shape<1, 2, 64, 4, 1, 1, 64, 4, 2> {};
+template <>
+struct WinFewShape<float, 64> : Shape<1, 1, 64, 4, 1, 1, 64, 4, 2> {};
+template <>
+struct WinFewShape<float, 96> : WinShape<float, 96> {};
+template <>
+struct WinFewShape<float, 128> : WinShape<float, 128> {};
+struct BwdTiles {
+  int q, k;           // rows and keys of a workgroup's tile
+  bool few_q, few_k;  // of WinFewShape
 };
 template <typename T, int DP>
-BwdRows rows_of(bool windowed) {
+BwdTiles tiles_of(const AttnArgs& a) {
   typedef BwdShape<T, DP> B;
   typedef WinShape<T, DP> W;
-  if (windowed) return {32 * W::NQ * W::QNW, 32 * W::NK * W::KNW};
-  return {128 * B::NQ, 128 * B::NK};
+  typedef WinFewShape<T, DP> F;
+  if (!a.windowed) return {128 * B::NQ, 128 * B::NK, false, false};
+  const int dtype = sizeof(T) == 2 ? IGC_BF16 : IGC_F32;
+  const bool q = window_few(dtype, a.dim, (a.nq + a.batch - 1) / a.batch * a.group, a.batch, a.kv_heads);
+  const bool k = window_few(dtype, a.dim, (a.nk + a.batch - 1) / a.batch, a.batch, a.kv_heads);
+  return {q ? F::kRows : W::kRows, k ? F::kKeys : W::kKeys, q, k};
 }
 template <typename T>
-BwdRows bwd_rows_t(int dim, bool windowed) {
-  if (dim <= 32) return rows_of<T, 32>(windowed);
-  if (dim <= 64) return rows_of<T, 64>(windowed);
-  if (dim <= 96) return rows_of<T, 96>(windowed);
-  return rows_of<T, 128>(windowed);
+BwdTiles tiles_t(const AttnArgs& a) {
+  if (a.dim <= 32) return tiles_of<T, 32>(a);
+  if (a.dim <= 64) return tiles_of<T, 64>(a);
+  if (a.dim <= 96) return tiles_of<T, 96>(a);
+  return tiles_of<T, 128>(a);
 }
-BwdRows bwd_rows(int dtype, int dim, bool windowed) {
-  return dtype == IGC_BF16 ? bwd_rows_t<bf16_t>(dim, windowed) : bwd_rows_t<float>(dim, windowed);
-}
+BwdTiles bwd_tiles(int dtype, const AttnArgs& a) { return dtype == IGC_BF16 ? tiles_t<bf16_t>(a) : tiles_t<float>(a); }
 
 // Key tiles of `bm` that may hold sinks.
 int64_t far_tiles(const AttnArgs& a, bool by_key, int bm) {
   return a.win.sinks == 0 ? 0 : by_key ? a.nk / bm + a.batch : (int64_t)a.batch * ((a.win.sinks + bm - 1) / bm);
 }
 
+template <typename T, int DP, typename W>
+void win_dq(const AttnArgs& a, unsigned wgs, bool vec, hipStream_t s) {
+  constexpr int NT = 64 * W::QNW;
+  if (a.mask) {
+    if (vec) k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, true, 2, W::QNW, W::KS><<<wgs, NT, 0, s>>>(a);
+    else k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, false, 2, W::QNW, W::KS><<<wgs, NT, 0, s>>>(a);
+  } else {
+    if (vec) k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, true, 1, W::QNW, W::KS><<<wgs, NT, 0, s>>>(a);
+    else k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, false, 1, W::QNW, W::KS><<<wgs, NT, 0, s>>>(a);
+  }
+}
+template <typename T, int DP, typename W>
+void win_dkv(const AttnArgs& a, unsigned wgs, bool vec, hipStream_t s) {
+  if (vec) k_attn_dkv<T, DP, W::NK, W::KB, W::KWPE, true, 1, W::KNW, W::KS><<<wgs, 64 * W::KNW, 0, s>>>(a);
+  else k_attn_dkv<T, DP, W::NK, W::KB, W::KWPE, false, 1, W::KNW, W::KS><<<wgs, 64 * W::KNW, 0, s>>>(a);
+}
+
 template <typename T, int DP>
 void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
   typedef BwdShape<T, DP> S;
-  typedef WinShape<T, DP> W;
-  const BwdRows tile = rows_of<T, DP>(a.windowed);
+  const BwdTiles tile = tiles_of<T, DP>(a);
   const bool vec = a.qvec && a.kvec && a.ovec;
   a.delta = ws;
   ws += (a.nq * a.heads + 63) / 64 * 64;
@@ -633,15 +689,13 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     d.splits = a.dq ? p.dq_splits : 1;
     d.part_a = ws;
     const unsigned wgs = (unsigned)((a.nq * a.group / tile.q + a.batch) * a.kv_heads * d.splits);
-    if (a.windowed && a.mask) {
-      if (vec) k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, true, 2, W::QNW><<<wgs, 64 * W::QNW, 0, s>>>(d);
-      else k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, false, 2, W::QNW><<<wgs, 64 * W::QNW, 0, s>>>(d);
-    } else if (a.windowed) {
-      if (vec) k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, true, 1, W::QNW><<<wgs, 64 * W::QNW, 0, s>>>(d);
-      else k_attn_dq<T, DP, W::NQ, W::QB, W::QWPE, false, 1, W::QNW><<<wgs, 64 * W::QNW, 0, s>>>(d);
+    if (!a.windowed) {
+      if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true, 0, 4, 1><<<wgs, kNT, 0, s>>>(d);
+      else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false, 0, 4, 1><<<wgs, kNT, 0, s>>>(d);
+    } else if (tile.few_q) {
+      win_dq<T, DP, WinFewShape<T, DP>>(d, wgs, vec, s);
     } else {
-      if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true, 0, 4><<<wgs, kNT, 0, s>>>(d);
-      else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false, 0, 4><<<wgs, kNT, 0, s>>>(d);
+      win_dq<T, DP, WinShape<T, DP>>(d, wgs, vec, s);
     }
     if (a.dq && d.splits > 1)
       sum_go<T>(ws, nullptr, d.splits, a.qo, a.batch, a.nq, a.heads, a.dim, a.ovec, a.dq, nullptr, s);
@@ -656,11 +710,11 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
       a.far_parts = p.far_parts, a.far_by_key = p.far_by_key, a.far_rows = p.far_rows;
       a.far = a.delta + p.far_at;
       a.far_wgs = (unsigned)(far_tiles(a, p.far_by_key, tile.k) * a.kv_heads * a.far_parts);
-      if (vec) k_attn_dkv<T, DP, W::NK, W::KB, W::KWPE, true, 1, W::KNW><<<wgs + a.far_wgs, 64 * W::KNW, 0, s>>>(a);
-      else k_attn_dkv<T, DP, W::NK, W::KB, W::KWPE, false, 1, W::KNW><<<wgs + a.far_wgs, 64 * W::KNW, 0, s>>>(a);
+      if (tile.few_k) win_dkv<T, DP, WinFewShape<T, DP>>(a, wgs + a.far_wgs, vec, s);
+      else win_dkv<T, DP, WinShape<T, DP>>(a, wgs + a.far_wgs, vec, s);
     } else {
-      if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, 0, 4><<<wgs, kNT, 0, s>>>(a);
-      else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false, 0, 4><<<wgs, kNT, 0, s>>>(a);
+      if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);
+      else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);
     }
     if (a.splits > 1)
       sum_go<T>(a.part_a, a.part_b, a.splits, a.ko, a.batch, a.nk, a.kv_heads, a.dim, a.ovec, a.dk, a.dv, s);
@@ -681,8 +735,8 @@ void bwd_t(const AttnArgs& a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
 
 // Parts of the axis a kernel walks: enough to fill the GPU, each of at least `least` rows. The query axis goes down to
 // 64 rows: its partial results are small next to what a part reads.
-int parts(int64_t wgs, int64_t axis, int64_t least) {
-  const int64_t want = wgs >= 512 ? 1 : 512 / std::max<int64_t>(1, wgs);
+int parts(int64_t wgs, int64_t axis, int64_t least, int64_t fill = 512) {
+  const int64_t want = wgs >= fill ? 1 : fill / std::max<int64_t>(1, wgs);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 128), axis / least));
 }
 
@@ -692,15 +746,16 @@ AttnBwdPlan attn_bwd_plan(int dtype, const AttnArgs& a) {
   const int64_t nq = a.nq, nk = a.nk;
   const int batch = a.batch, heads = a.heads, kv_heads = a.kv_heads, dim = a.dim;
   AttnBwdPlan p;
-  const BwdRows t = bwd_rows(dtype, dim, a.windowed);
+  const BwdTiles t = bwd_tiles(dtype, a);
   const int64_t rows = (nq + batch - 1) / batch * (heads / kv_heads), keys = (nk + batch - 1) / batch;
   int64_t seen_keys = keys, seen_rows = rows;  // that a tile walks
+  const int64_t fill = a.windowed && dtype == IGC_F32 && dim > 32 ? 256 : 512;  // the former: one workgroup a CU
   if (a.windowed && a.win.left >= 0 && a.win.right >= 0) {
     seen_keys = std::min<int64_t>(keys, a.win.left + a.win.right + t.q / a.group + a.win.sinks);
     seen_rows = std::min<int64_t>(rows, (a.win.left + a.win.right + t.k) * a.group);
   }
-  p.dq_splits = parts(batch * ((rows + t.q - 1) / t.q) * kv_heads, seen_keys, a.windowed ? kWindowPart : 256);
-  p.dkv_splits = parts(batch * ((keys + t.k - 1) / t.k) * kv_heads, seen_rows, a.windowed ? kWindowPart : 64);
+  p.dq_splits = parts(batch * ((rows + t.q - 1) / t.q) * kv_heads, seen_keys, a.windowed ? kWindowPart : 256, fill);
+  p.dkv_splits = parts(batch * ((keys + t.k - 1) / t.k) * kv_heads, seen_rows, a.windowed ? kWindowPart : 64, fill);
   const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * nq * heads * dim : 0;
   const size_t dkv = p.dkv_splits > 1 ? (size_t)2 * p.dkv_splits * nk * kv_heads * dim : 0;
   // The two kernels run one after the other, so their partial results share the space.

@@ -384,6 +384,27 @@ constexpr int lds_bytes(int tile_values, int waves = 4) {
   return tile_values * 2 > out ? tile_values * 2 : out;
 }
 
+// A result tile in LDS, for another wave's lanes to take over: 16 N values a lane, then `more` of its own.
+template <int N>
+constexpr int handover_bytes(int more) {
+  return (16 * N + more) * 64 * 4;
+}
+template <int N>
+__device__ __forceinline__ void hand_over(float* s, const f32x16 (&c)[N]) {
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[(16 * t + r) * 64 + lane_id()] = c[t][r];
+}
+// c = f c + g (what was handed over).
+template <int N>
+__device__ __forceinline__ void take_over(const float* s, f32x16 (&c)[N], float f, float g) {
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) c[t][r] = fmaf(s[(16 * t + r) * 64 + lane_id()], g, c[t][r] * f);
+}
+
 // Stores a wave's result tile (32 rows in the lanes, DP / 32 register tiles of columns) scaled by f as rows of
 // `dim` values: row `row` of this lane, none if negative. Through LDS (32 (DP + 4) fp32 values of the wave's own),
 // since a lane's values lie 8 bytes at a time a row apart: 16-byte stores of whole rows instead. vec: dim is a

@@ -285,6 +285,14 @@ constexpr int32_t kAttnMaxDim = 128;
 // Keys, and query rows (queries times the heads that share a key head), of a problem at most: the kernels count those of a
 // sequence in 32 bits and step up to 256 past its end.
 constexpr int64_t kAttnMaxRows = INT32_MAX - 1023;
+// Whether window attention's tiles of 64 rows (or keys) are so few that all their workgroups run at a time anyway: two
+// waves then share each row's axis, for half the latency. Of wide heads only one workgroup fits a CU. us, without and with, windows of 255
+// before, 2 heads, n rows, forward / gradients: bf16, heads of 64, 300 11.4, 8.3 / 28.7, 22.1; 7,000 15.7, 11.3 / 39.4, 32.5;
+// 14,000 16.5, 13.9 / 45.9, 47.0; 28,000 (limits twice as high) 25.4, 31.0 / 84.9, 81.4; heads of 128, 2,000 17.1, 13.1 / 50.0, 39.6; 14,000
+// 21.1, 19.9 / 79.5, 86.3; fp32, heads of 40, 2,000 27.0, 17.9 / 73.2, 49.8; 14,000 31.6, 40.8 / 119, 128.
+inline bool window_few(int dtype, int dim, int64_t rows, int batch, int kv_heads) {
+  return batch * ((rows + 63) / 64) * kv_heads <= (dim > (dtype == IGC_F32 ? 32 : 64) ? 256 : 512);
+}
 // Keys, or query rows, of a part of a split axis at least, for window attention's tiles.
 constexpr int64_t kWindowPart = 384;
 // Parts the key axis is split into; where there is more than one, the forward workspace holds dim partial results and two
