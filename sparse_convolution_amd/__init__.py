@@ -1,5 +1,6 @@
 """MI355X-native IndexGrid build, neighbour map and submanifold sparse convolution, and the operators between
-convolutions: layer norm, 8-bit activation checkpoints and cross attention.
+convolutions: layer norm, 8-bit activation checkpoints, cross attention, and self-attention of voxels in grid order (windows
+with sinks, norm and rotation of queries and keys, dropout).
 
 Thin Python binding over libigconv (include/igconv.h): it checks tensor shapes, dtypes and
 devices, and passes raw device pointers and the current HIP stream to the C ABI. All device

@@ -142,11 +142,11 @@ def _weights(q_weight, k_weight, dim: int, dtype: torch.dtype, index: int) -> in
     return _dtype_code(dt)
 
 
-def _problem(q, k, positions, frequencies, eps, layout, amplitude, norm) -> tuple[bytes, tuple]:
+def _problem(q, k, positions, frequencies, eps, layout, amplitude, norm, name="q") -> tuple[bytes, tuple]:
     """The problem as an igc_qk_t, and the sizes its workspace depends on."""
     dt = q.dtype
     code, index = _dtype_code(dt), q.get_device()
-    _heads(q, "q", dt, index)
+    _heads(q, name, dt, index)
     n, heads, dim = q.shape
     kv_heads, ks = 0, (0, 0, 0)
     if k is not None:
@@ -218,7 +218,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     """The rotation of qk_norm_rotary alone: x [n, heads, dim] turned by its positions (igc_qk_norm_rotary without the norm)."""
     if positions is None or frequencies is None:
         raise ValueError("the rotation needs positions and frequencies")
-    p, _ = _problem(x, None, positions, frequencies, 0.0, layout, amplitude, False)
+    p, _ = _problem(x, None, positions, frequencies, 0.0, layout, amplitude, False, "x")
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _call("igc_qk_norm_rotary", x.get_device(), p, x.data_ptr(), None, None, None, _dtype_code(x.dtype), y.data_ptr(), None)
     return y
@@ -229,7 +229,7 @@ def rotary_backward(dy: torch.Tensor, positions: torch.Tensor, frequencies: torc
     """Gradient of rotary for the output gradient dy (contiguous): the rotation back, times amplitude."""
     if positions is None or frequencies is None:
         raise ValueError("the rotation needs positions and frequencies")
-    p, _ = _problem(dy, None, positions, frequencies, 0.0, layout, amplitude, False)
+    p, _ = _problem(dy, None, positions, frequencies, 0.0, layout, amplitude, False, "dy")
     _same(dy, "dy", dy.dtype, dy.shape, dy.get_device())
     dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
     _call("igc_qk_norm_rotary_backward", dy.get_device(), p, dy.data_ptr(), None, None, None, None, None, _dtype_code(dy.dtype),

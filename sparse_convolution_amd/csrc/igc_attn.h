@@ -1,4 +1,4 @@
-// Pieces shared by the cross-attention kernels: ragged tiles, matrix-core fragments and staging.
+// Pieces shared by the attention kernels: ragged tiles, windows, matrix-core fragments and staging.
 //
 // Fragments. All products run on 32x32 matrix instructions whose result puts one column in each
 // lane (lane % 32) and 16 rows in its registers: register r of lane half h = lane / 32 is row

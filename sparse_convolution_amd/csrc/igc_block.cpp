@@ -138,7 +138,7 @@ int window_args(const char* fn, const Window* w, AttnArgs& a) {
   if (a.kl && !a.windowed)  // whose workspace would be cross attention's
     return set_error(IGC_ERR_INVALID_ARG, f + ": d_kv_lengths need a limit to one side (left 2^31-1 leaves nothing out)");
   a.win = *w;
-  if (w->left < 0) a.win.sinks = 0;  // all keys before a query are visible anyway
+  if (w->left < 0 || w->left >= a.nk) a.win.sinks = 0;  // all keys before a query are visible anyway
   return IGC_OK;
 }
 

@@ -66,8 +66,10 @@ struct Head {
         mine[p] = make_float2(t.x * a.amplitude, t.y * a.amplitude);
       }
   }
-  // This lane's factors: y[c] = z[c] co[c] + z[partner of c] si[c].
-  static __device__ __forceinline__ void factors(const QkArgs& a, const float2* s_table, float (&co)[NV][V], float (&si)[NV][V]) {
+  // This lane's factors: y[c] = z[c] co[c] + z[partner of c] si[c]. A row behind the last has no table: what lies there instead may
+  // be NaN, which would enter the weights' gradients.
+  static __device__ __forceinline__ void factors(const QkArgs& a, bool live, const float2* s_table, float (&co)[NV][V],
+                                                 float (&si)[NV][V]) {
     const int pairs = a.axes * a.pairs;
     const float2* const mine = s_table + lane_id() / LPR * kPairs;
 #pragma unroll
@@ -76,7 +78,7 @@ struct Head {
       for (int i = 0; i < V; ++i) {
         const int ch = channel(j, i);
         co[j][i] = 1.f, si[j][i] = 0.f;
-        if (ch < 2 * pairs) {
+        if (live && ch < 2 * pairs) {
           const bool second = a.interleaved ? ch & 1 : ch >= pairs;
           const float2 t = mine[a.interleaved ? ch >> 1 : second ? ch - pairs : ch];
           co[j][i] = t.x;
@@ -200,7 +202,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(5))) void k
     wave_sync();  // the last row's table has been read
     H::fill(a, r, live, s_table[wave]);
     wave_sync();
-    H::factors(a, s_table[wave], co, si);
+    H::factors(a, live, s_table[wave], co, si);
     for (int h = h0; h < h1; h += kAhead) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -280,7 +282,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4))) void k
     wave_sync();
     H::fill(a, r, live, s_table[wave]);
     wave_sync();
-    H::factors(a, s_table[wave], co, si);
+    H::factors(a, live, s_table[wave], co, si);
     for (int h = h0; h < h1; h += kAheadBwd) {
 #pragma unroll
       for (int u = 0; u < kAheadBwd; ++u) {

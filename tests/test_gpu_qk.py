@@ -204,6 +204,20 @@ def test_eps_zero_and_a_ragged_last_tile():
     assert bool(torch.isfinite(dw).all())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_behind_the_last_do_not_meet_what_other_kernels_left(dtype):
+    # Tables full of NaN, left by a call with such frequencies on every CU, and then tiles whose last rows have no table.
+    igc = _igc()
+    say(f"qk stale tables {dtype}")
+    many, pos = torch.randn(200000, 1, 64, device="cuda").to(dtype), torch.ones(200000, dtype=torch.int32, device="cuda")
+    for n in (5, 4099):
+        q, k, p, freq, w, dy = case(n, 16, 4, 64, 3, 10, dtype)
+        igc.rotary(many, pos, torch.full((32,), float("nan"), device="cuda"))
+        grads = igc.qk_norm_rotary_backward(dy[0], dy[1], q, k, p, freq, w[0], w[1])
+        y = igc.qk_norm_rotary(q, k, p, freq, w[0], w[1])
+        assert all(bool(torch.isfinite(t).all()) for t in grads + y)
+
+
 def test_no_rows():
     igc = _igc()
     x = torch.empty(0, 2, 16, device="cuda")
