@@ -8,7 +8,7 @@
 // A row's cosines and sines are computed once for all of its heads: the LPR lanes of a row first make a table in LDS, then
 // keep what their channels need of it and walk the heads, V channels a load, with the loads of the next heads in flight.
 //
-// Memory bound, each array moved once (a copy of 4 GiB reaches 4.8 TB/s); the vector unit is busy for 60% of the time with bf16
+// Memory bound, each array moved once (a copy of 4 GiB reaches 4.8 TB/s); the vector unit is busy for 70% of the time with bf16
 // data. 1,000,003 rows of 4 + 4 heads of 64 by voxel coordinates, bf16: 393 us, 5.2 TB/s; gradients 602 us, 5.1 TB/s. Rotation alone of
 // 500,003 rows of 4 heads of 48, fp32: 144 us, 5.4 TB/s.
 #include <hip/hip_runtime.h>
