@@ -176,6 +176,32 @@ def test_long_sequences(n, left, right, sinks, dtype):
     check([n], [n], 2, 1, 64, dtype, left, right, sinks)
 
 
+# More than 512 tiles of 64 rows (and keys): the kernels in which no two waves share a row's axis.
+MANY = [510, 33, 700, 64, 0, 129, 1] * 12
+
+
+@TYPES
+@pytest.mark.parametrize("heads,kv_heads,dim", [(2, 2, 32), (4, 2, 64), (3, 3, 20), (2, 2, 40), (2, 2, 96), (4, 2, 128)])
+@pytest.mark.parametrize("left,right,sinks", [(60, 9, 2), (100, 0, 70), (None, 0, 0)])
+def test_many_tiles(heads, kv_heads, dim, left, right, sinks, dtype):
+    assert len(MANY) * -(-(sum(MANY) // len(MANY)) // 64) * kv_heads > 512
+    check(MANY, MANY, heads, kv_heads, dim, dtype, left, right, sinks)
+
+
+@TYPES
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+def test_many_tiles_masked_and_strided(dim, dtype):
+    check(MANY, MANY, 2, 2, dim, dtype, 60, 9, 5, masked=0.3)
+    check(MANY, MANY, 4, 2, dim, dtype, 40, 40, 3, packed="odd")
+
+
+@TYPES
+def test_many_tiles_of_new_rows_behind_caches(dtype):
+    # Chunks of queries over longer caches, more far parts than one.
+    lk = [n + 300 for n in MANY]
+    check(MANY, lk, 2, 2, 64, dtype, 200, 0, 9)
+
+
 @TYPES
 def test_many_sequences_with_sinks(dtype):
     # More rows of sinks than keys: the far parts go by the keys themselves. And far parts of ragged sequences.
