@@ -562,8 +562,10 @@ template <>
 struct WinFewShape<float, 96> : WinShape<float, 96> {};
 template <>
 struct WinFewShape<float, 128> : WinShape<float, 128> {};
+typedef Shape<1, 64, 2, 8, 2> WinMidShape;  // of fp32 heads of 64
 template <typename T>
-int win_rows(int dim, bool few) {
+int win_rows(int dim, int few) {
+  if (few == 2) return WinMidShape::kRows;
   auto rows = [&](auto s, auto f) { return few ? f.kRows : s.kRows; };
   return dim <= 32   ? rows(WinShape<T, 32>{}, WinFewShape<T, 32>{})
          : dim <= 64 ? rows(WinShape<T, 64>{}, WinFewShape<T, 64>{})
@@ -600,7 +602,7 @@ int fwd_rows(int dtype, int dim, int64_t nq, int batch, int group, int kv_heads,
       if (rows <= r) return r;
   }
   if (windowed) {
-    const bool few = window_few(dtype, dim, (nq + batch - 1) / batch * group, batch, kv_heads);
+    const int few = window_few(dtype, dim, (nq + batch - 1) / batch * group, batch, kv_heads);
     return dtype == IGC_BF16 ? win_rows<bf16_t>(dim, few) : win_rows<float>(dim, few);
   }
   return dtype == IGC_BF16 && dim <= 64 ? 256 : 128;
@@ -677,11 +679,14 @@ void fwd_go(const AttnArgs& a, unsigned wgs, hipStream_t s) {
   if (!a.windowed) {
     if (vec) k_attn_fwd<T, DP, F::NQ, F::BN, F::WPE, true, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);
     else k_attn_fwd<T, DP, F::NQ, F::BN, F::WPE, false, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);
-  } else if (window_few(sizeof(T) == 2 ? IGC_BF16 : IGC_F32, a.dim, (a.nq + a.batch - 1) / a.batch * a.group, a.batch, a.kv_heads)) {
-    win_go<T, DP, WinFewShape<T, DP>>(a, wgs, vec, s);
-  } else {
-    win_go<T, DP, WinShape<T, DP>>(a, wgs, vec, s);
+    return;
   }
+  const int few = window_few(sizeof(T) == 2 ? IGC_BF16 : IGC_F32, a.dim, (a.nq + a.batch - 1) / a.batch * a.group, a.batch, a.kv_heads);
+  if constexpr (sizeof(T) == 4 && DP == 64) {
+    if (few == 2) return win_go<T, DP, WinMidShape>(a, wgs, vec, s);
+  }
+  if (few) win_go<T, DP, WinFewShape<T, DP>>(a, wgs, vec, s);
+  else win_go<T, DP, WinShape<T, DP>>(a, wgs, vec, s);
 }
 
 template <typename T, int LPK, int R>

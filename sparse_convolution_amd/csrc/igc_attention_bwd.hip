@@ -633,20 +633,21 @@ template <>
 struct WinFewShape<float, 96> : WinShape<float, 96> {};
 template <>
 struct WinFewShape<float, 128> : WinShape<float, 128> {};
+typedef Shape<1, 2, 64, 8, 1, 2, 64, 8, 2> WinMidShape;  // of fp32 heads of 64
 struct BwdTiles {
-  int q, k;           // rows and keys of a workgroup's tile
-  bool few_q, few_k;  // of WinFewShape
+  int q, k;          // rows and keys of a workgroup's tile
+  int few_q, few_k;  // see window_few
 };
 template <typename T, int DP>
 BwdTiles tiles_of(const AttnArgs& a) {
   typedef BwdShape<T, DP> B;
   typedef WinShape<T, DP> W;
   typedef WinFewShape<T, DP> F;
-  if (!a.windowed) return {128 * B::NQ, 128 * B::NK, false, false};
+  if (!a.windowed) return {128 * B::NQ, 128 * B::NK, 0, 0};
   const int dtype = sizeof(T) == 2 ? IGC_BF16 : IGC_F32;
-  const bool q = window_few(dtype, a.dim, (a.nq + a.batch - 1) / a.batch * a.group, a.batch, a.kv_heads);
-  const bool k = window_few(dtype, a.dim, (a.nk + a.batch - 1) / a.batch, a.batch, a.kv_heads);
-  return {q ? F::kRows : W::kRows, k ? F::kKeys : W::kKeys, q, k};
+  const int q = window_few(dtype, a.dim, (a.nq + a.batch - 1) / a.batch * a.group, a.batch, a.kv_heads);
+  const int k = window_few(dtype, a.dim, (a.nk + a.batch - 1) / a.batch, a.batch, a.kv_heads);
+  return {q == 2 ? WinMidShape::kRows : q ? F::kRows : W::kRows, k == 2 ? WinMidShape::kKeys : k ? F::kKeys : W::kKeys, q, k};
 }
 template <typename T>
 BwdTiles tiles_t(const AttnArgs& a) {
@@ -662,6 +663,15 @@ int64_t far_tiles(const AttnArgs& a, bool by_key, int bm) {
   return a.win.sinks == 0 ? 0 : by_key ? a.nk / bm + a.batch : (int64_t)a.batch * ((a.win.sinks + bm - 1) / bm);
 }
 
+// f(shape) with the shape of window attention that window_few chose.
+template <typename T, int DP, typename F>
+void with_win_shape(int few, F f) {
+  if constexpr (sizeof(T) == 4 && DP == 64) {
+    if (few == 2) return f(WinMidShape{});
+  }
+  if (few) f(WinFewShape<T, DP>{});
+  else f(WinShape<T, DP>{});
+}
 template <typename T, int DP, typename W>
 void win_dq(const AttnArgs& a, unsigned wgs, bool vec, hipStream_t s) {
   constexpr int NT = 64 * W::QNW;
@@ -694,10 +704,8 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     if (!a.windowed) {
       if (vec) k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, true, 0, 4, 1><<<wgs, kNT, 0, s>>>(d);
       else k_attn_dq<T, DP, S::NQ, S::QB, S::QWPE, false, 0, 4, 1><<<wgs, kNT, 0, s>>>(d);
-    } else if (tile.few_q) {
-      win_dq<T, DP, WinFewShape<T, DP>>(d, wgs, vec, s);
     } else {
-      win_dq<T, DP, WinShape<T, DP>>(d, wgs, vec, s);
+      with_win_shape<T, DP>(tile.few_q, [&](auto w) { win_dq<T, DP, decltype(w)>(d, wgs, vec, s); });
     }
     if (a.dq && d.splits > 1)
       sum_go<T>(ws, nullptr, d.splits, a.qo, a.batch, a.nq, a.heads, a.dim, a.ovec, a.dq, nullptr, s);
@@ -712,8 +720,7 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
       a.far_parts = p.far_parts, a.far_by_key = p.far_by_key, a.far_rows = p.far_rows;
       a.far = a.delta + p.far_at;
       a.far_wgs = (unsigned)(far_tiles(a, p.far_by_key, tile.k) * a.kv_heads * a.far_parts);
-      if (tile.few_k) win_dkv<T, DP, WinFewShape<T, DP>>(a, wgs + a.far_wgs, vec, s);
-      else win_dkv<T, DP, WinShape<T, DP>>(a, wgs + a.far_wgs, vec, s);
+      with_win_shape<T, DP>(tile.few_k, [&](auto w) { win_dkv<T, DP, decltype(w)>(a, wgs + a.far_wgs, vec, s); });
     } else {
       if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);
       else k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, false, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);

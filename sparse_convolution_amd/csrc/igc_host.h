@@ -290,8 +290,12 @@ constexpr int64_t kAttnMaxRows = INT32_MAX - 1023;
 // before, 2 heads, n rows, forward / gradients: bf16, heads of 64, 300 11.4, 8.3 / 28.7, 22.1; 7,000 15.7, 11.3 / 39.4, 32.5;
 // 14,000 16.5, 13.9 / 45.9, 47.0; 28,000 (limits twice as high) 25.4, 31.0 / 84.9, 81.4; heads of 128, 2,000 17.1, 13.1 / 50.0, 39.6; 14,000
 // 21.1, 19.9 / 79.5, 86.3; fp32, heads of 40, 2,000 27.0, 17.9 / 73.2, 49.8; 14,000 31.6, 40.8 / 119, 128.
-inline bool window_few(int dtype, int dim, int64_t rows, int batch, int kv_heads) {
-  return batch * ((rows + 63) / 64) * kv_heads <= (dim > (dtype == IGC_F32 ? 32 : 64) ? 256 : 512);
+// 2: fp32 heads of 33 to 64 channels, whose tiles leave room for one workgroup a CU: between 256 and 512 tiles a workgroup of
+// eight waves takes two (9,001 rows of 2 sequences, heads of 40, gradients 85.6 and 75.2; up to 256 tiles it is slower, 2,000 rows 49.8 and 61.5).
+inline int window_few(int dtype, int dim, int64_t rows, int batch, int kv_heads) {
+  const int64_t tiles = batch * ((rows + 63) / 64) * kv_heads;
+  if (dtype == IGC_F32 && dim > 32 && dim <= 64 && tiles > 256 && tiles <= 512) return 2;
+  return tiles <= (dim > (dtype == IGC_F32 ? 32 : 64) ? 256 : 512);
 }
 // Keys, or query rows, of a part of a split axis at least, for window attention's tiles.
 constexpr int64_t kWindowPart = 384;

@@ -195,6 +195,16 @@ def test_many_tiles_masked_and_strided(dim, dtype):
     check(MANY, MANY, 4, 2, dim, dtype, 40, 40, 3, packed="odd")
 
 
+@pytest.mark.parametrize("dim", [40, 64])
+@pytest.mark.parametrize("left,right,sinks", [(60, 9, 2), (100, 0, 70)])
+def test_between_256_and_512_tiles(dim, left, right, sinks):
+    # fp32 heads of 33 to 64 channels have a form of eight waves there.
+    lengths = [510, 33, 700, 64, 0, 129, 1] * 6
+    assert 256 < len(lengths) * -(-(sum(lengths) // len(lengths)) // 64) * 2 <= 512
+    check(lengths, lengths, 2, 2, dim, F32, left, right, sinks)
+    check(lengths, lengths, 4, 2, dim, F32, left, right, sinks, masked=0.3, packed="odd")
+
+
 @TYPES
 def test_many_tiles_of_new_rows_behind_caches(dtype):
     # Chunks of queries over longer caches, more far parts than one.
