@@ -436,6 +436,24 @@ def test_other_stream_repeat_and_graph_are_bit_identical(lq, lk, left, sinks):
             assert torch.equal(a, b), n
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 40), (4, 4, 64), (2, 1, 96), (1, 1, 100), (3, 1, 128)])
+def test_repeats_between_other_kernels_are_bit_identical(heads, kv_heads, dim, masked, dtype):
+    """What other kernels leave in registers and shared memory is in no result: cross attention runs between the calls."""
+    igc = _igc()
+    (q, k, v, do), (qo, ko), m = _case([150, 201], [150, 201], heads, kv_heads, dim, dtype, masked=masked)
+    win = 60, 9, 2
+    first = None
+    for _ in range(20):
+        igc.cross_attention(q, k, v, qo, ko)
+        out, lse = igc.window_attention(q, k, v, *win, qo, ko, m)
+        got = [out, lse, *igc.window_attention_backward(do, q, k, v, out, lse, *win, qo, ko, m)]
+        first = first or got
+        for name, a, b in zip(("out", "lse", "dq", "dk", "dv"), got, first):
+            assert torch.equal(a, b), name
+
+
 @pytest.mark.parametrize("rows", [1, 300])
 def test_caches_past_2_to_the_31_elements(rows):
     # The cache's end, and with it the window, lies beyond element 2^31 of k and v (4.4 GB each), its sinks at the start:
