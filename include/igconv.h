@@ -395,7 +395,8 @@ int igc_cross_attention_backward(const igc_attention_t* problem, const void* d_q
  * and the mask keeps it. left, right -1: no limit to that side (left 0, right 0: itself). d_kv_lengths (int32 [batch] on the
  * device, may be NULL): only the first of a sequence's key rows are in use, lk of them (caches with room; clamped to the rows; the
  * others may hold anything), in the forward call alone and with a limit to one side (left 2^31 - 1 leaves nothing out). All else is as for
- * igc_cross_attention: problem, results (no visible key: 0 and -infinity), precision, workspaces. k and v of keys that the mask keeps must be
+ * igc_cross_attention: problem, results (no visible key: 0 and -infinity), precision (but with bf16 data and a limit to a side the
+ * probabilities enter their products as two bf16 parts, 16 bits, in both passes), workspaces. k and v of keys that the mask keeps must be
  * finite, or rows beyond their windows may become NaN too. */
 int igc_window_attention_workspace(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks,
                                    int32_t backward, size_t* bytes);

@@ -229,15 +229,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
         // bf16 data: p rounded once, since the matrix cores take bf16. out is then off by 1.26 to 1.39 times what its own
         // rounding costs (30 to 1,500 keys, heads of 64, rms against 64 bits). In two parts it is off by 1.00, but a second
         // product and the remainders cost 30 to 33% (215,003 x 5 x ~1024, 4 heads of 64: 291 and 382 us; 60,000 x 1,500, 256
-        // channels, heads of 32, 64 and 128: 167 and 222, 125 and 165, 118 and 154).
-        frag p[NQ];
+        // channels, heads of 32, 64 and 128: 167 and 222, 125 and 165, 118 and 154). With windows, whose
+        // rows end in few roundings besides, p has two parts: out is off by 1.00 (rounded once 1.20 to 1.41), for 7 to 22% (us,
+        // once and in two parts: 200,003 rows, 256 to either side, 4 heads of 64, 225 and 273; 100,003 rows, 64 to either side, 4
+        // heads of 128, 126 and 138; 30,001 rows, 1,023 before, 8 heads of 32, 84 and 100).
+        constexpr bool kTwo = WIN != 0 && sizeof(T) == 2;
+        frag p[NQ], lo[NQ];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) p[n] = to_frag<T>(s[n][t], mm);
+        for (int n = 0; n < NQ; ++n) {
+          if constexpr (kTwo) to_frag2<T>(s[n][t], mm, p[n], lo[n]);
+          else p[n] = to_frag<T>(s[n][t], mm);
+        }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const frag fv = load_tr<T, LD, PS>(s_v(buf), (t0 + t) * 32 + mm * 16, d * 32);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) o[n][d] = mma(fv, p[n], o[n][d]);
+          for (int n = 0; n < NQ; ++n) {
+            if constexpr (kTwo) o[n][d] = mma(fv, lo[n], o[n][d]);
+            o[n][d] = mma(fv, p[n], o[n][d]);
+          }
         }
       }
   };

@@ -425,14 +425,18 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
       }
 #pragma unroll
       for (int mm = 0; mm < 2; ++mm) {
-        frag fp[NK], fs[NK], lo[NK];
+        constexpr bool kTwo = WIN != 0 && sizeof(T) == 2;
+        frag fp[NK], fs[NK], lo[NK], lp[NK];
 #pragma unroll
         for (int n = 0; n < NK; ++n) {
-          // bf16 data: rounded once, as in the forward pass. dv is off by 1.38 to 1.45 times its own rounding; in two parts by
-          // 1.00, for 5 to 10% of the backward pass (60,000 x 1,500, heads of 32, 64 and 128: 543 and 599 us, 450 and 490, 471
-          // and 496). p is positive, so the error is at most 2^-8 of the sum of p |dout| (in out 2^-8 of the sum of p |v|);
-          // that of ds can be far more than its sum.
-          fp[n] = to_frag<T>(s[n], mm);
+          // bf16 data: p as in the forward pass, without windows rounded once. dv is then off by 1.38 to 1.45 times its own
+          // rounding; in two parts by 1.00, for 5 to 10% of the backward pass (60,000 x 1,500, heads of 32, 64 and 128: 543 and
+          // 599 us, 450 and 490, 471 and 496). p is positive, so the error is at most 2^-8 of the sum of p |dout| (in out 2^-8 of
+          // the sum of p |v|); that of ds can be far more than its sum. With windows two parts: dv is off by 1.00 (rounded once
+          // 1.38 to 1.44) for 2 to 8% of the backward pass (100,003 rows, 256 to either side, 4 heads of 64 and 128: 429 and 449
+          // us, 861 and 894; 512 to either side, masked, 4 heads on 2 of 64: 650 and 703).
+          if constexpr (kTwo) to_frag2<T>(s[n], mm, fp[n], lp[n]);
+          else fp[n] = to_frag<T>(s[n], mm);
           to_frag2<T>(dp[n], mm, fs[n], lo[n]);
         }
 #pragma unroll
@@ -441,6 +445,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
           const frag gq = load_tr<T, LD, PS>(s_q(buf), t * 32 + mm * 16, d * 32);
 #pragma unroll
           for (int n = 0; n < NK; ++n) {
+            if constexpr (kTwo) dv[n][d] = mma(go, lp[n], dv[n][d]);
             dv[n][d] = mma(go, fp[n], dv[n][d]);
             if constexpr (sizeof(T) == 2) dk[n][d] = mma(gq, lo[n], dk[n][d]);
             dk[n][d] = mma(gq, fs[n], dk[n][d]);
