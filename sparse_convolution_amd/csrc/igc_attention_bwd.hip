@@ -642,17 +642,19 @@ typedef Shape<1, 2, 64, 8, 1, 2, 64, 8, 2> WinMidShape;  // of fp32 heads of 64
 struct BwdTiles {
   int q, k;          // rows and keys of a workgroup's tile
   int few_q, few_k;  // see window_few
+  int k_threads;     // of a workgroup of keys
 };
 template <typename T, int DP>
 BwdTiles tiles_of(const AttnArgs& a) {
   typedef BwdShape<T, DP> B;
   typedef WinShape<T, DP> W;
   typedef WinFewShape<T, DP> F;
-  if (!a.windowed) return {128 * B::NQ, 128 * B::NK, 0, 0};
+  if (!a.windowed) return {128 * B::NQ, 128 * B::NK, 0, 0, kNT};
   const int dtype = sizeof(T) == 2 ? IGC_BF16 : IGC_F32;
   const int q = window_few(dtype, a.dim, (a.nq + a.batch - 1) / a.batch * a.group, a.batch, a.kv_heads);
   const int k = window_few(dtype, a.dim, (a.nk + a.batch - 1) / a.batch, a.batch, a.kv_heads);
-  return {q == 2 ? WinMidShape::kRows : q ? F::kRows : W::kRows, k == 2 ? WinMidShape::kKeys : k ? F::kKeys : W::kKeys, q, k};
+  return {q == 2 ? WinMidShape::kRows : q ? F::kRows : W::kRows, k == 2 ? WinMidShape::kKeys : k ? F::kKeys : W::kKeys, q, k,
+          64 * (k == 2 ? WinMidShape::KNW : k ? F::KNW : W::KNW)};
 }
 template <typename T>
 BwdTiles tiles_t(const AttnArgs& a) {
@@ -666,6 +668,12 @@ BwdTiles bwd_tiles(int dtype, const AttnArgs& a) { return dtype == IGC_BF16 ? ti
 // Key tiles of `bm` that may hold sinks.
 int64_t far_tiles(const AttnArgs& a, bool by_key, int bm) {
   return a.win.sinks == 0 ? 0 : by_key ? a.nk / bm + a.batch : (int64_t)a.batch * ((a.win.sinks + bm - 1) / bm);
+}
+
+// Workgroups of the launch for dk and dv: those of the key tiles, and before them those of the sinks' far rows.
+int64_t dkv_wgs(const AttnArgs& a, const AttnBwdPlan& p, int bm) { return (a.nk / bm + a.batch) * a.kv_heads * p.dkv_splits; }
+int64_t far_wgs(const AttnArgs& a, const AttnBwdPlan& p, int bm) {
+  return p.far_rows > 0 ? far_tiles(a, p.far_by_key, bm) * a.kv_heads * p.far_parts : 0;
 }
 
 // f(shape) with the shape of window attention that window_few chose.
@@ -720,11 +728,11 @@ void bwd_go(AttnArgs a, const AttnBwdPlan& p, float* ws, hipStream_t s) {
     a.splits = p.dkv_splits;
     a.part_a = ws;
     a.part_b = ws + (p.dkv_splits > 1 ? p.dkv_splits * n : 0);
-    const unsigned wgs = (unsigned)((a.nk / tile.k + a.batch) * a.kv_heads * a.splits);
+    const unsigned wgs = (unsigned)dkv_wgs(a, p, tile.k);
     if (a.windowed) {
       a.far_parts = p.far_parts, a.far_by_key = p.far_by_key, a.far_rows = p.far_rows;
       a.far = a.delta + p.far_at;
-      a.far_wgs = (unsigned)(far_tiles(a, p.far_by_key, tile.k) * a.kv_heads * a.far_parts);
+      a.far_wgs = (unsigned)far_wgs(a, p, tile.k);
       with_win_shape<T, DP>(tile.few_k, [&](auto w) { win_dkv<T, DP, decltype(w)>(a, wgs + a.far_wgs, vec, s); });
     } else {
       if (vec) k_attn_dkv<T, DP, S::NK, S::KB, S::KWPE, true, 0, 4, 1><<<wgs, kNT, 0, s>>>(a);
@@ -783,6 +791,7 @@ AttnBwdPlan attn_bwd_plan(int dtype, const AttnArgs& a) {
     p.far_at = (p.floats + 3) / 4 * 4;
     p.floats = p.far_at + (size_t)2 * (1 + p.far_parts) * p.far_rows * kv_heads * dim;
   }
+  p.dkv_threads = (dkv_wgs(a, p, t.k) + far_wgs(a, p, t.k)) * t.k_threads;
   return p;
 }
 

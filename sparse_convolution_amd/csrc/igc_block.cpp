@@ -200,6 +200,8 @@ int attention_backward(const char* fn, const igc_attention_t* p, const Window* w
   attention_alignment(p, a, (const void*)((uintptr_t)d_out | (uintptr_t)d_dout | (uintptr_t)d_dq | (uintptr_t)d_dk |
                                           (uintptr_t)d_dv));
   const AttnBwdPlan plan = attn_bwd_plan(p->dtype, a);
+  if (d_dk && plan.dkv_threads > UINT32_MAX)
+    return set_error(IGC_ERR_RANGE, f + ": too many keys, key heads and sinks for one launch");
   if (const int bad = check_workspace(fn, w, d_ws, ws_bytes, plan.floats * sizeof(float))) return bad;
   return launch_attn_bwd(a, p->dtype, plan, d_ws, stream);
 }

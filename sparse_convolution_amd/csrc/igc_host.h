@@ -308,6 +308,7 @@ struct AttnBwdPlan {
   int far_parts = 0, far_by_key = 0;  // as in AttnArgs
   int64_t far_rows = 0;
   size_t floats = 0, far_at = 0;  // workspace, and where `far` starts in it
+  int64_t dkv_threads = 0;        // of the launch for dk and dv, which takes fewer than 2^32
 };
 AttnBwdPlan attn_bwd_plan(int dtype, const AttnArgs& a);
 int launch_attn_bwd(const AttnArgs& a, int dtype, const AttnBwdPlan& p, void* ws, hipStream_t s);
