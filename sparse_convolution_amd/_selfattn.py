@@ -242,32 +242,38 @@ def rotary_backward(dy: torch.Tensor, positions: torch.Tensor, frequencies: torc
     return dx
 
 
-def _dropout(x, p: float, seed: int, offset, residual):
+def _dropout(x, p: float, seed: int, offset, residual, counter):
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a tensor")
     code, index = _dtype_code(x.dtype), x.get_device()
     _same(x, "x", x.dtype, x.shape, index)
     if residual is not None:
         _same(residual, "residual", x.dtype, x.shape, index)
-    d_offset = None
     if isinstance(offset, torch.Tensor):
+        if counter is not None:
+            raise ValueError("with a counter the offset is a number")
         _same(offset, "offset", torch.int64, (1,), index)
-        d_offset, offset = offset.data_ptr(), 0
+        counter, offset = offset, 0
+    elif counter is not None:
+        _same(counter, "counter", torch.int64, (1,), index)
     if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
         raise ValueError("seed and offset must be 0 to 2^64 - 1")
     y = torch.empty_like(x)
-    _call("igc_dropout", index, x.data_ptr(), _ptr(residual), x.numel(), code, p, seed, offset, d_offset, y.data_ptr())
+    _call("igc_dropout", index, x.data_ptr(), _ptr(residual), x.numel(), code, p, seed, offset, _ptr(counter), y.data_ptr())
     return y
 
 
-def dropout(x: torch.Tensor, p: float, seed: int, offset: int | torch.Tensor = 0, residual: torch.Tensor | None = None):
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int | torch.Tensor = 0, residual: torch.Tensor | None = None,
+            counter: torch.Tensor | None = None):
     """x (any shape, contiguous) with each element dropped with probability p (a multiple of 2^-16 is taken) and the others scaled so that
     the expected value stays, plus residual. What is dropped depends on (p, seed, offset) and the element's index alone: no
-    mask is kept, and dropout_backward computes it again. Give every call of a step an offset of its own; offset may be an int64
-    tensor of one element on the device, so that a captured graph can count its steps (igc_dropout)."""
-    return _dropout(x, p, seed, offset, residual)
+    mask is kept, and dropout_backward computes it again. Give every call of a step an offset of its own. counter, an int64
+    tensor of one element on the device, is added to the offset (modulo 2^64), so that a captured graph can count its steps; calls that
+    share a counter take offsets further apart than it counts, for example layer << 32. An offset that is such a tensor itself is a
+    counter on the offset 0 (igc_dropout)."""
+    return _dropout(x, p, seed, offset, residual, counter)
 
 
-def dropout_backward(dy: torch.Tensor, p: float, seed: int, offset: int | torch.Tensor = 0):
-    """Gradient of dropout with the same p, seed and offset for the output gradient dy; residual's is dy itself."""
-    return _dropout(dy, p, seed, offset, None)
+def dropout_backward(dy: torch.Tensor, p: float, seed: int, offset: int | torch.Tensor = 0, counter: torch.Tensor | None = None):
+    """Gradient of dropout with the same p, seed, offset and counter for the output gradient dy; residual's is dy itself."""
+    return _dropout(dy, p, seed, offset, None, counter)
