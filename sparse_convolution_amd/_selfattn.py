@@ -93,7 +93,7 @@ def rotary_frequencies(dim: int, base: float = 10000.0, axes: int = 1, scaling: 
     """Frequencies float32 [axes, pairs] (on the host) for rotating `dim` channels of a head, pairs = dim // 2 // axes
     on each of 1 to 3 position axes: base ** (-i / pairs). For positions up to `factor` times those trained on:
     scaling="linear" divides all by factor; "base" raises the base so that the slowest frequency is divided by factor and the
-    fastest stays; "parts" divides those that make fewer than `low` turns over the `original` length, keeps
+    fastest stays (at least two pairs); "parts" divides those that make fewer than `low` turns over the `original` length, keeps
     those that make more than `high`, and blends in between."""
     if not 1 <= axes <= 3 or dim < 2 * axes:
         raise ValueError("axes must be 1 to 3, and dim at least 2 a axis")
@@ -101,7 +101,9 @@ def rotary_frequencies(dim: int, base: float = 10000.0, axes: int = 1, scaling: 
         raise ValueError("base and factor must be positive and finite")
     pairs = dim // 2 // axes
     i = torch.arange(pairs, dtype=torch.float64)
-    if scaling == "base" and pairs > 1:
+    if scaling == "base" and factor != 1:
+        if pairs < 2:
+            raise ValueError("scaling by the base needs at least two pairs: one is the fastest and the slowest")
         base = base * factor ** (pairs / (pairs - 1))
     f = base ** (-i / pairs)
     if scaling == "linear":
