@@ -290,12 +290,19 @@ constexpr int64_t kAttnMaxRows = INT32_MAX - 1023;
 // before, 2 heads, n rows, forward / gradients: bf16, heads of 64, 300 11.4, 8.3 / 28.7, 22.1; 7,000 15.7, 11.3 / 39.4, 32.5;
 // 14,000 16.5, 13.9 / 45.9, 47.0; 28,000 (limits twice as high) 25.4, 31.0 / 84.9, 81.4; heads of 128, 2,000 17.1, 13.1 / 50.0, 39.6; 14,000
 // 21.1, 19.9 / 79.5, 86.3; fp32, heads of 40, 2,000 27.0, 17.9 / 73.2, 49.8; 14,000 31.6, 40.8 / 119, 128.
-// 2: fp32 heads of 33 to 64 channels, whose tiles leave room for one workgroup a CU: between 256 and 512 tiles a workgroup of
-// eight waves takes two (9,001 rows of 2 sequences, heads of 40, gradients 85.6 and 75.2; up to 256 tiles it is slower, 2,000 rows 49.8 and 61.5).
+// Counted are the launch's workgroups (one more than its rows fill for each sequence, see find_tile), not tiles: those without
+// rows hold a CU on their way out too, and come in a rhythm that leaves some XCDs without work. Sequences of 64 rows, 2 heads, gradients, with
+// and without: 241 of bf16 heads of 64 39 and 24, 113 of fp32 heads of 64 52 and 33. What this gives away: 120 of 128 rows, bf16 heads
+// of 64, 27 and 33.
+// 2: fp32 heads of 33 to 64 channels, where one workgroup fits a CU: eight waves take two tiles where one a workgroup are too many.
+// 1 / 2 / 0, 255 before, 2 heads of 40, forward and gradients: 9,001 rows of 2 sequences 40 / 26 / 31 and 104 / 76 / 83; 14,000 rows 41 /
+// 26 / 32 and 132 / 105 / 123; 16,200 rows of 2 sequences (256 workgroups) 43 / 27 / 32 and 133 / 107 / 125. Above 256 workgroups, heads of 64: 200
+// sequences of 64 rows 36 / 21 / 15 and 116 / 78 / 63, 96 of 100 rows 2: 24 and 74, 0: 18 and 65; given away: 48 of 256 rows 2: 19 and
+// 61, 0: 22 and 65.
 inline int window_few(int dtype, int dim, int64_t rows, int batch, int kv_heads) {
-  const int64_t tiles = batch * ((rows + 63) / 64) * kv_heads;
-  if (dtype == IGC_F32 && dim > 32 && dim <= 64 && tiles > 256 && tiles <= 512) return 2;
-  return tiles <= (dim > (dtype == IGC_F32 ? 32 : 64) ? 256 : 512);
+  auto wgs = [&](int bm) { return (rows * batch / bm + batch) * kv_heads; };
+  if (wgs(64) <= (dim > (dtype == IGC_F32 ? 32 : 64) ? 256 : 512)) return 1;
+  return dtype == IGC_F32 && dim > 32 && dim <= 64 && wgs(128) <= 256 ? 2 : 0;
 }
 // Keys, or query rows, of a part of a split axis at least, for window attention's tiles.
 constexpr int64_t kWindowPart = 384;
