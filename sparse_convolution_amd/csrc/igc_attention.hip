@@ -320,7 +320,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
 template <typename T, int LPK, int R, bool VEC, bool WIN>
 __global__ __launch_bounds__(kNT) void k_attn_few(AttnArgs a) {
   typedef typename Raw8<T>::type frag;
-  constexpr int U = 4, KPW = 64 / LPK, STEP = 4 * KPW * U;  // keys of a wave's round: KPW * U
+  constexpr int U = 4, KPW = 64 / LPK, STEP = 4 * KPW * U;  // keys of a wave's round: KPW * U; STEP: see few_keys
   __shared__ float s_o[4][R][LPK * 8 + 2];
 
   const int lane = lane_id(), wave = threadIdx.x >> 6;
@@ -584,6 +584,8 @@ int win_rows(int dim, int few) {
 }
 
 constexpr int kFewRows = 4;
+// Keys that a workgroup of k_attn_few takes in a round.
+constexpr int few_keys(int dim) { return 1024 / (dim <= 32 ? 4 : dim <= 64 ? 8 : 16); }
 
 // Query rows of a tile: a few (k_attn_few) or those of the matrix kernel. Decided from the average number of rows
 // that share a key head in a sequence; either kernel takes any number of rows. The whole batch takes one form: a sequence of
@@ -755,9 +757,19 @@ int attn_fwd_splits(int dtype, const AttnArgs& a) {
   int64_t keys = nk / batch;  // that a tile walks
   if (a.windowed && a.win.left >= 0 && a.win.right >= 0)
     keys = std::min<int64_t>(keys, a.win.left + a.win.right + bm / a.group + a.win.sinks);
-  // Single tokens: a workgroup on every CU reads up to 2,048 keys each sooner than parts of them are joined. 64 queries, 8 heads on 4
-  // of 64, bf16, us whole / in parts for 2,048 workgroups: 1,028 keys 27 / 37, 3,005 keys 59 / 50.
-  if (a.windowed && bm <= kFewRows && wgs >= 256 && keys <= 2048) return 1;
+  // Single tokens: with a workgroup on every CU, few rounds of the key axis (few_keys) take less time than its parts and their
+  // join: up to 8, and 2 more for each row, which costs arithmetic of its own in every round and its part of the join. us whole / in parts for
+  // 2,048 workgroups, windows of as many rounds:
+  //                            6            10           14           23
+  //   256 workgroups, a row, bf16 heads of 64
+  //                            20 / 21      31 / 29      40 / 34      63 / 46
+  //   the same, fp32 heads of 32, 64 and 128, 12, 10 and 11 rounds: 64 / 53, 55 / 48, 54 / 49
+  //   256 workgroups, 4 rows, bf16 heads of 64
+  //                            32 / 42      47 / 62      60 / 74      92 / 85
+  //   384, 2 rows, bf16 heads of 64, 8 and 16: 39 / 41, 70 / 61; fp32 64 / 60, 119 / 97 (heads of 128 16: 110 / 94, 32: 215 / 164)
+  // Over 240 such problems of 256 to 900 workgroups this is 2.4% from the better of both on average (a limit of 2,048 keys 5.0%), and up to
+  // 30% with 250 sequences and 2 key heads, where the whole axis stays ahead for longer.
+  if (a.windowed && bm <= kFewRows && wgs >= 256 && keys <= (8 + 2 * bm) * few_keys(dim)) return 1;
   // Rows of windows are many, and so is what their parts leave to be joined. Parts of at least 256 / 384 / 1,024 keys, us: 9,001
   // rows of 2 sequences, 2 heads of 64, bf16, 511 keys before: 26 / 19 / 19; 4,000 rows, 1,999 before: 27 / 26 / 32.
   const int64_t least = a.windowed && bm > kFewRows ? kWindowPart : 256;
