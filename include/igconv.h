@@ -430,7 +430,7 @@ typedef struct {
 /* d_yq [n, heads, dim] and d_yk [n, kv_heads, dim] (dense, type `dtype`): for the pair (z1, z2) of angle t
  *     y1 = amplitude * (z1 cos t - z2 sin t), y2 = amplitude * (z2 cos t + z1 sin t),
  * and y = z elsewhere. d_qw and d_kw [dim] of type `wdtype` (IGC_F32 or `dtype`; NULL: ones). Sums and products are fp32, the
- * angle is reduced in 64 bits (far positions keep fp32 accuracy), the result is rounded once. Outputs must not alias inputs. */
+ * angle is reduced in 64 bits (far positions keep fp32 accuracy at frequencies up to 2^40), the result is rounded once. Outputs must not alias inputs. */
 int igc_qk_norm_rotary(const igc_qk_t* problem, const void* d_q, const void* d_k, const void* d_qw, const void* d_kw,
                        int32_t wdtype, void* d_yq, void* d_yk, igc_stream stream);
 

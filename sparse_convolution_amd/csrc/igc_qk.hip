@@ -26,21 +26,23 @@ namespace {
 constexpr int kNT = 256;
 
 // Cosine and sine of position * frequency. The product and its share of a turn are formed in 64 bits with the rounding
-// errors carried along, so that positions up to 2^31 keep an angle exact to fp32; the rest of an eighth of a turn to either
-// side goes through the Taylor series, whose first missing terms are below 2^-29.
+// errors carried along, whole turns leave before these are added (behind them they could be more than a turn themselves), so that
+// positions up to 2^31 keep an angle exact to fp32 for frequencies up to 2^40, and a bounded one beyond; the rest of an eighth of a
+// turn to either side goes through the Taylor series, whose first missing terms are below 2^-29.
 __device__ __forceinline__ float2 cos_sin(int32_t position, float frequency) {
+#pragma clang fp contract(off)  // t - rint(t) is of the rounded t: a fused one would hold what t_low adds
   constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591534e-18;  // 1 / (2 pi) in two parts
   const double a = position, f = frequency;
   const double p = a * f, p_low = fma(a, f, -p);
   const double t = p * kTurn, t_low = fma(p_low, kTurn, fma(p, kTurnLow, fma(p, kTurn, -t)));
-  const double quarter = rint(4.0 * t);
-  const float x = (float)((fma(quarter, -0.25, t) + t_low) * 6.283185307179586);
-  const int q = (int)(quarter - 4.0 * floor(0.25 * quarter));
+  const double u = (t - rint(t)) + t_low, quarter = rint(4.0 * u);
+  const float x = (float)(fma(quarter, -0.25, u) * 6.283185307179586);
+  const int q = (int)quarter & 3;
   const float x2 = x * x;
   const float s = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
   const float c = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
-  const float u = q & 1 ? s : c, v = q & 1 ? c : s;
-  return make_float2(q == 1 || q == 2 ? -u : u, q >= 2 ? -v : v);
+  const float co = q & 1 ? s : c, si = q & 1 ? c : s;
+  return make_float2(q == 1 || q == 2 ? -co : co, q >= 2 ? -si : si);
 }
 
 // What a lane holds of a head: NV times V channels. The LPR lanes of a row, and with them its table, lie in one wave.
