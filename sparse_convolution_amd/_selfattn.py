@@ -129,6 +129,8 @@ def _turn(positions, frequencies, n: int, layout: str, index: int) -> tuple[int,
     if not isinstance(frequencies, torch.Tensor) or frequencies.dim() not in (1, 2):
         raise ValueError("frequencies must have shape [pairs] or [axes, pairs]")
     axes, pairs = (1, frequencies.shape[0]) if frequencies.dim() == 1 else frequencies.shape
+    if axes < 1:
+        raise ValueError("frequencies must have at least one axis")
     _same(frequencies, "frequencies", torch.float32, frequencies.shape, index)
     flat = axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1
     _same(positions, "positions", torch.int32, (n,) if flat else (n, axes), index)

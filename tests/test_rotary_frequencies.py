@@ -21,3 +21,11 @@ def test_the_base_divides_the_slowest_and_leaves_the_fastest(dim, axes, factor):
     assert bool((g[:, 0] == 1).all())
     # Both are rounded to fp32 once: 2^-24 each, and powers in 64 bits.
     assert bool(((g[:, -1].double() * factor / f[:, -1].double() - 1).abs() < 2 * 2.0 ** -24 * (1 + 1e-6)).all())
+
+
+@pytest.mark.parametrize("shape", [(0, 5), (0, 0)])
+def test_frequencies_of_no_axis_are_refused(shape):
+    # They would leave every channel as it is.
+    from sparse_convolution_amd._selfattn import _turn
+    with pytest.raises(ValueError, match="at least one axis"):
+        _turn(torch.zeros(4, 0, dtype=torch.int32), torch.zeros(shape), 4, "half", 0)
