@@ -396,8 +396,9 @@ int igc_cross_attention_backward(const igc_attention_t* problem, const void* d_q
  * device, may be NULL): only the first of a sequence's key rows are in use, lk of them (caches with room; clamped to the rows; the
  * others may hold anything), in the forward call alone and with a limit to one side (left 2^31 - 1 leaves nothing out). All else is as for
  * igc_cross_attention: problem, results (no visible key: 0 and -infinity), precision (but with bf16 data and a limit to a side the
- * probabilities enter their products as two bf16 parts, 16 bits, in both passes), workspaces. k and v of keys that the mask keeps must be
- * finite, or rows beyond their windows may become NaN too. */
+ * probabilities enter their products as two bf16 parts, 16 bits, in both passes), workspaces. k and v of keys that the mask keeps, and
+ * for gradients q and d_dout of rows that see a key, must be finite, or rows and keys beyond their windows may become NaN too; masked
+ * keys and rows without keys may hold anything. */
 int igc_window_attention_workspace(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks,
                                    int32_t backward, size_t* bytes);
 int igc_window_attention(const igc_attention_t* problem, int32_t left, int32_t right, int32_t sinks,

@@ -49,7 +49,8 @@ def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: in
     key_mask keeps it. None: no limit to that side; right 0 is causal. With as many queries as keys this is attention within
     a sequence, with fewer that of its last rows to a cache (single tokens); kv_lengths (int32 [batch] on the device) says how many
     of a sequence's key rows are in use where a cache has room for more (its lk then; without gradients). k and v in use must be finite where
-    key_mask keeps them. Returns (out, lse) as cross_attention (igc_window_attention)."""
+    key_mask keeps them, and for gradients q and dout of rows that see a key; masked keys and rows without keys may hold anything.
+    Returns (out, lse) as cross_attention (igc_window_attention)."""
     window = _window(left, right, sinks)
     p, sizes = _attention_problem(q, k, v, q_offsets, kv_offsets, key_mask, scale)
     dev = q.device

@@ -142,6 +142,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   WindowWave wave_sees;
   if constexpr (WIN) wave_sees.start(see[0], see[NQ - 1]);
 
+  // WIN 2: a masked key's score has to be -infinity whatever the query is, but a bias added to NaN is NaN. Rows that are not
+  // finite are walked as zeros, and give NaN in the end if they saw a key.
+  bool not_finite[NQ] = {};
+  if constexpr (WIN == 2) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      f32x16 nan = zero16();
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) nan = mma(bf16x8v{}, fq[n][kk].p[0], nan);  // 0 times the row: 0 or NaN
+      not_finite[n] = nan[0] != 0.f;
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk)
+        if (not_finite[n]) fq[n][kk] = frag{};
+    }
+  }
+
   // Finite, so that the first reference (-infinity) is passed whatever the scale.
   const float c = a.scale * kLog2e, slack = fminf(kSlack / c, 3.4e38f);
   f32x16 o[NQ][DT];
@@ -296,7 +312,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   void* const s_out = s_mem + row_wave * (32 * (DP + 4) * 4);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const float total = l[n] + __shfl_xor(l[n], 32, 64);
+    float total = l[n] + __shfl_xor(l[n], 32, 64);
+    if (WIN == 2 && not_finite[n] && total > 0.f) total = NAN;
     if (a.splits > 1) {
       const int64_t first = (int64_t)split * a.nq * a.heads;
       store_tile<float, DP>(a.part_a + first * a.dim, s_out, o[n], 1.f, row[n], a.dim, a.dim % 4 == 0);

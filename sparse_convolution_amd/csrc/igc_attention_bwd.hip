@@ -117,20 +117,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
     const int64_t at = qi * a.heads + head;
     row[n] = r < rows ? at : -1;
     const T* p = (const T*)a.q + qi * a.qs[0] + head * a.qs[1];
+    const float row_lse = row[n] >= 0 ? a.lse_in[row[n]] : -INFINITY;
+    const bool blind = WIN == 2 && row_lse == -INFINITY;  // what a row without keys holds need not be finite
+    lse[n] = lse_base2(row_lse);
     delta[n] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
+      typedef typename Raw8<T>::type raw;
       const int d = kk * 16 + h * 8, have = r < rows ? a.dim - d : 0;
-      fq[n][kk] = to_parts(load8<T>(p + d, have, VEC));
-      const auto g = load8<T>((const T*)a.dout + at * a.dim + d, have, VEC);
-      const auto f = load8<T>((const T*)a.out_in + at * a.dim + d, have, VEC);
-      fo[n][kk] = to_parts(g);
+      const raw x = load8<T>(p + d, have, VEC);
+      const raw g = load8<T>((const T*)a.dout + at * a.dim + d, have, VEC);
+      const raw f = load8<T>((const T*)a.out_in + at * a.dim + d, have, VEC);
+      fq[n][kk] = to_parts(blind ? raw{} : x);
+      fo[n][kk] = to_parts(blind ? raw{} : g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) delta[n] = fmaf((float)g[i], (float)f[i], delta[n]);
     }
     delta[n] += __shfl_xor(delta[n], 32, 64);
+    if (blind) delta[n] = 0.f;
     if (row[n] >= 0 && h == 0 && split == 0 && share == 0) a.delta[row[n]] = delta[n];
-    lse[n] = lse_base2(row[n] >= 0 ? a.lse_in[row[n]] : -INFINITY);
   }
   WindowWave wave_sees;
   if constexpr (WIN) wave_sees.start(see[0], see[NQ - 1]);
@@ -299,19 +304,22 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
   const int n_rows = (int)(r1 - r0);
   Stage<T, BQ, DP, NT, VEC> sq, so;
   float n_lse = 0.f, n_delta = 0.f;  // as loaded: worked on a tile later (with ds rounded once 223 and 211 us)
+  // A mask may leave rows without keys among those that a tile of keys walks, and what such rows hold need not be finite: each
+  // wave then looks at the tile's lse and makes them zeros. (Windows alone leave none there.)
+  const bool masked = WIN && a.mask;
   auto fetch = [&](int t0) {
     sq.load(n_rows - t0);
     so.load(n_rows - t0);
-    if (threadIdx.x < BQ) {
+    if (lane < BQ && (wave == 0 || masked)) {
       n_lse = -INFINITY;
       n_delta = 0.f;
-      if (t0 + (int)threadIdx.x < n_rows) {
+      if (t0 + lane < n_rows) {
         int64_t qi;
         int g;
-        split_row(r0 + t0 + threadIdx.x, a.group, qi, g);
+        split_row(r0 + t0 + lane, a.group, qi, g);
         const int64_t at = (q0 + qi) * a.heads + kh * a.group + g;
         n_lse = a.lse_in[at];
-        n_delta = a.delta[at];
+        if (wave == 0) n_delta = a.delta[at];
       }
     }
   };
@@ -370,6 +378,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(WPE))) 
 
   int buf = 0;
   for (int t0 = 0; t0 < n_rows; t0 += BQ, buf ^= 1) {
+    if (masked) {
+      const uint64_t seeing = __ballot(n_lse != -INFINITY);
+      if (seeing != ~0ull >> (64 - BQ)) sq.clear(seeing), so.clear(seeing);
+    }
     sq.template store<LD, PS>(s_q(buf));
     so.template store<LD, PS>(s_o(buf));
     if (threadIdx.x < BQ) s_lse[buf][threadIdx.x] = lse_base2(n_lse), s_delta[buf][threadIdx.x] = -n_delta;

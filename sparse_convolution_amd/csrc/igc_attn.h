@@ -312,6 +312,12 @@ struct Stage {
         put<LD, PS>(s, i, x);
       }
   }
+  // Zeroes the rows whose bit in `keep` is off.
+  __device__ __forceinline__ void clear(uint64_t keep) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(keep >> row(i) & 1)) r[i] = typename Raw8<T>::type{};
+  }
   template <int LD, int PS>
   __device__ __forceinline__ void store(bf16_t* s) const {
 #pragma unroll
