@@ -15,10 +15,11 @@
 // queries on 262,147 keys where half of the sequences have no query and one has 33: 39 us and 5 to join; the 81,157 keys
 // in use are 166 MB, 4.3 TB/s, and that one sequence's keys are read 33 times, once for each row (see fwd_rows).
 //
-// Windows: the same bound, with what narrow windows add: staging, prologue and edges are 40% of the vector instructions of a block of
-// 32 x 32 scores (146 of them; 85 without). 200,003 rows, 256 to either side and 8 sinks, 4 heads of 64 bf16: 207 to 234 us by the
-// GPU's clock, 456 to 515 TFLOP/s of visible pairs, vector unit busy 67%, matrix cores 26%, the last of 6.1 rounds of workgroups. 64 tokens
-// with 1,028 visible keys each, 8 heads on 4 of 64: 26 us, 2.6 TB/s: latency of a workgroup on every CU.
+// Windows: the same bound, with what narrow windows add: staging, prologue and edges, and the second part of p, are half of the vector
+// instructions of a block of 32 x 32 scores (174 of them, 28 for that part; 85 without windows). 200,003 rows, 256 to either side and 8 sinks, 4
+// heads of 64 bf16: 261 to 273 us by the GPU's clock, 391 to 409 TFLOP/s of visible pairs, vector unit busy 66%, matrix cores 33%, the last
+// of 6.1 rounds of workgroups. 64 tokens with 1,028 visible keys each, 8 heads on 4 of 64: 28 us, 2.4 TB/s: latency of a workgroup
+// on every CU.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -556,8 +557,8 @@ struct FwdShape<float, DP> {
   static constexpr int NQ = 1, BN = 32, WPE = DP <= 64 ? 2 : 1;
 };
 
-// Shapes of window attention: 32 NQ rows of a wave, keys of a tile, waves per SIMD, waves of a workgroup. Other than without
-// windows, where heads of 64 do best with two tiles of rows a wave and two waves per SIMD: a wave's rows see few keys each and
+// Shapes of window attention: 32 NQ rows of a wave, keys of a tile, waves per SIMD, waves of a workgroup (chosen with p rounded once, as the
+// figures are). Other than without windows, where heads of 64 do best with two tiles of rows a wave and two waves per SIMD: a wave's rows see few keys each and
 // more of them beside its own rows' windows, so one tile of rows and more waves do better. us, bf16, heads of 64, windows of 256
 // to either side over 200,003 rows / 64 over 200,003 / 2,047 before over 60,000, 4 heads: (1, 32, 4, 4) 207, 108, 186; (1, 64, 3,
 // 4) 228, 108, 196; (2, 64, 2, 4) 273, 149, 199; (2, 32, 2, 2) 240, 126, 207; (1, 32, 4, 2) 304, 138, 265. Heads of 32, 256 to

@@ -14,8 +14,9 @@
 // k_attn_dkv for both sides). Bound like the forward pass, by the vector unit beside the matrix cores: bf16, 100,003 queries,
 // 4 heads on 2 key heads of 64, three sequences of ~800 keys: 443 us in all (400 with ds rounded once for dk, on the same GPU);
 // under the profiler, whose clock is lower, dq 227 us, dk and dv 290, sums 7.
-// Windows: 100,003 rows, 512 to either side and 16 sinks, masked, 4 heads on 2 of 64: 605 to 615 us in all, 387 to 393 TFLOP/s of the
-// five products of visible pairs; under the profiler dq 325, dk and dv 385, sinks 6.
+// Windows (ten products, p in two parts for dv): 100,003 rows, 512 to either side and 16 sinks, masked, 4 heads on 2 of 64: 678 to
+// 731 us in all by the GPU's clock, 326 to 351 TFLOP/s of the five products of visible pairs; under the profiler, whose clock is lower, dq 318, dk
+// and dv 445, sinks 6.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -613,11 +614,14 @@ template <int DP>
 struct BwdShape<float, DP> {
   static constexpr int NQ = 1, QWPE = DP <= 64 ? 2 : 1, QB = 32, NK = 1, KWPE = DP <= 32 ? 2 : 1, KB = 32;
 };
-// Window attention: for dq rows, waves per SIMD, keys of a tile and waves of a workgroup, then the same for dk and dv. One tile of rows
+// Window attention: for dq rows, waves per SIMD, keys of a tile and waves of a workgroup, then the same for dk and dv (chosen with p rounded once for
+// dv, as the figures are). One tile of rows
 // and three waves per SIMD for dq, since the masks of two spill. us, dq (1, 3, 32, 4) / (2, 2, 32, 4) / (1, 2, 64, 4): 100,003 rows, 512
 // to either side, masked, 4 heads on 2 of 64: 605 / 672 / 622; 100,003 rows, 256 to either side, 4 heads: 388 / 491 / 387. Heads of 32
 // (200,003 rows, 8 heads, 256 to either side): 901, with the shapes without windows 996; of 96 (100,003 rows, 4 heads) 645 and 705.
 // fp32, heads of 32, two waves / four waves: 50,003 rows, 4 heads, 256 to either side 358 / 359, 7,131 rows, 2 heads, 64: 44 / 54.
+// Registers that the compiler spills: dk and dv of fp32 heads over 96 73 to 76 (6 without windows), of eight waves 19 to 22; dq of bf16 heads over
+// 96 at addresses that are no multiple of 16 bytes 33 to 66 (34 without windows).
 template <int Q, int QE, int QN, int QW, int K, int KE, int KN, int KW, int S = 1>
 struct Shape {
   static constexpr int NQ = Q, QWPE = QE, QB = QN, QNW = QW, NK = K, KWPE = KE, KB = KN, KNW = KW, KS = S;

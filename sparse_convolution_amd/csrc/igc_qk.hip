@@ -8,9 +8,9 @@
 // A row's cosines and sines are computed once for all of its heads: the LPR lanes of a row first make a table in LDS, then
 // keep what their channels need of it and walk the heads, V channels a load, with the loads of the next heads in flight.
 //
-// Memory bound, each array moved once (a copy of 4 GiB reaches 4.8 TB/s); the vector unit is busy for 70% of the time with bf16
-// data. 1,000,003 rows of 4 + 4 heads of 64 by voxel coordinates, bf16: 393 us, 5.2 TB/s; gradients 602 us, 5.1 TB/s. Rotation alone of
-// 500,003 rows of 4 heads of 48, fp32: 144 us, 5.4 TB/s.
+// Memory bound, each array moved once (a copy of 4 GiB reaches 4.8 TB/s); the vector unit is busy for 73% of the time with bf16
+// data. 1,000,003 rows of 4 + 4 heads of 64 by voxel coordinates, bf16: 391 us, 5.2 TB/s; gradients 598 us, 5.1 TB/s. Rotation alone of
+// 500,003 rows of 4 heads of 48, fp32: 150 us, 5.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -165,7 +165,7 @@ struct Head {
 
 // How many heads' loads are in flight; the registers that this takes are bounded by the waves per SIMD (k_qk five, k_qk_bwd
 // four). 1,000,003 rows of 4 + 4 heads of 64, bf16, us: forward 4 heads 393, 3 399, 2 with six waves 459, 1 435; without a bound 457;
-// backward 1 head 602, 2 609, 2 with three waves 663.
+// backward 1 head 602, 2 609, 2 with three waves 663. At five waves bf16 heads of 16 to 128 channels in steps of 8 spill two registers.
 constexpr int kAhead = 4, kAheadBwd = 1;
 
 // blockIdx.x: the rows, blockIdx.y: a share of the heads (those of the queries first).
